@@ -343,6 +343,112 @@ zeta_status_t zeta_attend_bwd(const zeta_problem_t *p, const float *q, const flo
                               cudaStream_t stream);
 
 /*
+ * Paged cache: serving a trained model.
+ *
+ * The calls above take whole sequences.  The three calls below hold the keys and
+ * values of many sequences in fixed-size pages and take, per call, a batch of up
+ * to n <= C new tokens per sequence (n = 1: one token each).  A prompt read in
+ * pieces and the tokens that follow it get the outputs that zeta_attend_fwd
+ * computes for the whole sequence: the same codes, prefixes, windows and weights.
+ *
+ *   p     B sequences in this call, H, d_K, d_V, k, C, bits, v_dtype, flags as
+ *         everywhere; N is the longest sequence the cache holds (C | N).
+ *   cc    n: rows of new tokens per sequence in q, k, v, out (1 <= n <= C);
+ *         page: tokens per page, a power of two up to 65536;
+ *         pages, order_pages: pages in the pools; table_len: row length of the
+ *         page tables, table_len * page >= N.
+ *   start, count   int32 [B] (device): tokens sequence b held before this call
+ *         and tokens it brings (0 <= count <= n, start + count <= N).  Rows
+ *         count[b] .. n-1 are padding: never read, and left as they were where
+ *         they are outputs.  A sequence outside these ranges is skipped whole and
+ *         ZETA_ERR_BOUNDS recorded.
+ *   page_table     int32 [B, table_len]: token t of sequence b is row t % page of
+ *         page page_table[b][t / page].  Only entries of tokens that exist are
+ *         read; one outside [0, pages) skips its tokens (ZETA_ERR_BOUNDS).
+ *   k_pages        float [pages, H, page, d_K]
+ *   v_pages        v_dtype [pages, H, page, d_V]  (16-B aligned)
+ *   order_codes    code type [2, order_pages, H, page]
+ *   order_idx      int32 [2, order_pages, H, page]
+ *   order_table    int32 [B, table_len]: entry e of prefix c of sequence b is row
+ *         e % page of page order_table[b][e / page] in plane c % 2.  It may be
+ *         page_table itself.  Sequences may share K/V pages (a common prompt), but
+ *         a page of the order pools belongs to one sequence.
+ *
+ * One step: zeta_cache_append, zeta_cache_order (needed in the calls in which
+ * some sequence completes a chunk, a no-op for the others), zeta_cache_attend,
+ * on one stream, with the same start and count.  As n <= C a call completes at
+ * most one chunk per sequence, and the two planes hold the prefixes of both
+ * chunks that its tokens lie in.
+ *
+ * Limits beside those above: C <= 8192, B*H*n < 2^31, pages * H * page < 2^31
+ * (order_pages likewise).  No call needs a workspace; calls on different
+ * sequences may overlap on different streams.  The calls have no backward.
+ */
+typedef struct {
+    int32_t n, page, pages, order_pages, table_len;
+} zeta_cache_t;
+
+/*
+ * zeta_cache_append -- keys and values of new tokens into their pages.
+ *   k         in : float [B, H, n, d_K]
+ *   v         in : v_dtype [B, H, n, d_V]  (16-B aligned)
+ *   k_pages, v_pages  in/out (written at the new tokens' rows only)
+ *   dev_status  optional int32 device word (ZETA_ERR_BOUNDS as above)
+ * Two new tokens of one call that map to the same row (a page given to two
+ * sequences) leave one of them there, which one is not defined.
+ * Errors: ZETA_ERR_INVALID_ARG, ZETA_ERR_UNSUPPORTED.
+ */
+zeta_status_t zeta_cache_append(const zeta_problem_t *p, const zeta_cache_t *cc, const float *k,
+                                const void *v, const int32_t *start, const int32_t *count,
+                                const int32_t *page_table, float *k_pages, void *v_pages,
+                                int32_t *dev_status, cudaStream_t stream);
+
+/*
+ * zeta_cache_order -- the sorted prefix of every sequence that completes a chunk.
+ * Passage: as for zeta_sort_chunks (OpenReview reply A3 "Chunking ... & Where
+ * efficiency is coming from").
+ * If floor((start + count) / C) > floor(start / C), with c the chunk completed,
+ * prefix c + 1 (the (c + 1) C keys of chunks 0..c ordered by (code, token)) is
+ * written to plane (c + 1) % 2 from prefix c in plane c % 2 and the keys of chunk
+ * c, whose codes are those of zeta_encode.  Other sequences are left alone.
+ *   k_pages   in : after zeta_cache_append
+ *   order_codes, order_idx  in/out
+ *   dev_status  optional int32 device word: a page out of range skips the
+ *               sequence's head (nothing of its new prefix is defined then).
+ * Errors: ZETA_ERR_INVALID_ARG, ZETA_ERR_UNSUPPORTED.
+ */
+zeta_status_t zeta_cache_order(const zeta_problem_t *p, const zeta_cache_t *cc,
+                               const int32_t *start, const int32_t *count,
+                               const int32_t *page_table, const float *k_pages,
+                               const int32_t *order_table, void *order_codes, int32_t *order_idx,
+                               int32_t *dev_status, cudaStream_t stream);
+
+/*
+ * zeta_cache_attend -- attention of the new tokens over the cache.
+ * Passage: as for zeta_select_topk and zeta_attend_fwd.
+ * The token at position i = start[b] + t, in chunk c = i / C, attends to the k
+ * keys around its code's rank in prefix c (none for c = 0) and to the keys of
+ * its own chunk up to itself; weights, out and rowsum as in zeta_attend_fwd.
+ *   q         in : float [B, H, n, d_K]
+ *   gamma     in : float [H]
+ *   k_pages, v_pages, order_codes, order_idx  in : after append and order
+ *   out       out: v_dtype [B, H, n, d_V]  (16-B aligned)
+ *   rowsum    out: float [B, H, n]
+ *   idx       out: int32 [B, H, n, k], the window's tokens (-1 in chunk 0), or
+ *             null
+ *   dev_status  optional int32 device word; an order entry outside [0, cC) or a
+ *             page out of range drops its key and records ZETA_ERR_BOUNDS.
+ * Errors: ZETA_ERR_INVALID_ARG, ZETA_ERR_UNSUPPORTED.
+ */
+zeta_status_t zeta_cache_attend(const zeta_problem_t *p, const zeta_cache_t *cc, const float *q,
+                                const float *gamma, const int32_t *start, const int32_t *count,
+                                const int32_t *page_table, const float *k_pages,
+                                const void *v_pages, const int32_t *order_table,
+                                const void *order_codes, const int32_t *order_idx, void *out,
+                                float *rowsum, int32_t *idx, int32_t *dev_status,
+                                cudaStream_t stream);
+
+/*
  * zeta_check_bounded_wait -- diagnostic of the device-side failure detection.
  * The pages have no counterpart: every wait of the TMA-fed and tensor-core
  * kernels (zeta_project_encode, the own-chunk block of zeta_attend_bwd) on an

@@ -48,6 +48,11 @@ class zeta_proj_t(ctypes.Structure):
     _fields_ = [("D", ctypes.c_int32), ("F", ctypes.c_int32)]
 
 
+class zeta_cache_t(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("page", ctypes.c_int32), ("pages", ctypes.c_int32),
+                ("order_pages", ctypes.c_int32), ("table_len", ctypes.c_int32)]
+
+
 def problem(B, H, N, d_K, d_V, k, C, bits, v_dtype="bf16", flags=0,
             weight="cauchy") -> zeta_problem_t:
     """flags: raw flag bits; weight: 'cauchy', 'softmax' or 'inv_euclid' (ORed in)."""
@@ -107,6 +112,13 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
     L.zeta_check_bounded_wait.restype = S
     L.zeta_select_attend_fwd.restype = S
     L.zeta_attend_bwd.restype = S
+    PC = ctypes.POINTER(zeta_cache_t)
+    L.zeta_cache_append.argtypes = [PP, PC] + [P] * 9
+    L.zeta_cache_append.restype = S
+    L.zeta_cache_order.argtypes = [PP, PC] + [P] * 9
+    L.zeta_cache_order.restype = S
+    L.zeta_cache_attend.argtypes = [PP, PC] + [P] * 15
+    L.zeta_cache_attend.restype = S
     _lib = L
     return L
 
@@ -366,3 +378,74 @@ def zeta_attend_bwd(p, q, k, v, gamma, idx, dout, dq, dk, dv, dgamma, workspace,
                                  _ptr(idx), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
                                  _ptr(dgamma), _ptr(workspace), ws_bytes, _ptr(dev_status),
                                  _stream(stream)))
+
+
+# ------------------------------------------------------------- paged cache ---
+
+def _expect_cache(p, c, start, count, tables, dev_status):
+    _expect(start, "start", torch.int32, p.B)
+    _expect(count, "count", torch.int32, p.B)
+    for t, name in tables:
+        _expect(t, name, torch.int32, p.B * c.table_len)
+    _expect(dev_status, "dev_status", torch.int32, 1)
+
+
+def zeta_cache_append(p, c, k, v, start, count, page_table, k_pages, v_pages, dev_status=None,
+                      stream=None):
+    """c: zeta_cache_t; k [B,H,n,d_K], v [B,H,n,d_V] into k_pages [pages,H,page,d_K],
+    v_pages [pages,H,page,d_V]; start, count int32 [B]; page_table int32 [B,table_len]."""
+    S, R = p.B * p.H * c.n, c.pages * p.H * c.page
+    vt = v_torch_dtype(p)
+    _expect(k, "k", torch.float32, S * p.d_K)
+    _expect(v, "v", vt, S * p.d_V)
+    _expect(k_pages, "k_pages", torch.float32, R * p.d_K)
+    _expect(v_pages, "v_pages", vt, R * p.d_V)
+    _expect_cache(p, c, start, count, [(page_table, "page_table")], dev_status)
+    _check("zeta_cache_append",
+           lib().zeta_cache_append(ctypes.byref(p), ctypes.byref(c), _ptr(k), _ptr(v),
+                                   _ptr(start), _ptr(count), _ptr(page_table), _ptr(k_pages),
+                                   _ptr(v_pages), _ptr(dev_status), _stream(stream)))
+
+
+def zeta_cache_order(p, c, start, count, page_table, k_pages, order_table, order_codes,
+                     order_idx, dev_status=None, stream=None):
+    """order_codes, order_idx [2,order_pages,H,page]: the prefix of every sequence that
+    completes a chunk with this call's tokens."""
+    R = 2 * c.order_pages * p.H * c.page
+    _expect(k_pages, "k_pages", torch.float32, c.pages * p.H * c.page * p.d_K)
+    _expect(order_codes, "order_codes", code_dtype(p), R)
+    _expect(order_idx, "order_idx", torch.int32, R)
+    _expect_cache(p, c, start, count,
+                  [(page_table, "page_table"), (order_table, "order_table")], dev_status)
+    _check("zeta_cache_order",
+           lib().zeta_cache_order(ctypes.byref(p), ctypes.byref(c), _ptr(start), _ptr(count),
+                                  _ptr(page_table), _ptr(k_pages), _ptr(order_table),
+                                  _ptr(order_codes), _ptr(order_idx), _ptr(dev_status),
+                                  _stream(stream)))
+
+
+def zeta_cache_attend(p, c, q, gamma, start, count, page_table, k_pages, v_pages, order_table,
+                      order_codes, order_idx, out, rowsum, idx=None, dev_status=None,
+                      stream=None):
+    """q [B,H,n,d_K]; out [B,H,n,d_V], rowsum [B,H,n], idx [B,H,n,k] or None: rows
+    count[b] .. n-1 are left as they were."""
+    S, R = p.B * p.H * c.n, c.pages * p.H * c.page
+    O = 2 * c.order_pages * p.H * c.page
+    vt = v_torch_dtype(p)
+    _expect(q, "q", torch.float32, S * p.d_K)
+    _expect(gamma, "gamma", torch.float32, p.H)
+    _expect(k_pages, "k_pages", torch.float32, R * p.d_K)
+    _expect(v_pages, "v_pages", vt, R * p.d_V)
+    _expect(order_codes, "order_codes", code_dtype(p), O)
+    _expect(order_idx, "order_idx", torch.int32, O)
+    _expect(out, "out", vt, S * p.d_V)
+    _expect(rowsum, "rowsum", torch.float32, S)
+    _expect(idx, "idx", torch.int32, S * p.k)
+    _expect_cache(p, c, start, count,
+                  [(page_table, "page_table"), (order_table, "order_table")], dev_status)
+    _check("zeta_cache_attend",
+           lib().zeta_cache_attend(ctypes.byref(p), ctypes.byref(c), _ptr(q), _ptr(gamma),
+                                   _ptr(start), _ptr(count), _ptr(page_table), _ptr(k_pages),
+                                   _ptr(v_pages), _ptr(order_table), _ptr(order_codes),
+                                   _ptr(order_idx), _ptr(out), _ptr(rowsum), _ptr(idx),
+                                   _ptr(dev_status), _stream(stream)))

@@ -6,7 +6,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
-#include "common.cuh"
+#include "cache.cuh"
 
 zeta::CallRange::CallRange(const char *name) { nvtxRangePushA(name); }
 zeta::CallRange::~CallRange() { nvtxRangePop(); }
@@ -40,6 +40,32 @@ zeta_status_t check_problem(const zeta_problem_t *pp, Prob *out) {
     r.code64 = p.d_K * p.bits > 32;
     r.wk = (int)(p.flags & 3u);
     *out = r;
+    return ZETA_OK;
+}
+
+// The cache's sizes and the tables that every cache call takes; an empty call
+// (no sequences, heads or rows) needs no pointers.
+zeta_status_t check_cache(const zeta_problem_t *pp, const zeta_cache_t *cc, Prob *pr,
+                          zeta::Cache *out) {
+    const zeta_status_t s = check_problem(pp, pr);
+    if (s != ZETA_OK) return s;
+    if (!cc || cc->n < 0 || cc->page < 1 || (cc->page & (cc->page - 1)) != 0 || cc->pages < 0 ||
+        cc->order_pages < 0 || cc->table_len < 0)
+        return ZETA_ERR_INVALID_ARG;
+    if ((int64_t)cc->table_len * cc->page < pr->N) return ZETA_ERR_INVALID_ARG;
+    if (cc->page > 65536 || cc->n > pr->C || pr->C > 8192) return ZETA_ERR_UNSUPPORTED;
+    if (pr->S * cc->n > INT32_MAX) return ZETA_ERR_UNSUPPORTED;
+    const int64_t per = (int64_t)pr->H * cc->page;
+    if (cc->pages * per > INT32_MAX || cc->order_pages * per > INT32_MAX)
+        return ZETA_ERR_UNSUPPORTED;
+    zeta::Cache c{};
+    c.n = cc->n;
+    while ((1 << c.psh) < cc->page) ++c.psh;
+    c.pmask = cc->page - 1;
+    c.pages = cc->pages;
+    c.opages = cc->order_pages;
+    c.tlen = cc->table_len;
+    *out = c;
     return ZETA_OK;
 }
 
@@ -242,6 +268,75 @@ ZETA_API zeta_status_t zeta_attend_bwd(const zeta_problem_t *p, const float *q, 
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ZETA_ERR_WORKSPACE;
     return from_cuda(zeta::launch_attend_bwd(pr, q, k, v, gamma, idx, dout, dq, dk, dv, dgamma,
                                              workspace, dev_status, stream));
+}
+
+ZETA_API zeta_status_t zeta_cache_append(const zeta_problem_t *p, const zeta_cache_t *cc,
+                                         const float *k, const void *v, const int32_t *start,
+                                         const int32_t *count, const int32_t *page_table,
+                                         float *k_pages, void *v_pages, int32_t *dev_status,
+                                         cudaStream_t stream) {
+    zeta::CallRange range_("zeta_cache_append");
+    Prob pr;
+    zeta::Cache c;
+    zeta_status_t s = check_cache(p, cc, &pr, &c);
+    if (s != ZETA_OK) return s;
+    if (empty(pr) || c.n == 0) return ZETA_OK;
+    if (!k || !v || !start || !count || !page_table || !k_pages || !v_pages)
+        return ZETA_ERR_INVALID_ARG;
+    if (!aligned16(v) || !aligned16(v_pages)) return ZETA_ERR_INVALID_ARG;
+    c.start = start;
+    c.count = count;
+    c.ptab = page_table;
+    return from_cuda(
+        zeta::launch_cache_append(pr, c, k, v, k_pages, v_pages, dev_status, stream));
+}
+
+ZETA_API zeta_status_t zeta_cache_order(const zeta_problem_t *p, const zeta_cache_t *cc,
+                                        const int32_t *start, const int32_t *count,
+                                        const int32_t *page_table, const float *k_pages,
+                                        const int32_t *order_table, void *order_codes,
+                                        int32_t *order_idx, int32_t *dev_status,
+                                        cudaStream_t stream) {
+    zeta::CallRange range_("zeta_cache_order");
+    Prob pr;
+    zeta::Cache c;
+    zeta_status_t s = check_cache(p, cc, &pr, &c);
+    if (s != ZETA_OK) return s;
+    if (empty(pr) || c.n == 0) return ZETA_OK;
+    if (!start || !count || !page_table || !k_pages || !order_table || !order_codes || !order_idx)
+        return ZETA_ERR_INVALID_ARG;
+    c.start = start;
+    c.count = count;
+    c.ptab = page_table;
+    c.otab = order_table;
+    return from_cuda(
+        zeta::launch_cache_order(pr, c, k_pages, order_codes, order_idx, dev_status, stream));
+}
+
+ZETA_API zeta_status_t zeta_cache_attend(const zeta_problem_t *p, const zeta_cache_t *cc,
+                                         const float *q, const float *gamma,
+                                         const int32_t *start, const int32_t *count,
+                                         const int32_t *page_table, const float *k_pages,
+                                         const void *v_pages, const int32_t *order_table,
+                                         const void *order_codes, const int32_t *order_idx,
+                                         void *out, float *rowsum, int32_t *idx,
+                                         int32_t *dev_status, cudaStream_t stream) {
+    zeta::CallRange range_("zeta_cache_attend");
+    Prob pr;
+    zeta::Cache c;
+    zeta_status_t s = check_cache(p, cc, &pr, &c);
+    if (s != ZETA_OK) return s;
+    if (empty(pr) || c.n == 0) return ZETA_OK;
+    if (!q || !gamma || !start || !count || !page_table || !k_pages || !v_pages ||
+        !order_table || !order_codes || !order_idx || !out || !rowsum)
+        return ZETA_ERR_INVALID_ARG;
+    if (!aligned16(v_pages) || !aligned16(out)) return ZETA_ERR_INVALID_ARG;
+    c.start = start;
+    c.count = count;
+    c.ptab = page_table;
+    c.otab = order_table;
+    return from_cuda(zeta::launch_cache_attend(pr, c, q, gamma, k_pages, v_pages, order_codes,
+                                               order_idx, out, rowsum, idx, dev_status, stream));
 }
 
 ZETA_API zeta_status_t zeta_check_bounded_wait(uint32_t iterations, int32_t arrive,

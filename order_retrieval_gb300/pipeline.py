@@ -11,8 +11,13 @@ are indexed along the cyclic shifts, or all orderings, of the three
 coordinates and every curve contributes k // curves keys): the codes and
 prefix tables gain a leading curve dimension, one sort call covers every
 curve, and the union of the windows feeds the same attend kernels.
+
+``ZetaCache`` serves a trained model: keys and values of many sequences in
+pages, new tokens appended and attended in batches of up to C per sequence.
 """
 from __future__ import annotations
+
+import ctypes
 
 import torch
 
@@ -126,3 +131,147 @@ def zeta_attention(q, k, v, gamma, C: int, k_sel: int, bits: int = 10, curves: i
     """weight: 'cauchy' (the method), 'softmax' (of -|q-k|^2/gamma^2) or
     'inv_euclid' (1/|q-k|); see zeta_weight_t in include/zeta.h."""
     return ZetaAttention.apply(q, k, v, gamma, C, k_sel, bits, curves, weight)
+
+
+class ZetaCache:
+    """Paged key/value cache: the three serving calls on one set of pools.
+
+    k_pages f32 [pages, H, page, d_K], v_pages [pages, H, page, d_V],
+    order_codes (the problem's code type) and order_idx (int32)
+    [2, order_pages, H, page]; ``empty`` allocates them.  N: the longest
+    sequence (a multiple of C); C, k, bits, weight as for ``zeta_attention``.
+
+    Tables are int32 [B, table_len]: token t of sequence b is row t % page of page
+    table[b, t // page]; which pages a sequence gets is the caller's business.
+    Per step and batch, with the same start and count (int32 [B], tokens before
+    the step and tokens brought, count <= n <= C)::
+
+        cache.append(k, v, start, count, table)
+        cache.order(start, count, table)          # when a sequence completes a chunk
+        cache.attend(q, gamma, start, count, table, out, rowsum)
+
+    The prefixes of completed chunks are kept in the order pools through
+    order_table (default: table; pass another one when sequences share K/V pages).
+    Everything is enqueued on the given or current stream and allocates nothing,
+    so a step can be captured into a CUDA graph.  Findings of the kernels (a
+    length or page out of range) go to ``status``, one int32 word, unless
+    dev_status is given.  There is no backward.
+    """
+
+    def __init__(self, k_pages, v_pages, order_codes, order_idx, N: int, C: int, k: int,
+                 bits: int = 10, weight: str = "cauchy"):
+        if k_pages.dim() != 4 or v_pages.dim() != 4 or k_pages.shape[:3] != v_pages.shape[:3]:
+            raise ValueError("k_pages and v_pages must be [pages, H, page, d] of the same pages")
+        self.pages, self.H, self.page, self.d_K = k_pages.shape
+        self.d_V = v_pages.shape[3]
+        if v_pages.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"v_pages: dtype {v_pages.dtype}, expected bfloat16 or float32")
+        self.v_dtype = zb.ZETA_BF16 if v_pages.dtype == torch.bfloat16 else zb.ZETA_F32
+        self.N, self.C, self.k, self.bits = N, C, k, bits
+        self.flags = zb.WEIGHTS[weight]
+        p = self._problem(1)
+        if zb.zeta_code_bytes(p) == 0:
+            raise zb.ZetaError("zeta_code_bytes", 1)
+        shape = (2, order_codes.shape[1], self.H, self.page)
+        self.order_pages = order_codes.shape[1]
+        self.device = k_pages.device
+        if self.device.type != "cuda":
+            raise ValueError("ZETA tensors must be CUDA tensors")
+        self._take(k_pages, "k_pages", torch.float32, tuple(k_pages.shape))
+        self._take(v_pages, "v_pages", v_pages.dtype, tuple(v_pages.shape))
+        self._take(order_codes, "order_codes", zb.code_dtype(p), shape)
+        self._take(order_idx, "order_idx", torch.int32, shape)
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.order_codes, self.order_idx = order_codes, order_idx
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    @classmethod
+    def empty(cls, pages: int, page: int, H: int, d_K: int, d_V: int, N: int, C: int, k: int,
+              bits: int = 10, v_dtype=torch.bfloat16, weight: str = "cauchy", device="cuda",
+              order_pages: int | None = None):
+        """A cache with pools of its own (order_pages defaults to pages)."""
+        op = pages if order_pages is None else order_pages
+        ct = torch.int64 if d_K * bits > 32 else torch.int32
+        return cls(torch.zeros(pages, H, page, d_K, device=device),
+                   torch.zeros(pages, H, page, d_V, dtype=v_dtype, device=device),
+                   torch.zeros(2, op, H, page, dtype=ct, device=device),
+                   torch.zeros(2, op, H, page, dtype=torch.int32, device=device),
+                   N, C, k, bits, weight)
+
+    def _problem(self, B: int) -> zb.zeta_problem_t:
+        return zb.zeta_problem_t(B, self.H, self.N, self.d_K, self.d_V, self.k, self.C, self.bits,
+                                 self.v_dtype, self.flags)
+
+    def _take(self, t, name, dtype, shape):
+        """Pointer of a tensor of the given type, shape and the cache's device."""
+        if t.dtype is not dtype:
+            raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+        if t.device != self.device:
+            raise ValueError(f"{name}: on {t.device}, the cache is on {self.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: ZETA tensors must be contiguous")
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name}: the cache calls have no backward (use torch.no_grad)")
+        return t.data_ptr()
+
+    def _batch(self, start, count, tables, n):
+        """What every call takes: problem, cache sizes, pointers of start, count and tables."""
+        if tables[0].dim() != 2:
+            raise ValueError(f"page_table: {tables[0].dim()} dimensions, expected 2")
+        B, width = tables[0].shape
+        got = [self._take(start, "start", torch.int32, (B,)),
+               self._take(count, "count", torch.int32, (B,))]
+        for t, name in zip(tables, ("page_table", "order_table")):
+            got.append(self._take(t, name, torch.int32, (B, width)))
+        return (self._problem(B),
+                zb.zeta_cache_t(n, self.page, self.pages, self.order_pages, width), *got)
+
+    def _call(self, fn, p, c, args, dev_status, stream):
+        st = self.status if dev_status is None else dev_status
+        sp = self._take(st, "dev_status", torch.int32, (1,))
+        f = getattr(zb.lib(), fn)
+        if torch.cuda.current_device() == self.device.index:
+            code = f(ctypes.byref(p), ctypes.byref(c), *args, sp, zb._stream(stream))
+        else:
+            with torch.cuda.device(self.device):
+                code = f(ctypes.byref(p), ctypes.byref(c), *args, sp, zb._stream(stream))
+        if code != 0:
+            raise zb.ZetaError(fn, code)
+
+    def append(self, k, v, start, count, page_table, dev_status=None, stream=None):
+        """k f32 [B,H,n,d_K], v [B,H,n,d_V]: rows 0 .. count[b]-1 of sequence b become its
+        tokens start[b] .. start[b]+count[b]-1."""
+        p, c, sp, cp, tp = self._batch(start, count, (page_table,), k.shape[2])
+        kp = self._take(k, "k", torch.float32, (p.B, self.H, c.n, self.d_K))
+        vp = self._take(v, "v", self.v_pages.dtype, (p.B, self.H, c.n, self.d_V))
+        self._call("zeta_cache_append", p, c,
+                   (kp, vp, sp, cp, tp, self.k_pages.data_ptr(), self.v_pages.data_ptr()),
+                   dev_status, stream)
+
+    def order(self, start, count, page_table, order_table=None, dev_status=None, stream=None):
+        """The sorted prefix of every sequence that completes a chunk with these tokens."""
+        p, c, sp, cp, tp, op = self._batch(
+            start, count, (page_table, page_table if order_table is None else order_table), self.C)
+        self._call("zeta_cache_order", p, c,
+                   (sp, cp, tp, self.k_pages.data_ptr(), op, self.order_codes.data_ptr(),
+                    self.order_idx.data_ptr()), dev_status, stream)
+
+    def attend(self, q, gamma, start, count, page_table, out, rowsum, order_table=None, idx=None,
+               dev_status=None, stream=None):
+        """q f32 [B,H,n,d_K], gamma f32 [H] -> out [B,H,n,d_V], rowsum f32 [B,H,n] and, where
+        given, idx int32 [B,H,n,k]; rows count[b] .. n-1 stay as they were."""
+        p, c, sp, cp, tp, op = self._batch(
+            start, count, (page_table, page_table if order_table is None else order_table),
+            q.shape[2])
+        lead = (p.B, self.H, c.n)
+        qp = self._take(q, "q", torch.float32, (*lead, self.d_K))
+        gp = self._take(gamma, "gamma", torch.float32, (self.H,))
+        outp = self._take(out, "out", self.v_pages.dtype, (*lead, self.d_V))
+        rp = self._take(rowsum, "rowsum", torch.float32, lead)
+        ip = None if idx is None else self._take(idx, "idx", torch.int32, (*lead, self.k))
+        self._call("zeta_cache_attend", p, c,
+                   (qp, gp, sp, cp, tp, self.k_pages.data_ptr(), self.v_pages.data_ptr(), op,
+                    self.order_codes.data_ptr(), self.order_idx.data_ptr(), outp, rp, ip),
+                   dev_status, stream)
