@@ -177,13 +177,18 @@ class ZetaCache:
         self.device = k_pages.device
         if self.device.type != "cuda":
             raise ValueError("ZETA tensors must be CUDA tensors")
-        self._take(k_pages, "k_pages", torch.float32, tuple(k_pages.shape))
-        self._take(v_pages, "v_pages", v_pages.dtype, tuple(v_pages.shape))
-        self._take(order_codes, "order_codes", zb.code_dtype(p), shape)
-        self._take(order_idx, "order_idx", torch.int32, shape)
+        self._index = self.device.index
+        self._vt = v_pages.dtype
+        self._kp = self._take(k_pages, "k_pages", torch.float32, tuple(k_pages.shape))
+        self._vp = self._take(v_pages, "v_pages", self._vt, tuple(v_pages.shape))
+        self._ocp = self._take(order_codes, "order_codes", zb.code_dtype(p), shape)
+        self._oip = self._take(order_idx, "order_idx", torch.int32, shape)
         self.k_pages, self.v_pages = k_pages, v_pages
         self.order_codes, self.order_idx = order_codes, order_idx
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._status_ptr = self.status.data_ptr()
+        self._lib = zb.lib()
+        self._structs = {}
 
     @classmethod
     def empty(cls, pages: int, page: int, H: int, d_K: int, d_V: int, N: int, C: int, k: int,
@@ -202,8 +207,25 @@ class ZetaCache:
         return zb.zeta_problem_t(B, self.H, self.N, self.d_K, self.d_V, self.k, self.C, self.bits,
                                  self.v_dtype, self.flags)
 
+    def _sizes(self, B: int, n: int, width: int):
+        """References to the C structs of a batch size, made once per (B, n, width) and
+        never changed (a step costs the host a few microseconds, of which building them
+        would be a good part)."""
+        got = self._structs.get((B, n, width))
+        if got is None:
+            if len(self._structs) >= 1024:
+                self._structs.clear()
+            got = (ctypes.byref(self._problem(B)),
+                   ctypes.byref(zb.zeta_cache_t(n, self.page, self.pages, self.order_pages,
+                                                width)))
+            self._structs[B, n, width] = got
+        return got
+
     def _take(self, t, name, dtype, shape):
         """Pointer of a tensor of the given type, shape and the cache's device."""
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == self._index
+                and t.is_contiguous() and not t.requires_grad):
+            return t.data_ptr()
         if t.dtype is not dtype:
             raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
         if t.shape != shape:
@@ -212,66 +234,66 @@ class ZetaCache:
             raise ValueError(f"{name}: on {t.device}, the cache is on {self.device}")
         if not t.is_contiguous():
             raise ValueError(f"{name}: ZETA tensors must be contiguous")
-        if t.requires_grad and torch.is_grad_enabled():
+        if torch.is_grad_enabled():
             raise ValueError(f"{name}: the cache calls have no backward (use torch.no_grad)")
         return t.data_ptr()
 
-    def _batch(self, start, count, tables, n):
-        """What every call takes: problem, cache sizes, pointers of start, count and tables."""
-        if tables[0].dim() != 2:
-            raise ValueError(f"page_table: {tables[0].dim()} dimensions, expected 2")
-        B, width = tables[0].shape
-        got = [self._take(start, "start", torch.int32, (B,)),
-               self._take(count, "count", torch.int32, (B,))]
-        for t, name in zip(tables, ("page_table", "order_table")):
-            got.append(self._take(t, name, torch.int32, (B, width)))
-        return (self._problem(B),
-                zb.zeta_cache_t(n, self.page, self.pages, self.order_pages, width), *got)
+    def _table(self, t):
+        if t.dim() != 2:
+            raise ValueError(f"page_table: {t.dim()} dimensions, expected 2")
+        return t.shape
 
-    def _call(self, fn, p, c, args, dev_status, stream):
-        st = self.status if dev_status is None else dev_status
-        sp = self._take(st, "dev_status", torch.int32, (1,))
-        f = getattr(zb.lib(), fn)
-        if torch.cuda.current_device() == self.device.index:
-            code = f(ctypes.byref(p), ctypes.byref(c), *args, sp, zb._stream(stream))
+    def _call(self, fn, pc, args, dev_status, stream):
+        st = self._status_ptr if dev_status is None else self._take(dev_status, "dev_status",
+                                                                    torch.int32, (1,))
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(self._index)
+        elif not isinstance(stream, int):
+            stream = stream.cuda_stream
+        f = getattr(self._lib, fn)
+        if torch._C._cuda_getDevice() == self._index:
+            code = f(*pc, *args, st, stream)
         else:
-            with torch.cuda.device(self.device):
-                code = f(ctypes.byref(p), ctypes.byref(c), *args, sp, zb._stream(stream))
+            with torch.cuda.device(self._index):
+                code = f(*pc, *args, st, stream)
         if code != 0:
             raise zb.ZetaError(fn, code)
 
     def append(self, k, v, start, count, page_table, dev_status=None, stream=None):
         """k f32 [B,H,n,d_K], v [B,H,n,d_V]: rows 0 .. count[b]-1 of sequence b become its
         tokens start[b] .. start[b]+count[b]-1."""
-        p, c, sp, cp, tp = self._batch(start, count, (page_table,), k.shape[2])
-        kp = self._take(k, "k", torch.float32, (p.B, self.H, c.n, self.d_K))
-        vp = self._take(v, "v", self.v_pages.dtype, (p.B, self.H, c.n, self.d_V))
-        self._call("zeta_cache_append", p, c,
-                   (kp, vp, sp, cp, tp, self.k_pages.data_ptr(), self.v_pages.data_ptr()),
+        B, width = self._table(page_table)
+        n, take, i32 = k.shape[2], self._take, torch.int32
+        self._call("zeta_cache_append", self._sizes(B, n, width),
+                   (take(k, "k", torch.float32, (B, self.H, n, self.d_K)),
+                    take(v, "v", self._vt, (B, self.H, n, self.d_V)),
+                    take(start, "start", i32, (B,)), take(count, "count", i32, (B,)),
+                    take(page_table, "page_table", i32, (B, width)), self._kp, self._vp),
                    dev_status, stream)
 
     def order(self, start, count, page_table, order_table=None, dev_status=None, stream=None):
         """The sorted prefix of every sequence that completes a chunk with these tokens."""
-        p, c, sp, cp, tp, op = self._batch(
-            start, count, (page_table, page_table if order_table is None else order_table), self.C)
-        self._call("zeta_cache_order", p, c,
-                   (sp, cp, tp, self.k_pages.data_ptr(), op, self.order_codes.data_ptr(),
-                    self.order_idx.data_ptr()), dev_status, stream)
+        B, width = self._table(page_table)
+        take, i32 = self._take, torch.int32
+        tp = take(page_table, "page_table", i32, (B, width))
+        op = tp if order_table is None else take(order_table, "order_table", i32, (B, width))
+        self._call("zeta_cache_order", self._sizes(B, self.C, width),
+                   (take(start, "start", i32, (B,)), take(count, "count", i32, (B,)), tp, self._kp,
+                    op, self._ocp, self._oip), dev_status, stream)
 
     def attend(self, q, gamma, start, count, page_table, out, rowsum, order_table=None, idx=None,
                dev_status=None, stream=None):
         """q f32 [B,H,n,d_K], gamma f32 [H] -> out [B,H,n,d_V], rowsum f32 [B,H,n] and, where
         given, idx int32 [B,H,n,k]; rows count[b] .. n-1 stay as they were."""
-        p, c, sp, cp, tp, op = self._batch(
-            start, count, (page_table, page_table if order_table is None else order_table),
-            q.shape[2])
-        lead = (p.B, self.H, c.n)
-        qp = self._take(q, "q", torch.float32, (*lead, self.d_K))
-        gp = self._take(gamma, "gamma", torch.float32, (self.H,))
-        outp = self._take(out, "out", self.v_pages.dtype, (*lead, self.d_V))
-        rp = self._take(rowsum, "rowsum", torch.float32, lead)
-        ip = None if idx is None else self._take(idx, "idx", torch.int32, (*lead, self.k))
-        self._call("zeta_cache_attend", p, c,
-                   (qp, gp, sp, cp, tp, self.k_pages.data_ptr(), self.v_pages.data_ptr(), op,
-                    self.order_codes.data_ptr(), self.order_idx.data_ptr(), outp, rp, ip),
+        B, width = self._table(page_table)
+        H, n, take, f32, i32 = self.H, q.shape[2], self._take, torch.float32, torch.int32
+        tp = take(page_table, "page_table", i32, (B, width))
+        op = tp if order_table is None else take(order_table, "order_table", i32, (B, width))
+        self._call("zeta_cache_attend", self._sizes(B, n, width),
+                   (take(q, "q", f32, (B, H, n, self.d_K)), take(gamma, "gamma", f32, (H,)),
+                    take(start, "start", i32, (B,)), take(count, "count", i32, (B,)), tp,
+                    self._kp, self._vp, op, self._ocp, self._oip,
+                    take(out, "out", self._vt, (B, H, n, self.d_V)),
+                    take(rowsum, "rowsum", f32, (B, H, n)),
+                    None if idx is None else take(idx, "idx", i32, (B, H, n, self.k))),
                    dev_status, stream)
