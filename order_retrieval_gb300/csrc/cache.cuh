@@ -42,10 +42,24 @@ __device__ __forceinline__ int page_row(const int32_t *__restrict__ tab, int t, 
     return (unsigned)id < (unsigned)pages ? (((id * H + h) << psh) | (t & pmask)) : -1;
 }
 
+// The same in two halves, so that independent lookups are in flight together and
+// nothing looks at a page number before it is needed (a warp issues in order: a
+// check placed behind a load waits for that load).
+__device__ __forceinline__ int page_id(const int32_t *__restrict__ tab, int t, int psh) {
+    return __ldg(tab + (t >> psh));
+}
+__device__ __forceinline__ int row_in(int id, int t, int h, int H, int psh, int pmask, int pages) {
+    return (unsigned)id < (unsigned)pages ? (((id * H + h) << psh) | (t & pmask)) : -1;
+}
+
 // Z-order code of one point in registers (zeta_encode's, see encode.cu).
 __device__ __forceinline__ uint64_t code_of(const float (&x)[kMaxDK], int dK, int bits) {
     const float scale = __int_as_float((126 + bits) << 23);   // 2^(bits-1)
     const float umax = static_cast<float>((1u << bits) - 1u);
+    if (dK == 3 && bits <= 10)
+        return (dilate3_10(quantise(x[0], scale, umax)) << 2) |
+               (dilate3_10(quantise(x[1], scale, umax)) << 1) |
+               dilate3_10(quantise(x[2], scale, umax));
     if (dK == 3)
         return morton3(quantise(x[0], scale, umax), quantise(x[1], scale, umax),
                        quantise(x[2], scale, umax));
@@ -67,6 +81,42 @@ __device__ __forceinline__ uint64_t code_of(const float (&x)[kMaxDK], int dK, in
 __device__ __forceinline__ void load_point(float (&x)[kMaxDK], const float *p, int dK) {
 #pragma unroll
     for (int d = 0; d < kMaxDK; ++d) x[d] = d < dK ? p[d] : 0.f;
+}
+
+// 16 bytes through the read-only path, zeros where `ok` is false: one predicated
+// load.  (Written as a branch, the loads of a row's pieces wait for one another:
+// 7 us per gathered row instead of one memory latency.)
+__device__ __forceinline__ uint4 ld16_if(const void *p, bool ok) {
+    uint4 a = make_uint4(0u, 0u, 0u, 0u);
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n"
+        " @q ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];\n}\n"
+        : "+r"(a.x), "+r"(a.y), "+r"(a.z), "+r"(a.w)
+        : "l"(p), "r"((int)ok));
+    return a;
+}
+__device__ __forceinline__ uint32_t ld4_if(const void *p, bool ok) {
+    uint32_t a = 0u;
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n @q ld.global.nc.b32 %0, [%1];\n}\n"
+                 : "+r"(a)
+                 : "l"(p), "r"((int)ok));
+    return a;
+}
+__device__ __forceinline__ uint32_t ld2_if(const void *p, bool ok) {
+    unsigned short a = 0;
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n @q ld.global.nc.u16 %0, [%1];\n}\n"
+                 : "+h"(a)
+                 : "l"(p), "r"((int)ok));
+    return a;
+}
+
+// The same for a word that is -1 where `ok` is false.
+__device__ __forceinline__ int ldi_if(const int32_t *p, bool ok) {
+    int a = -1;
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n @q ld.global.nc.b32 %0, [%1];\n}\n"
+                 : "+r"(a)
+                 : "l"(p), "r"((int)ok));
+    return a;
 }
 
 cudaError_t launch_cache_append(const Prob &p, const Cache &c, const float *k, const void *v,

@@ -21,7 +21,7 @@
 //    distributed shared memory: no workspace, one launch, the same bits each run.
 #include <cooperative_groups.h>
 
-#include "cache.cuh"
+#include "cache_tile.cuh"
 
 namespace zeta {
 namespace {
@@ -29,6 +29,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kWarps = 8;
+constexpr int kTileRows = 4;           // rows of a call from which the tile kernel runs
 constexpr int kThreads = kWarps * 32;
 
 // One (b, h, t): where its keys are and what they are weighed with.
@@ -60,21 +61,15 @@ struct Cut {
     struct Piece {
         uint32_t w[WIDE ? 4 : 1];
     };
-    static __device__ __forceinline__ Piece none() {
-        Piece p;
-#pragma unroll
-        for (int e = 0; e < (WIDE ? 4 : 1); ++e) p.w[e] = 0u;
-        return p;
-    }
-    static __device__ __forceinline__ Piece load(const V *row, int piece) {
+    static __device__ __forceinline__ Piece load(const V *row, int piece, bool ok) {
         Piece p;
         if constexpr (WIDE) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(row) + piece);
+            const uint4 x = ld16_if(reinterpret_cast<const uint4 *>(row) + piece, ok);
             p.w[0] = x.x; p.w[1] = x.y; p.w[2] = x.z; p.w[3] = x.w;
         } else if constexpr (sizeof(V) == 2) {
-            p.w[0] = (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(row) + piece);
+            p.w[0] = ld2_if(row + piece, ok);
         } else {
-            p.w[0] = __float_as_uint(__ldg(reinterpret_cast<const float *>(row) + piece));
+            p.w[0] = ld4_if(row + piece, ok);
         }
         return p;
     }
@@ -128,7 +123,7 @@ __device__ __forceinline__ void take(Sums<X> &a, const Args &g, const Row &r,
 #pragma unroll
             for (int p = 0; p < X::NP; ++p) {
                 const int pc = sub + p * X::LPR;
-                buf[u][p] = ok && pc < ppr ? X::load(vr, pc) : X::none();
+                buf[u][p] = X::load(vr, pc, ok && pc < ppr);
             }
         }
         if (u0 == 0) {                                  // the weights, once the rows are asked for
@@ -394,6 +389,14 @@ cudaError_t launch_cache_attend(const Prob &p, const Cache &c, const float *q, c
                                 float *rowsum, int32_t *idx, int32_t *status, cudaStream_t st) {
     const Args g{c, q, gamma, k_pages, order_idx, rowsum, idx, status,
                  p.N, p.H, p.dK, p.dV, p.k, p.C, p.bits, p.wk};
+    if (p.vdt == ZETA_BF16 && p.dV % 8 == 0 && p.dV <= 128 && p.dK <= 4 && c.n >= kTileRows) {
+        const TileArgs t{c, q, gamma, k_pages, static_cast<const __nv_bfloat16 *>(v_pages),
+                         order_codes, order_idx, static_cast<__nv_bfloat16 *>(out), rowsum, idx,
+                         status, p.N, p.H, p.dK, p.dV, p.k, p.C, p.bits, p.wk, p.code64};
+        // Sixteen rows a block until the rows fill the SMs 128 at a time.
+        const bool wide = p.S * c.n >= 152 * 128;
+        return p.dV <= 64 ? launch_cache_tile64(p, t, wide, st) : launch_cache_tile128(p, t, wide, st);
+    }
     if (p.vdt == ZETA_BF16) {
         if (p.code64)
             return dispatch_rows<uint64_t, __nv_bfloat16>(g, p, order_codes, v_pages, out, st);

@@ -31,6 +31,16 @@ __device__ __forceinline__ uint64_t dilate3(uint64_t x) {
     return x;
 }
 
+// The same for the low 10 bits, in 32-bit arithmetic.
+__device__ __forceinline__ uint32_t dilate3_10(uint32_t x) {
+    x &= 0x3ffu;
+    x = (x | (x << 16)) & 0x030000ffu;
+    x = (x | (x << 8)) & 0x0300f00fu;
+    x = (x | (x << 4)) & 0x030c30c3u;
+    x = (x | (x << 2)) & 0x09249249u;
+    return x;
+}
+
 // Spread the low 32 bits of x so that bit j moves to bit 2j.
 __device__ __forceinline__ uint64_t dilate2(uint64_t x) {
     x &= 0xffffffffull;
