@@ -367,8 +367,8 @@ zeta_status_t zeta_attend_bwd(const zeta_problem_t *p, const float *q, const flo
  *         read; one outside [0, pages) skips its tokens (ZETA_ERR_BOUNDS).
  *   k_pages        float [pages, H, page, d_K]
  *   v_pages        v_dtype [pages, H, page, d_V]  (16-B aligned)
- *   order_codes    code type [2, order_pages, H, page]
- *   order_idx      int32 [2, order_pages, H, page]
+ *   order_codes    code type [2, order_pages, H, page]  (16-B aligned)
+ *   order_idx      int32 [2, order_pages, H, page]  (16-B aligned)
  *   order_table    int32 [B, table_len]: entry e of prefix c of sequence b is row
  *         e % page of page order_table[b][e / page] in plane c % 2.  It may be
  *         page_table itself.  Sequences may share K/V pages (a common prompt), but

@@ -305,6 +305,7 @@ ZETA_API zeta_status_t zeta_cache_order(const zeta_problem_t *p, const zeta_cach
     if (empty(pr) || c.n == 0) return ZETA_OK;
     if (!start || !count || !page_table || !k_pages || !order_table || !order_codes || !order_idx)
         return ZETA_ERR_INVALID_ARG;
+    if (!aligned16(order_codes) || !aligned16(order_idx)) return ZETA_ERR_INVALID_ARG;
     c.start = start;
     c.count = count;
     c.ptab = page_table;

@@ -11,20 +11,26 @@
 //   the run's entry j with code z goes to j + #{old codes <= z}.
 // The call reads and writes the prefix once; nothing else moves with M.
 //
-// A block sorts the run of its (b, h) in shared memory (bitonic, the token's
-// place in the chunk packed below the code where both fit 64 bits), then takes
-// tiles of the old prefix: the tile's codes in shared memory, each old entry
-// placed by a binary search in the run, each run entry that falls into the tile
-// by a binary search in the tile.  Several blocks share a slice when there are
-// few slices; each sorts the run for itself, which costs less than a second
-// launch and a round trip of the run through memory.
+// A block sorts the run of its (b, h) in shared memory, the token's place in the
+// chunk packed below the code where both fit 64 bits: keys are dealt into buckets
+// by the codes' top bits and ranked inside their bucket; where a bucket is crowded
+// (equal or close codes) a bitonic sort takes over.  Its warps then stream the old
+// prefix, each a span of its own, 128 entries at a time (four consecutive ones a
+// lane) with the next ones on their way: the run entries that fall among them are
+// found from where the last ones ended, counted into the old entries' places (one
+// by one, or by binary search where there are many), and old and new go out
+// through a stage in shared memory, so that the stores are whole sectors.  Several
+// blocks share a slice when there are few slices; each sorts the run for itself,
+// which costs less than a second launch and a round trip of the run through memory.
 #include "cache.cuh"
 
 namespace zeta {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kTile = 1024;             // old entries per tile
+constexpr int kStep = 128;              // old entries a warp takes at a time
+constexpr int kFew = 8;                 // run entries among them up to which they go one by one
+constexpr int kCrowd = 48;              // keys of a bucket above which the bitonic sort runs
 constexpr int kLocBits = 13;            // a place in the chunk: C <= 8192
 
 // The run in shared memory: keys ordered by (code, place).  Packed: one word
@@ -33,19 +39,47 @@ template <bool PACK>
 struct Run {
     uint64_t *key;
     uint16_t *loc;
-    __device__ __forceinline__ bool after(int i, int j) const {   // entry i sorts after entry j
-        if constexpr (PACK) return key[i] > key[j];
-        else return key[i] > key[j] || (key[i] == key[j] && loc[i] > loc[j]);
-    }
-    __device__ __forceinline__ void swap(int i, int j) {
-        const uint64_t a = key[i];
-        key[i] = key[j];
-        key[j] = a;
-        if constexpr (!PACK) {
-            const uint16_t l = loc[i];
-            loc[i] = loc[j];
-            loc[j] = l;
+    // Compare-exchange of entries i < j, ascending if up.
+    __device__ __forceinline__ void order2(int i, int j, bool up) {
+        const uint64_t a = key[i], b = key[j];
+        if constexpr (PACK) {
+            if ((a > b) == up) {
+                key[i] = b;
+                key[j] = a;
+            }
+        } else {
+            const uint16_t la = loc[i], lb = loc[j];
+            if ((a > b || (a == b && la > lb)) == up) {
+                key[i] = b;
+                key[j] = a;
+                loc[i] = lb;
+                loc[j] = la;
+            }
         }
+    }
+    // The steps of stride 16 .. 1 of stages [from, to] (sizes) on 32 entries, one a lane.
+    __device__ __forceinline__ void order32(int base, int lane, int from, int to) {
+        const int i = base + lane;
+        uint64_t a = key[i];
+        unsigned la = 0;
+        if constexpr (!PACK) la = loc[i];
+        for (int size = from; size <= to; size <<= 1) {
+            for (int d = min(size >> 1, 16); d > 0; d >>= 1) {
+                const uint64_t b = __shfl_xor_sync(kFull, a, d);
+                const bool keep_min = ((i & size) == 0) == ((lane & d) == 0);
+                if constexpr (PACK) {
+                    if ((b < a) == keep_min) a = b;
+                } else {
+                    const unsigned lb = __shfl_xor_sync(kFull, la, d);
+                    if ((b < a || (b == a && lb < la)) == keep_min) {
+                        a = b;
+                        la = lb;
+                    }
+                }
+            }
+        }
+        key[i] = a;
+        if constexpr (!PACK) loc[i] = (uint16_t)la;
     }
     __device__ __forceinline__ void set(int i, uint64_t code, int place) {
         if constexpr (PACK) key[i] = (code << kLocBits) | (unsigned)place;
@@ -61,10 +95,9 @@ struct Run {
     __device__ __forceinline__ int place(int i) const {
         return PACK ? (int)(key[i] & ((1u << kLocBits) - 1)) : loc[i];
     }
-    // Entries with a code below z.
-    __device__ __forceinline__ int below(uint64_t z, int C) const {
+    // Entries with a code below z, known to be lo .. hi.
+    __device__ __forceinline__ int below(uint64_t z, int lo, int hi) const {
         const uint64_t x = PACK ? z << kLocBits : z;
-        int lo = 0, hi = C;
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (key[mid] < x) lo = mid + 1; else hi = mid;
@@ -73,25 +106,58 @@ struct Run {
     }
 };
 
+// Old entries in registers: four consecutive ones a lane.
+template <typename K>
+struct Old {
+    K z[4];
+    int token[4];
+    bool lost;
+};
+
+// One warp's output stage.
+template <typename K>
+struct Stage {
+    K z[kStep + 32];
+    int token[kStep + 32];
+};
+
 template <typename K, bool PACK>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 cache_order_kernel(Cache c, const float *__restrict__ k_pages, K *codes, int32_t *idx,
-                   int32_t *status, int N, int H, int dK, int bits, int C, int C2) {
+                   int32_t *status, int N, int H, int dK, int bits, int C, int C2, int NB) {
     extern __shared__ __align__(16) unsigned char raw[];
+    __shared__ int warp_sum[kThreads / 32];
     const int s = blockIdx.y, b = s / H, h = s - b * H;
     const Seq q = seq_of(c, b, N, status);
     const int c1 = (q.start + q.count) / C;               // the prefix to make
     if (c1 <= q.start / C) return;
     const int M = (c1 - 1) * C;
+    // The warps' spans of the old prefix; a block without any returns (the first
+    // block stays for an empty prefix).
+    constexpr int kWarps = kThreads / 32;
+    const int warps = (int)gridDim.x * kWarps;
+    const int span = ((M + warps - 1) / warps + kStep - 1) / kStep * kStep;
+    if (blockIdx.x > 0 && (int64_t)blockIdx.x * kWarps * span >= M) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Run<PACK> run;
     run.key = reinterpret_cast<uint64_t *>(raw);
-    K *tile = reinterpret_cast<K *>(run.key + C2);
-    run.loc = reinterpret_cast<uint16_t *>(tile + kTile + 1);
+    uint64_t *tmp = run.key + C2;                          // dealt keys; later the stages
+    int *cnt = reinterpret_cast<int *>(tmp + C2);          // buckets (NB + 1)
+    run.loc = reinterpret_cast<uint16_t *>(tmp);           // !PACK: no buckets
     const int32_t *ptab = c.ptab + (int64_t)b * c.tlen, *otab = c.otab + (int64_t)b * c.tlen;
-    const int tid = threadIdx.x;
+
+    const int64_t plane = (int64_t)c.opages * H << c.psh;
+    const K *src_z = codes + ((c1 - 1) & 1) * plane;
+    const int32_t *src_i = idx + ((c1 - 1) & 1) * plane;
+    K *dst_z = codes + (c1 & 1) * plane;
+    int32_t *dst_i = idx + (c1 & 1) * plane;
+    auto order_row = [&](int id, int e) { return row_in(id, e, h, H, c.psh, c.pmask, c.opages); };
 
     // ------------------------------------------------------------ the run ---
     bool bad = false;
+    const int sh = PACK ? max(0, dK * bits - (31 - __clz(NB))) + kLocBits : 0;
+    if constexpr (PACK)
+        for (int i = tid; i <= NB; i += kThreads) cnt[i] = 0;
     for (int j = tid; j < C2; j += kThreads) {
         if (j < C) {
             const int row = page_row(ptab, M + j, h, H, c.psh, c.pmask, c.pages);
@@ -107,97 +173,246 @@ cache_order_kernel(Cache c, const float *__restrict__ k_pages, K *codes, int32_t
         if (tid == 0) set_status(status, ZETA_ERR_BOUNDS);
         return;
     }
-    for (int size = 2; size <= C2; size <<= 1) {
-        for (int d = size >> 1; d > 0; d >>= 1) {
-            for (int p = tid; p < C2 / 2; p += kThreads) {
-                const int i = 2 * p - (p & (d - 1)), j = i + d;
-                const bool up = (i & size) == 0;
-                if (run.after(i, j) == up) run.swap(i, j);
+    bool crowded = true;
+    if constexpr (PACK) {
+        // Count, exclusive sums, deal; then each key's rank among its bucket's.
+        for (int j = tid; j < C; j += kThreads) atomicAdd(&cnt[run.key[j] >> sh], 1);
+        __syncthreads();
+        const int per = NB / kThreads;                     // NB is a multiple
+        int sum = 0, most = 0;
+        for (int i = 0; i < per; ++i) {
+            const int n = cnt[tid * per + i];
+            most = max(most, n);
+            sum += n;
+        }
+        int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) warp_sum[warp] = inc;
+        crowded = __syncthreads_or(most > kCrowd);
+        if (!crowded) {
+            int base = inc - sum;
+            for (int w = 0; w < warp; ++w) base += warp_sum[w];
+            for (int i = 0; i < per; ++i) {
+                const int n = cnt[tid * per + i];
+                cnt[tid * per + i] = base;
+                base += n;
             }
             __syncthreads();
+            // Dealing moves every bucket's start to its end, the next one's start.
+            for (int j = tid; j < C; j += kThreads) {
+                const uint64_t x = run.key[j];
+                tmp[atomicAdd(&cnt[x >> sh], 1)] = x;
+            }
+            __syncthreads();
+            for (int j = tid; j < C; j += kThreads) {
+                const uint64_t x = tmp[j];
+                const int bk = (int)(x >> sh), first = bk > 0 ? cnt[bk - 1] : 0, end = cnt[bk];
+                int r = first;
+                for (int i = first; i < end; ++i) r += tmp[i] < x;
+                run.key[r] = x;
+            }
         }
     }
+    if (crowded) {
+        for (int g = warp * 32; g < C2; g += kThreads) run.order32(g, lane, 2, 32);
+        for (int size = 64; size <= C2; size <<= 1) {
+            for (int d = size >> 1; d >= 32; d >>= 1) {
+                __syncthreads();
+                for (int p = tid; p < C2 / 2; p += kThreads) {
+                    const int i = 2 * p - (p & (d - 1));
+                    run.order2(i, i + d, (i & size) == 0);
+                }
+            }
+            __syncthreads();
+            for (int g = warp * 32; g < C2; g += kThreads) run.order32(g, lane, size, size);
+        }
+    }
+    __syncthreads();
 
     // ---------------------------------------------------------- the merge ---
-    const int64_t plane = (int64_t)c.opages * H << c.psh;
-    const K *src_z = codes + ((c1 - 1) & 1) * plane;
-    const int32_t *src_i = idx + ((c1 - 1) & 1) * plane;
-    K *dst_z = codes + (c1 & 1) * plane;
-    int32_t *dst_i = idx + (c1 & 1) * plane;
-    auto put = [&](int e, uint64_t z, int token) {
-        const int row = page_row(otab, e, h, H, c.psh, c.pmask, c.opages);
-        if (row < 0) {
-            set_status(status, ZETA_ERR_BOUNDS);
-            return;
+    bool lost = false;
+    auto put = [&](int id, int e, K z, int token) {        // entry e, id its page
+        const int row = order_row(id, e);
+        lost |= row < 0;
+        if (row >= 0) {
+            dst_z[row] = z;
+            dst_i[row] = token;
         }
-        dst_z[row] = (K)z;
-        dst_i[row] = token;
     };
-    if (M == 0) {
-        for (int j = blockIdx.x * kThreads + tid; j < C; j += gridDim.x * kThreads)
-            put(j, run.code(j), run.place(j));
-        return;
-    }
-    const int tiles = (M + kTile - 1) / kTile;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const int i0 = t * kTile, cnt = min(kTile, M - i0);
-        int token[kTile / kThreads];
+    if (M == 0)
+        for (int j = tid; j < C; j += kThreads)
+            put(page_id(otab, j, c.psh), j, (K)run.code(j), run.place(j));
+    const int i0 = (int)min((int64_t)(blockIdx.x * kWarps + warp) * span, (int64_t)M);
+    const int i1 = min(i0 + span, M);
+    Stage<K> &out = reinterpret_cast<Stage<K> *>(reinterpret_cast<unsigned char *>(tmp) +
+                                                 (PACK ? 0 : (size_t)C2 * 2))[warp];
+    // Pages of less than four entries are looked up entry by entry.
+    const bool quad = c.pmask >= 3;
+    struct Ids { int id[4]; };
+    auto ask = [&](int i) {                                // pages of the lane's entries
+        Ids a;
+        const int e = i + 4 * lane;
 #pragma unroll
-        for (int u = 0; u < kTile / kThreads; ++u) {
-            const int l = u * kThreads + tid;
-            token[u] = 0;
-            if (l < cnt) {
-                const int row = page_row(otab, i0 + l, h, H, c.psh, c.pmask, c.opages);
-                if (row < 0) set_status(status, ZETA_ERR_BOUNDS);
-                tile[l] = row < 0 ? K(0) : src_z[row];
-                token[u] = row < 0 ? 0 : src_i[row];
-            }
-        }
-        if (tid == 0 && i0 + cnt < M) {                    // the next tile's first code
-            const int row = page_row(otab, i0 + cnt, h, H, c.psh, c.pmask, c.opages);
-            tile[kTile] = row < 0 ? K(0) : src_z[row];
-        }
-        __syncthreads();
+        for (int k = 0; k < 4; ++k)
+            if (k == 0 || !quad) a.id[k] = page_id(otab, min(e + k, M - 1), c.psh);
+        return a;
+    };
+    auto fetch = [&](const Ids &a, int i) {                // the entries on those pages
+        Old<K> o;
+        o.lost = false;
+        const int e = i + 4 * lane;
 #pragma unroll
-        for (int u = 0; u < kTile / kThreads; ++u) {
-            const int l = u * kThreads + tid;
-            if (l < cnt) put(i0 + l + run.below(tile[l], C), tile[l], token[u]);
+        for (int k = 0; k < 4; ++k) {
+            o.z[k] = K(0);
+            o.token[k] = 0;
         }
-        const int ja = t == 0 ? 0 : run.below(tile[0], C);
-        const int jb = i0 + cnt < M ? run.below(tile[kTile], C) : C;
-        for (int j = ja + tid; j < jb; j += kThreads) {
-            const uint64_t z = run.code(j);
-            int lo = 0, hi = cnt;                          // old entries of the tile with code <= z
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if ((uint64_t)tile[mid] <= z) lo = mid + 1; else hi = mid;
+        if (quad && e + 3 < M) {
+            const int row = order_row(a.id[0], e);
+            o.lost = row < 0;
+            if (row >= 0) {
+                const int4 t = __ldg(reinterpret_cast<const int4 *>(src_i + row));
+                o.token[0] = t.x; o.token[1] = t.y; o.token[2] = t.z; o.token[3] = t.w;
+                if constexpr (sizeof(K) == 4) {
+                    const uint4 z = __ldg(reinterpret_cast<const uint4 *>(src_z + row));
+                    o.z[0] = z.x; o.z[1] = z.y; o.z[2] = z.z; o.z[3] = z.w;
+                } else {
+                    const ulonglong2 u = __ldg(reinterpret_cast<const ulonglong2 *>(src_z + row));
+                    const ulonglong2 v = __ldg(reinterpret_cast<const ulonglong2 *>(src_z + row) + 1);
+                    o.z[0] = u.x; o.z[1] = u.y; o.z[2] = v.x; o.z[3] = v.y;
+                }
             }
-            put(i0 + lo + j, z, M + run.place(j));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (e + k < M) {
+                    const int row = order_row(quad ? a.id[0] : a.id[k], e + k);
+                    o.lost |= row < 0;
+                    if (row >= 0) {
+                        o.z[k] = __ldg(src_z + row);
+                        o.token[k] = __ldg(src_i + row);
+                    }
+                }
         }
-        __syncthreads();
+        return o;
+    };
+    Old<K> cur, nxt;
+    Ids ids;
+    if (i0 < i1) {
+        const Ids first = ask(i0);
+        ids = ask(i0 + kStep);
+        cur = fetch(first, i0);
     }
+    // lo: run entries below the span's first code; those at the prefix's ends belong
+    // to its first and last entries.
+    int lo = 0;
+    if (i0 > 0 && i0 < i1) lo = run.below(__shfl_sync(kFull, (uint64_t)cur.z[0], 0), 0, C);
+    for (int i = i0; i < i1; i += kStep) {
+        nxt = fetch(ids, i + kStep);
+        ids = ask(i + 2 * kStep);
+        lost |= cur.lost;
+        const int e = i + 4 * lane, cnt = min(kStep, M - i), mine = min(4, M - e);
+        // hi: run entries below the next step's first code.
+        const bool last = i + kStep >= M;
+        const uint64_t run_z = lo + lane < C ? run.code(lo + lane) : ~0ull;
+        const uint64_t zn = __shfl_sync(kFull, (uint64_t)nxt.z[0], 0);
+        const unsigned in = __ballot_sync(kFull, lo + lane < C && (last || run_z < zn));
+        const int few = __popc(in);
+        int hi = lo + few;
+        if (few <= kFew) {                                 // one at a time, through the stage
+            int place[4] = {0, 0, 0, 0};
+            for (int j = 0; j < few; ++j) {
+                const uint64_t z = __shfl_sync(kFull, run_z, j);
+                int le = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const bool after = (uint64_t)cur.z[k] > z;
+                    place[k] += after;
+                    le += k < mine && !after;
+                }
+                le = __reduce_add_sync(kFull, le);
+                if (lane == j) {
+                    out.z[j + le] = (K)z;
+                    out.token[j + le] = M + run.place(lo + j);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < mine) {
+                    out.z[4 * lane + k + place[k]] = cur.z[k];
+                    out.token[4 * lane + k + place[k]] = cur.token[k];
+                }
+            __syncwarp();
+            const int total = cnt + few;
+            int pid[5];
+#pragma unroll
+            for (int u = 0; u < 5; ++u)
+                pid[u] = page_id(otab, min(i + lo + u * 32 + lane, M + C - 1), c.psh);
+#pragma unroll
+            for (int u = 0; u < 5; ++u) {
+                const int o = u * 32 + lane;
+                if (o < total) put(pid[u], i + lo + o, out.z[o], out.token[o]);
+            }
+            __syncwarp();
+        } else {                                           // many: by binary search
+            if (in == kFull) hi = last ? C : run.below(zn, lo, C);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < mine) {
+                    const int at = e + k + run.below((uint64_t)cur.z[k], lo, hi);
+                    put(page_id(otab, at, c.psh), at, cur.z[k], cur.token[k]);
+                    out.z[4 * lane + k] = cur.z[k];
+                }
+            __syncwarp();
+            for (int j = lo + lane; j < hi; j += 32) {
+                const uint64_t z = run.code(j);
+                int a = 0, n = cnt;                        // old entries of the step with code <= z
+                while (a < n) {
+                    const int mid = (a + n) >> 1;
+                    if ((uint64_t)out.z[mid] <= z) a = mid + 1; else n = mid;
+                }
+                put(page_id(otab, i + j + a, c.psh), i + j + a, (K)z, M + run.place(j));
+            }
+            __syncwarp();
+        }
+        lo = hi;
+        cur = nxt;
+    }
+    if (lost) set_status(status, ZETA_ERR_BOUNDS);
 }
 
 template <typename K, bool PACK>
 cudaError_t run_order(const Prob &p, const Cache &c, const float *k_pages, void *codes,
                       int32_t *idx, int32_t *status, cudaStream_t st) {
     static PerDeviceOnce once;
-    constexpr size_t kMost = (size_t)8192 * 10 + (kTile + 1) * sizeof(K) + 16;
-    cudaError_t e = once.run([] {
+    // Keys; then the dealt keys and their buckets, or the places (!PACK), and in the
+    // same space, after the sort, the warps' stages.
+    int C2 = 32, NB = kThreads;
+    while (C2 < p.C) C2 <<= 1;
+    while (NB < C2 && NB < 4096) NB <<= 1;
+    const size_t stages = sizeof(Stage<K>) * (kThreads / 32);
+    auto bytes = [&](size_t n, size_t nb) {
+        const size_t sort = PACK ? n * 8 + (nb + 1) * 4 : n * 2;
+        return n * 8 + (PACK ? (sort > stages ? sort : stages) : sort + stages);
+    };
+    const size_t smem = bytes(C2, NB), most_smem = bytes(8192, 4096);
+    cudaError_t e = once.run([&] {
         return cudaFuncSetAttribute(cache_order_kernel<K, PACK>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most_smem);
     });
     if (e != cudaSuccess) return e;
-    int C2 = 2;
-    while (C2 < p.C) C2 <<= 1;
-    const size_t smem = (size_t)C2 * (PACK ? 8 : 10) + (kTile + 1) * sizeof(K) + 16;
-    // Blocks per slice: enough for four on each of the 152 SMs, at most one per tile.
-    const int64_t tiles = (p.N + kTile - 1) / kTile;
-    int64_t g = (152 * 4 + p.S - 1) / p.S;
-    g = g < tiles ? g : tiles;
+    // Blocks per slice: enough for two on each of the 152 SMs (what fits at once); the
+    // kernel leaves out those that its prefix has no entries for.
+    int64_t g = (152 * 2 + p.S - 1) / p.S;
+    const int64_t most = p.N / (kStep * kThreads / 32) + 1;
+    g = g < most ? g : most;
     const dim3 grid((unsigned)(g < 1 ? 1 : g), (unsigned)p.S);
     cache_order_kernel<K, PACK><<<grid, kThreads, smem, st>>>(
-        c, k_pages, static_cast<K *>(codes), idx, status, p.N, p.H, p.dK, p.bits, p.C, C2);
+        c, k_pages, static_cast<K *>(codes), idx, status, p.N, p.H, p.dK, p.bits, p.C, C2,
+        NB);
     return cudaGetLastError();
 }
 

@@ -79,6 +79,10 @@ def test_null_and_unaligned_pointers(L):
         a = [FAKE] * 7
         a[pos] = odd
         assert L.zeta_cache_append(P, Q, *a, None, None) == 1
+    for pos in (5, 6):                     # order_codes, order_idx
+        a = [FAKE] * 7
+        a[pos] = odd
+        assert L.zeta_cache_order(P, Q, *a, None, None) == 1
     for pos in (6, 10):                    # v_pages, out
         a = [FAKE] * 13
         a[pos] = odd
