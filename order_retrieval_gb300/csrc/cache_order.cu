@@ -306,19 +306,21 @@ cache_order_kernel(Cache c, const float *__restrict__ k_pages, K *codes, int32_t
         ids = ask(i0 + kStep);
         cur = fetch(first, i0);
     }
-    // lo: run entries below the span's first code; those at the prefix's ends belong
-    // to its first and last entries.
+    // A step takes the run entries below its last code that no step before it took
+    // (the prefix's last step all that are left): lo .. hi.
     int lo = 0;
-    if (i0 > 0 && i0 < i1) lo = run.below(__shfl_sync(kFull, (uint64_t)cur.z[0], 0), 0, C);
+    if (i0 > 0 && i0 < i1) {
+        const int row = order_row(page_id(otab, i0 - 1, c.psh), i0 - 1);
+        lo = row >= 0 ? run.below((uint64_t)__ldg(src_z + row), 0, C) : 0;
+    }
     for (int i = i0; i < i1; i += kStep) {
         nxt = fetch(ids, i + kStep);
         ids = ask(i + 2 * kStep);
         lost |= cur.lost;
         const int e = i + 4 * lane, cnt = min(kStep, M - i), mine = min(4, M - e);
-        // hi: run entries below the next step's first code.
         const bool last = i + kStep >= M;
         const uint64_t run_z = lo + lane < C ? run.code(lo + lane) : ~0ull;
-        const uint64_t zn = __shfl_sync(kFull, (uint64_t)nxt.z[0], 0);
+        const uint64_t zn = __shfl_sync(kFull, (uint64_t)cur.z[3], 31);
         const unsigned in = __ballot_sync(kFull, lo + lane < C && (last || run_z < zn));
         const int few = __popc(in);
         int hi = lo + few;
