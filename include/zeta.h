@@ -355,8 +355,9 @@ zeta_status_t zeta_attend_bwd(const zeta_problem_t *p, const float *q, const flo
  *         everywhere; N is the longest sequence the cache holds (C | N).
  *   cc    n: rows of new tokens per sequence in q, k, v, out (1 <= n <= C);
  *         page: tokens per page, a power of two up to 65536;
- *         pages, order_pages: pages in the pools; table_len: row length of the
- *         page tables, table_len * page >= N.
+ *         pages, order_pages: pages in the pools (at least one each; append does
+ *         not look at order_pages); table_len: row length of the page tables,
+ *         table_len * page >= N.
  *   start, count   int32 [B] (device): tokens sequence b held before this call
  *         and tokens it brings (0 <= count <= n, start + count <= N).  Rows
  *         count[b] .. n-1 are padding: never read, and left as they were where

@@ -281,6 +281,7 @@ ZETA_API zeta_status_t zeta_cache_append(const zeta_problem_t *p, const zeta_cac
     zeta_status_t s = check_cache(p, cc, &pr, &c);
     if (s != ZETA_OK) return s;
     if (empty(pr) || c.n == 0) return ZETA_OK;
+    if (c.pages < 1) return ZETA_ERR_INVALID_ARG;
     if (!k || !v || !start || !count || !page_table || !k_pages || !v_pages)
         return ZETA_ERR_INVALID_ARG;
     if (!aligned16(v) || !aligned16(v_pages)) return ZETA_ERR_INVALID_ARG;
@@ -303,6 +304,7 @@ ZETA_API zeta_status_t zeta_cache_order(const zeta_problem_t *p, const zeta_cach
     zeta_status_t s = check_cache(p, cc, &pr, &c);
     if (s != ZETA_OK) return s;
     if (empty(pr) || c.n == 0) return ZETA_OK;
+    if (c.pages < 1 || c.opages < 1) return ZETA_ERR_INVALID_ARG;
     if (!start || !count || !page_table || !k_pages || !order_table || !order_codes || !order_idx)
         return ZETA_ERR_INVALID_ARG;
     if (!aligned16(order_codes) || !aligned16(order_idx)) return ZETA_ERR_INVALID_ARG;
@@ -328,6 +330,7 @@ ZETA_API zeta_status_t zeta_cache_attend(const zeta_problem_t *p, const zeta_cac
     zeta_status_t s = check_cache(p, cc, &pr, &c);
     if (s != ZETA_OK) return s;
     if (empty(pr) || c.n == 0) return ZETA_OK;
+    if (c.pages < 1 || c.opages < 1) return ZETA_ERR_INVALID_ARG;
     if (!q || !gamma || !start || !count || !page_table || !k_pages || !v_pages ||
         !order_table || !order_codes || !order_idx || !out || !rowsum)
         return ZETA_ERR_INVALID_ARG;

@@ -299,12 +299,12 @@ cache_order_kernel(Cache c, const float *__restrict__ k_pages, K *codes, int32_t
         }
         return o;
     };
-    Old<K> cur, nxt;
+    Old<K> one, two;
     Ids ids;
     if (i0 < i1) {
         const Ids first = ask(i0);
         ids = ask(i0 + kStep);
-        cur = fetch(first, i0);
+        one = fetch(first, i0);
     }
     // A step takes the run entries below its last code that no step before it took
     // (the prefix's last step all that are left): lo .. hi.
@@ -313,7 +313,9 @@ cache_order_kernel(Cache c, const float *__restrict__ k_pages, K *codes, int32_t
         const int row = order_row(page_id(otab, i0 - 1, c.psh), i0 - 1);
         lo = row >= 0 ? run.below((uint64_t)__ldg(src_z + row), 0, C) : 0;
     }
-    for (int i = i0; i < i1; i += kStep) {
+    // Two sets of registers in turn: copying the next entries would wait for them.
+    int i = i0;
+    auto turn = [&](const Old<K> &cur, Old<K> &nxt) {
         nxt = fetch(ids, i + kStep);
         ids = ask(i + 2 * kStep);
         lost |= cur.lost;
@@ -381,7 +383,12 @@ cache_order_kernel(Cache c, const float *__restrict__ k_pages, K *codes, int32_t
             __syncwarp();
         }
         lo = hi;
-        cur = nxt;
+        i += kStep;
+    };
+    while (i < i1) {
+        turn(one, two);
+        if (i >= i1) break;
+        turn(two, one);
     }
     if (lost) set_status(status, ZETA_ERR_BOUNDS);
 }

@@ -27,8 +27,7 @@
 //    whose result is not finite is taken again, key by key, without the others.
 #pragma once
 
-#include "cache.cuh"
-#include "mma.cuh"
+#include "cache_gather.cuh"
 
 namespace zeta {
 
@@ -88,10 +87,6 @@ struct TileSmem {
     int wst[TQ];                       // window start of query l
     int bad;                           // a key of the own chunk has no page
 };
-
-__device__ __forceinline__ float4 ld_key(const float *p, int dK) {
-    return make_float4(p[0], dK > 1 ? p[1] : 0.f, dK > 2 ? p[2] : 0.f, dK > 3 ? p[3] : 0.f);
-}
 
 __device__ __forceinline__ uint64_t order_code(const TileArgs &g, int64_t at) {
     return g.code64 ? __ldg(static_cast<const unsigned long long *>(g.order_codes) + at)
@@ -682,7 +677,7 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
         for (int u = 0; u < 2; ++u)
             id.u[u] = page_id(ptab, (unsigned)j.u[u] < (unsigned)cC ? j.u[u] : 0, g.c.psh);
     };
-    Two e0, e1, e2, e3, o1, j0, j1, j2, i1;
+    Two e0, e1, e2, e3, o1, j0, j1, i1;
     if (items > 0) {
         Two o0, o2;
         entries(0, e0);
@@ -699,13 +694,8 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
     int it = 0;
     for (int r = 0; r < (band ? 0 : QW); ++r) {
         const int l = wl0 + r;
-        float cacc[CB][4][4];                                // column 0 of the mma tiles
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) cacc[cb][m][e] = 0.f;
+        GatherSum<CB> sum;
+        sum.zero();
         float sw = 0.f, mrun = INFINITY;
         if (r < nqw) {
             const int t = sm.qrow[l];
@@ -727,92 +717,46 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
                     kk[u] = ld_key(g.k_pages + (int64_t)max(pcur[u], 0) * g.dK, g.dK);
-                const int nmt = min(4, (g.k - t0 + 15) >> 4);
-                float w[2];
+                gather64<CB>(sum, g.v_pages, g.dV, ppr, pcur, min(4, (g.k - t0 + 15) >> 4), lane, [&] {
+                    ask_page(j1, i1);
+                    j0 = j1;
+                    ask_tok(e2, o1, j1);                     // into j1: a copy would wait for it
+                    entries(it + 3, e3);
+                    ask_oid(e3, o1);
+                    e0 = e1;
+                    e1 = e2;
+                    e2 = e3;
+                    ++it;
 #pragma unroll
-                for (int cb = 0; cb < CB; ++cb) {
-                    uint4 buf[4][4];                         // rows g4, g4 + 8 of tile mt: pieces s4, s4 + 4
+                    for (int u = 0; u < 2; ++u) {
+                        const float kc[4] = {kk[u].x, kk[u].y, kk[u].z, kk[u].w};
+                        float d2 = 0.f;
 #pragma unroll
-                    for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                        for (int hh = 0; hh < 2; ++hh) {
-                            const int pr = __shfl_sync(kFull, pcur[mt >> 1], (16 * mt + 8 * hh + g4) & 31);
-                            const uint4 *vr = reinterpret_cast<const uint4 *>(
-                                g.v_pages + (int64_t)max(pr, 0) * g.dV);
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int pc = cb * 8 + s4 + 4 * e;
-                                buf[mt][2 * hh + e] = ld16_if(vr + pc, mt < nmt && pr >= 0 && pc < ppr);
-                            }
+                        for (int d = 0; d < DK; ++d) {
+                            const float e = qa[d] - kc[d];
+                            d2 = __fmaf_rn(e, e, d2);
                         }
-                    if (cb == 0) {
-                        ask_page(j1, i1);
-                        ask_tok(e2, o1, j2);
-                        entries(it + 3, e3);
-                        ask_oid(e3, o1);
-                        j0 = j1;
-                        j1 = j2;
-                        e0 = e1;
-                        e1 = e2;
-                        e2 = e3;
-                        ++it;
+                        d2v[u] = pcur[u] >= 0 ? d2 : INFINITY;
+                    }
+                    if constexpr (WK == kWSoftmax) {
+                        float pm = fminf(d2v[0], d2v[1]);
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const float kc[4] = {kk[u].x, kk[u].y, kk[u].z, kk[u].w};
-                            float d2 = 0.f;
-#pragma unroll
-                            for (int d = 0; d < DK; ++d) {
-                                const float e = qa[d] - kc[d];
-                                d2 = __fmaf_rn(e, e, d2);
-                            }
-                            d2v[u] = pcur[u] >= 0 ? d2 : INFINITY;
-                        }
-                        if constexpr (WK == kWSoftmax) {
-                            float pm = fminf(d2v[0], d2v[1]);
-#pragma unroll
-                            for (int o = 16; o > 0; o >>= 1)
-                                pm = fminf(pm, __shfl_xor_sync(kFull, pm, o));
-                            if (pm < mrun) {
-                                const float sc = mrun == INFINITY ? 0.f : __expf((pm - mrun) * inv_g2);
-#pragma unroll
-                                for (int c2 = 0; c2 < CB; ++c2)
-#pragma unroll
-                                    for (int m = 0; m < 4; ++m)
-#pragma unroll
-                                        for (int e = 0; e < 4; ++e) cacc[c2][m][e] *= sc;
-                                sw *= sc;
-                                mrun = pm;
-                            }
-                        }
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            w[u] = pcur[u] >= 0 ? weight_fast<WK>(d2v[u], mrun, inv_g2) : 0.f;
-                            sw += w[u];
+                        for (int o = 16; o > 0; o >>= 1) pm = fminf(pm, __shfl_xor_sync(kFull, pm, o));
+                        if (pm < mrun) {
+                            const float sc = mrun == INFINITY ? 0.f : __expf((pm - mrun) * inv_g2);
+                            sum.scale(sc);
+                            sw *= sc;
+                            mrun = pm;
                         }
                     }
+                    float w[2];
 #pragma unroll
-                    for (int mt = 0; mt < 4; ++mt) {
-                        if (mt < nmt) {
-                            const int sb = 16 * mt + 2 * s4;
-                            const float e0 = __shfl_sync(kFull, w[mt >> 1], sb & 31);
-                            const float e1 = __shfl_sync(kFull, w[mt >> 1], (sb + 1) & 31);
-                            const float e2 = __shfl_sync(kFull, w[mt >> 1], (sb + 8) & 31);
-                            const float e3 = __shfl_sync(kFull, w[mt >> 1], (sb + 9) & 31);
-                            const uint32_t ba = g4 == 0 ? pack_bf16(e0, e1) : 0u;
-                            const uint32_t bb = g4 == 0 ? pack_bf16(e2, e3) : 0u;
-                            const uint32_t a0[4] = {buf[mt][0].x, buf[mt][0].y, buf[mt][0].z, buf[mt][0].w};
-                            const uint32_t a1[4] = {buf[mt][1].x, buf[mt][1].y, buf[mt][1].z, buf[mt][1].w};
-                            const uint32_t b0[4] = {buf[mt][2].x, buf[mt][2].y, buf[mt][2].z, buf[mt][2].w};
-                            const uint32_t b1[4] = {buf[mt][3].x, buf[mt][3].y, buf[mt][3].z, buf[mt][3].w};
-#pragma unroll
-                            for (int m = 0; m < 4; ++m) {
-                                const uint32_t af[4] = {movmatrix_trans(a0[m]), movmatrix_trans(a1[m]),
-                                                        movmatrix_trans(b0[m]), movmatrix_trans(b1[m])};
-                                mma16816(cacc[cb][m], af, ba, bb);
-                            }
-                        }
+                    for (int u = 0; u < 2; ++u) {
+                        w[u] = pcur[u] >= 0 ? weight_fast<WK>(d2v[u], mrun, inv_g2) : 0.f;
+                        sw += w[u];
                     }
-                }
+                    return make_float2(w[0], w[1]);
+                });
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sw += __shfl_xor_sync(kFull, sw, o);
@@ -820,18 +764,7 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
             const int t = sm.qrow[l];
             for (int u = lane; u < g.k; u += 32) g.idx[(row0 + t) * g.k + u] = -1;
         }
-        // Lane 4m holds mma rows m and m + 8 of column 0: tile `mm`, block cb:
-        // dimension 64 cb + 8 (m / 2) + 2 mm + m % 2, and 32 more.
-        if (s4 == 0) {
-            const int d0 = 8 * (g4 >> 1) + (g4 & 1);
-#pragma unroll
-            for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    sm.win[l][64 * cb + d0 + 2 * m] = cacc[cb][m][0];
-                    sm.win[l][64 * cb + d0 + 2 * m + 32] = cacc[cb][m][2];
-                }
-        }
+        sum.each(lane, [&](int d, float x) { sm.win[l][d] = x; });
         if (lane == 0) {
             sm.swin[l] = sw;
             sm.mwin[l] = mrun;

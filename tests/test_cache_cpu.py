@@ -58,6 +58,11 @@ def test_unsupported_caches(L, pk, ck):
     assert _all(L, _prob(**pk), _cache(**ck)) == [2, 2, 2]
 
 
+def test_pools_without_pages(L):
+    assert _all(L, _prob(), _cache(pages=0)) == [1, 1, 1]
+    assert _all(L, _prob(), _cache(order_pages=0))[1:] == [1, 1]
+
+
 def test_invalid_problems(L):
     for kw in (dict(N=1000), dict(k=0), dict(k=129), dict(d_K=0)):
         assert _all(L, _prob(**kw), _cache()) == [1, 1, 1]
