@@ -365,7 +365,7 @@ zeta_status_t zeta_attend_bwd(const zeta_problem_t *p, const float *q, const flo
  *         ZETA_ERR_BOUNDS recorded.
  *   page_table     int32 [B, table_len]: token t of sequence b is row t % page of
  *         page page_table[b][t / page].  Only entries of tokens that exist are
- *         read; one outside [0, pages) skips its tokens (ZETA_ERR_BOUNDS).
+ *         looked at; one outside [0, pages) skips its tokens (ZETA_ERR_BOUNDS).
  *   k_pages        float [pages, H, page, d_K]
  *   v_pages        v_dtype [pages, H, page, d_V]  (16-B aligned)
  *   order_codes    code type [2, order_pages, H, page]  (16-B aligned)

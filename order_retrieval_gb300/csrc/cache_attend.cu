@@ -10,18 +10,19 @@
 // and values, contiguous within pages) and of k scattered rows, bound by HBM when
 // many tokens come at once and by the chain of dependent loads (rank search, window
 // entry, page, row) when few do:
-//  * Own chunk, in two phases per 1024 keys: a thread per key looks up its row and
-//    computes its weight into shared memory; then LPR threads per value row stream
-//    the rows, a 16-byte piece each, four pieces in flight per thread.  The first
-//    pieces are asked for before the weights are computed.
+//  * Own chunk, in two phases per 1024 keys: a thread per key computes its weight into
+//    shared memory; then warps stream the value rows, LPR lanes per row, two batches
+//    of four 16-byte pieces in flight per lane.  A warp's rows follow one another in their page, so a
+//    batch needs one address; its first batch is asked for before the weights.
 //  * Meanwhile one warp searches the rank (32 P probes a step instead of one), looks
-//    up the window's rows and weighs them; when it is done, all threads stream them.
+//    up the window's rows and weighs them; when it is done, all warps stream them.
 //    In a cluster the last block takes the window and the others the own chunk.
-//  * About 50 registers a thread leave five blocks on an SM, so that one block's
-//    search and joins hide behind the others' loads.  (A warp per row with its rows
-//    in flight through shared memory, summed on the tensor cores, needs a third of
-//    the instructions but waits for each of its steps alone: 90 to 100 us where this
-//    takes see below.)
+//  * Blocks of four warps and at most 64 registers, eight to an SM, so that one
+//    block's search and joins hide behind the others' loads.  (A warp per row with
+//    its rows in flight through shared memory, summed on the tensor cores, needs
+//    fewer instructions but waits for each of its steps alone: 100 us for 4,096 rows
+//    of 512 own keys.  Eight warps a block spend most of theirs on setting up and
+//    joining: 81 us.)
 //  * Sums of weights and of weighted values are held in float32 per thread and
 //    joined in a fixed order, in shared memory and across the cluster through
 //    distributed shared memory: no workspace, one launch, the same bits each run.
@@ -97,13 +98,13 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
-// Barrier of the first `n` threads' warps of the group that takes the own chunk.
+// Barrier of the first `n` threads, the warps that take the own chunk.
 __device__ __forceinline__ void bar_own(int n) { asm volatile("bar.sync 1, %0;\n" ::"r"(n) : "memory"); }
 
 // Entries of the prefix with a code <= z: a warp probes 32 P of them per step.
-template <typename K, int P>
-__device__ __forceinline__ int rank_of(const Args &g, const int32_t *otab, int h, const K *codes, K z,
-                                       int M, int lane) {
+template <typename K, int P, typename Page>
+__device__ __forceinline__ int rank_of(const Args &g, Page page, int h, const K *codes, K z, int M,
+                                       int lane) {
     int lo = 0, hi = M;
     while (lo < hi) {
         const int step = (hi - lo + 32 * P - 1) / (32 * P);
@@ -111,7 +112,7 @@ __device__ __forceinline__ int rank_of(const Args &g, const int32_t *otab, int h
         int row[P];
         K c[P];
 #pragma unroll
-        for (int p = 0; p < P; ++p) row[p] = page_id(otab, min(at(p), M - 1), g.c.psh);
+        for (int p = 0; p < P; ++p) row[p] = page(min(at(p), M - 1));
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             row[p] = row_in(row[p], at(p), h, g.H, g.c.psh, g.c.pmask, g.c.opages);
@@ -135,271 +136,332 @@ struct Total {
     float s, m;
 };
 
-// V: value type; LPR: threads per value row; NT: threads.
-template <typename K, typename V, bool WIDE, int LPR, int NT>
-__global__ void __launch_bounds__(NT, LPR <= 32 ? 1280 / NT : 1024 / NT)
+// V: value type; LPR lanes per value row, NP pieces per lane; LOW: d_K <= 4.
+template <typename K, typename V, bool WIDE, int LPR, int NP, bool LOW>
+__global__ void __launch_bounds__(128, 8)
 cache_rows_kernel(const __grid_constant__ Args g, const K *__restrict__ order_codes,
                   const V *__restrict__ v_pages, V *__restrict__ out, int cs, int ppr) {
     using P = Piece<V, WIDE>;
-    constexpr int U = 4, NA = (P::N + 1) / 2, NW = NT / 32;
+    constexpr int NT = 128, NW = NT / 32, NA = (P::N + 1) / 2, DM = LOW ? 4 : kMaxDK;
+    constexpr int RPI = 32 / LPR, U = NP >= 4 ? 1 : 4 / NP, BR = RPI * U;   // rows per load, batch
+    constexpr int UK = 2;                                        // keys a thread weighs at a time
     __shared__ float w_sh[kSeg];                                 // weights (softmax: distances) of a segment
-    __shared__ int row_sh[kSeg];
+    __shared__ int row_sh[kSeg];                                 // rows of long windows
     __shared__ float ww_sh[kWin];                                // the window's, prepared by the searching warp
     __shared__ int wr_sh[kWin];
-    __shared__ float part[NW][(LPR < 32 ? LPR : 32) * P::N];
+    __shared__ float part[NW][LPR * NP * P::N];
     __shared__ float red_s[NW], red_m[NW];
     __shared__ int st_sh;
     __shared__ Total tot;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const unsigned rid = blockIdx.x / (unsigned)cs;
-    const int cr = (int)(blockIdx.x - rid * (unsigned)cs);       // block in the cluster
-    const unsigned s = rid / (unsigned)g.c.n;
-    const int t = (int)(rid - s * (unsigned)g.c.n);
-    const int b = (int)(s / (unsigned)g.H), h = (int)(s - (unsigned)b * (unsigned)g.H);
-    float q[kMaxDK];
-    load_point(q, g.q + (int64_t)rid * g.dK, g.dK);
-    const float gm = g.gamma[h];
-    const Seq seq = seq_of(g.c, b, g.N, g.status);
-    if (t >= seq.count) return;                                  // the whole cluster returns
+    const int cr = cs == 1 ? 0 : (int)(blockIdx.x % (unsigned)cs);   // block in the cluster
+    const int t = cs == 1 ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)cs);
+    const int h = blockIdx.y, b = blockIdx.z;
+    const int64_t rid = ((int64_t)b * g.H + h) * g.c.n + t;
     const int32_t *ptab = g.c.ptab + (int64_t)b * g.c.tlen, *otab = g.c.otab + (int64_t)b * g.c.tlen;
+    auto ppage = [&](int j) { return page_id(ptab, j, g.c.psh); };
+    auto opage = [&](int e) { return page_id(otab, e, g.c.psh); };
+    const Seq seq = seq_of(g.c, b, g.N, g.status);
+    float q[DM];
+#pragma unroll
+    for (int d = 0; d < DM; ++d) q[d] = d < g.dK ? __ldg(g.q + rid * g.dK + d) : 0.f;
+    const float gm = __ldg(g.gamma + h);
+    if (t >= seq.count) return;                                  // the whole cluster returns
     const int i = seq.start + t, chunk = i / g.C, cC = chunk * g.C;
     const float inv_g2 = __frcp_rn(gm * gm);
     const int64_t plane = ((int64_t)g.c.opages * g.H << g.c.psh) * (chunk & 1);
     const bool window = chunk > 0, soft = g.wk == kWSoftmax;
     const bool win_here = window && cr == cs - 1;                // this block takes the window
     const bool searcher = win_here && warp == NW - 1;
-    // Own-chunk keys of this block: all of them, or an equal share of the cluster's
-    // blocks but the one with the window.
-    const int sharers = cs == 1 ? 1 : window ? cs - 1 : cs;
-    const int per = ((i - cC + sharers) / sharers + 31) & ~31;
-    const int k0 = cC + cr * per, k1 = cr < sharers ? min(k0 + per, i + 1) : k0;
+    // Own-chunk keys of this block: an equal share for each of the row's warps but the
+    // one that searches.
     const int own = win_here ? NT - 32 : NT;                     // threads on the own chunk
+    const int takers = cs * NW - (window ? 1 : 0);
+    const int per = cs == 1 ? i - cC + 1 : ((i - cC + takers) / takers * NW + 31) & ~31;
+    const int k0 = min(cC + cr * per, i + 1), k1 = cr == cs - 1 ? i + 1 : min(k0 + per, i + 1);
 
-    float2 acc[NA];
+    float2 acc[NP][NA];
 #pragma unroll
-    for (int e = 0; e < NA; ++e) acc[e] = make_float2(0.f, 0.f);
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int e = 0; e < NA; ++e) acc[p][e] = make_float2(0.f, 0.f);
     float sum = 0.f, m_own = INFINITY;
-    const int sub = tid % LPR, grp = tid / LPR;
-    auto row_of = [&](int id, int j) { return row_in(id, j, h, g.H, g.c.psh, g.c.pmask, g.c.pages); };
-    auto dist = [&](int row) {
-        float x[kMaxDK], d2 = 0.f;
-        load_point(x, g.k_pages + (int64_t)row * g.dK, g.dK);
+    auto rescale = [&](float f) {
+        sum *= f;
 #pragma unroll
-        for (int d = 0; d < kMaxDK; ++d) {
-            if (d < g.dK) {
-                const float e = q[d] - x[d];
-                d2 = __fmaf_rn(e, e, d2);
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+            for (int e = 0; e < NA; ++e) acc[p][e] = mul2(acc[p][e], dup2(f));
+    };
+    const int sub = lane % LPR, grp = lane / LPR;
+    auto row_of = [&](int id, int j) { return row_in(id, j, h, g.H, g.c.psh, g.c.pmask, g.c.pages); };
+    // Squared distances of UK rows (row 0 in the place of none), all asked for together.
+    auto dists = [&](const int (&row)[UK], float (&d2)[UK]) {
+        float x[UK][DM];
+#pragma unroll
+        for (int u = 0; u < UK; ++u) {
+            const float *kp = g.k_pages + (int64_t)max(row[u], 0) * g.dK;
+#pragma unroll
+            for (int d = 0; d < DM; ++d) x[u][d] = d < g.dK ? __ldg(kp + d) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < UK; ++u) {
+            d2[u] = 0.f;
+#pragma unroll
+            for (int d = 0; d < DM; ++d) {
+                const float e = q[d] - x[u][d];                  // both 0 beyond d_K
+                d2[u] = __fmaf_rn(e, e, d2[u]);
             }
         }
-        return d2;
     };
-    // Pool row of window entry `slot` (looked up through the order's and the keys' pages).
-    auto window_row = [&](int st, int slot, bool there) {
-        const int e = st + slot;
-        const int orow = row_in(page_id(otab, min(e, cC - 1), g.c.psh), e, h, g.H, g.c.psh, g.c.pmask, g.c.opages);
-        const int j = ldi_if(g.order_idx + plane + orow, there && orow >= 0);
-        const bool in = (unsigned)j < (unsigned)cC;
-        const int row = in ? row_of(page_id(ptab, j, g.c.psh), j) : -1;
-        if (there) {
-            if (row < 0) set_status(g.status, ZETA_ERR_BOUNDS);
-            if (g.idx) g.idx[(int64_t)rid * g.k + slot] = in ? j : -1;
-        }
-        return row;
-    };
-    // Stream n value rows (rows, weights in shared memory) with `groups` row groups; the
-    // first U of the thread's rows may already be on their way in buf.
-    auto stream = [&](const int *rows, const float *ws, int n, int groups, P (&buf)[U], bool have) {
-        if (grp >= groups) return;
-        for (int r0 = grp; r0 < n; r0 += U * groups) {
-            if (!have || r0 != grp) {
+    // Pool rows of UK window entries (looked up through the order's and the keys' pages).
+    auto window_rows = [&](int st, const int (&slot)[UK], int (&row)[UK]) {
+        int j[UK];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int r = r0 + u * groups, row = r < n ? rows[r] : -1;
-                    buf[u].load(v_pages + (int64_t)max(row, 0) * g.dV, sub, row >= 0 && sub < ppr);
-                }
+        for (int u = 0; u < UK; ++u) j[u] = opage(min(st + slot[u], cC - 1));
+#pragma unroll
+        for (int u = 0; u < UK; ++u) {
+            const int r = row_in(j[u], st + slot[u], h, g.H, g.c.psh, g.c.pmask, g.c.opages);
+            j[u] = ldi_if(g.order_idx + plane + r, slot[u] < g.k && r >= 0);
+        }
+#pragma unroll
+        for (int u = 0; u < UK; ++u) row[u] = ppage((unsigned)j[u] < (unsigned)cC ? j[u] : 0);
+#pragma unroll
+        for (int u = 0; u < UK; ++u) {
+            const bool in = (unsigned)j[u] < (unsigned)cC;
+            row[u] = in ? row_of(row[u], j[u]) : -1;
+            if (slot[u] < g.k) {
+                if (row[u] < 0) set_status(g.status, ZETA_ERR_BOUNDS);
+                if (g.idx) g.idx[rid * g.k + slot[u]] = in ? j[u] : -1;
+            }
+        }
+    };
+    P buf[U][NP], buf2[U][NP];
+    // Ask for the value rows of own keys j0 .. j0 + BR - 1 (below k1).
+    auto ask = [&](P (&buf)[U][NP], int j0) {
+        if (j0 + BR <= k1 && (j0 & g.c.pmask) + BR - 1 <= g.c.pmask) {   // one run in one page
+            const int row = row_of(ppage(j0), j0);
+            const V *src = v_pages + ((int64_t)max(row, 0) + grp) * g.dV;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+                    buf[u][p].load(src + u * RPI * g.dV, sub + p * LPR, row >= 0 && sub + p * LPR < ppr);
+        } else {
+            int row[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) row[u] = ppage(min(j0 + u * RPI + grp, i));
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int j = j0 + u * RPI + grp;
+                row[u] = j < k1 ? row_of(row[u], j) : -1;
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+                    buf[u][p].load(v_pages + (int64_t)max(row[u], 0) * g.dV, sub + p * LPR,
+                                   row[u] >= 0 && sub + p * LPR < ppr);
+            }
+        }
+    };
+    // Value rows rows[0 .. n) (weights ws) by every warp of the block, the rows spread
+    // over the warps.
+    auto stream = [&](const int *rows, const float *ws, int n) {
+        for (int r0 = warp * RPI + grp; r0 < n; r0 += NW * BR) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + u * NW * RPI, row = r < n ? rows[r] : -1;
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+                    buf[u][p].load(v_pages + (int64_t)max(row, 0) * g.dV, sub + p * LPR,
+                                   row >= 0 && sub + p * LPR < ppr);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int r = r0 + u * groups;
-                if (r < n) buf[u].add(acc, ws[r]);
+                const int r = r0 + u * NW * RPI;
+                const float w = r < n ? ws[r] : 0.f;
+#pragma unroll
+                for (int p = 0; p < NP; ++p) buf[u][p].add(acc[p], w);
             }
         }
     };
-    P buf[U];
+    // Weigh rows into ws (softmax: distances) and this thread's sum; the least distance.
+    auto weigh = [&](const int (&row)[UK], const float (&d2)[UK], int r0, int stride, int n, float *ws) {
+        float least = INFINITY;
+#pragma unroll
+        for (int u = 0; u < UK; ++u) {
+            const int r = r0 + u * stride;
+            if (r < n) {
+                const float x2 = row[u] >= 0 ? d2[u] : INFINITY;
+                const float w = row[u] >= 0 && !soft ? weight_rt(g.wk, x2, 0.f, inv_g2) : 0.f;
+                ws[r] = soft ? x2 : w;
+                sum += w;
+                least = fminf(least, x2);
+            }
+        }
+        return least;
+    };
+    // Softmax: distances ws[0 .. n) become weights on the shift m_own.
+    auto soften = [&](float *ws, int n, int threads) {
+        for (int r = tid; r < n; r += threads) {
+            const float w = ws[r] == INFINITY ? 0.f : weight_of<kWSoftmax>(ws[r], m_own, inv_g2);
+            ws[r] = w;
+            sum += w;
+        }
+    };
+    auto shift_down = [&](float least) {                         // the same value in all threads
+        if (least < m_own) {
+            rescale(m_own == INFINITY ? 0.f : expf((least - m_own) * inv_g2));
+            m_own = least;
+        }
+    };
 
     if (searcher) {
         float x[kMaxDK];
 #pragma unroll
-        for (int d = 0; d < kMaxDK; ++d) x[d] = q[d];
+        for (int d = 0; d < kMaxDK; ++d) x[d] = d < DM ? q[d < DM ? d : 0] : 0.f;
         const K z = (K)code_of(x, g.dK, g.bits);
-        const int rk = rank_of<K, 4>(g, otab, h, order_codes + plane, z, cC, lane);
+        // Many probes a step where latency counts; few where every probe's sector comes
+        // out of the HBM time of the others (256 probes: 124 MB more for 4,096 rows).
+        const int rk = cs > 1 || gridDim.z * gridDim.y * gridDim.x < 152 * 2
+                           ? rank_of<K, 8>(g, opage, h, order_codes + plane, z, cC, lane)
+                           : rank_of<K, 1>(g, opage, h, order_codes + plane, z, cC, lane);
         const int st = min(max(rk - (g.k + 1) / 2, 0), cC - g.k);
-        float wmin = INFINITY;
-        int row[2];
-        float d2[2];
+        int slot[UK];                                            // two a lane
 #pragma unroll
-        for (int u = 0; u < 2; ++u) row[u] = window_row(st, u * 32 + lane, u * 32 + lane < g.k);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) d2[u] = dist(max(row[u], 0));
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            wr_sh[u * 32 + lane] = row[u];
-            const float x2 = row[u] >= 0 ? d2[u] : INFINITY;
-            wmin = fminf(wmin, x2);
-            const float w = row[u] >= 0 && !soft ? weight_rt(g.wk, x2, 0.f, inv_g2) : 0.f;
-            sum += w;
-            ww_sh[u * 32 + lane] = soft ? x2 : w;
-        }
-        wmin = warp_min(wmin);
+        for (int u = 0; u < UK; ++u) slot[u] = u < 2 ? u * 32 + lane : g.k;
+        int row[UK];
+        float d2[UK];
+        window_rows(st, slot, row);
+        dists(row, d2);
+        wr_sh[lane] = row[0];
+        wr_sh[32 + lane] = row[1];
+        const float least = warp_min(weigh(row, d2, lane, 32, kWin, ww_sh));
         if (lane == 0) {
             st_sh = st;
-            red_m[NW - 1] = wmin;                                // the searcher's own slot
+            red_m[NW - 1] = least;
         }
-    } else if (cr < sharers) {
-        const int groups = own / LPR;
+    } else {
         for (int j0 = k0; j0 < k1; j0 += kSeg) {
             const int n = min(kSeg, k1 - j0);
-            // The first rows of this thread's pieces, then the weights.
-            if (grp < groups) {
-                int id[U];
+            const int step = own / 32 * BR, r1 = warp * BR;      // the warp's batches: r1, r1 + step, ...
+            if (r1 < n) ask(buf, j0 + r1);
+            if (r1 + step < n) ask(buf2, j0 + r1 + step);
+            float least = INFINITY;
+            for (int r0 = tid; r0 < n; r0 += UK * own) {
+                int row[UK];
+                float d2[UK];
 #pragma unroll
-                for (int u = 0; u < U; ++u) id[u] = page_id(ptab, min(j0 + grp + u * groups, i), g.c.psh);
+                for (int u = 0; u < UK; ++u) row[u] = ppage(min(j0 + r0 + u * own, i));
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int r = grp + u * groups, row = r < n ? row_of(id[u], j0 + r) : -1;
-                    buf[u].load(v_pages + (int64_t)max(row, 0) * g.dV, sub, row >= 0 && sub < ppr);
-                }
-            }
-            float dmin = INFINITY;
-            for (int r = tid; r < n; r += own) {
-                const int row = row_of(page_id(ptab, j0 + r, g.c.psh), j0 + r);
-                if (row < 0) set_status(g.status, ZETA_ERR_BOUNDS);
-                const float d2 = dist(max(row, 0));
-                const float x2 = row >= 0 ? d2 : INFINITY;
-                row_sh[r] = row;
-                if (soft) {
-                    w_sh[r] = x2;
-                    dmin = fminf(dmin, x2);
-                } else {
-                    const float w = row >= 0 ? weight_rt(g.wk, x2, 0.f, inv_g2) : 0.f;
-                    w_sh[r] = w;
-                    sum += w;
-                }
+                for (int u = 0; u < UK; ++u) row[u] = row_of(row[u], j0 + r0 + u * own);
+                dists(row, d2);
+#pragma unroll
+                for (int u = 0; u < UK; ++u)
+                    if (r0 + u * own < n && row[u] < 0) set_status(g.status, ZETA_ERR_BOUNDS);
+                least = fminf(least, weigh(row, d2, r0, own, n, w_sh));
             }
             if (soft) {                                          // onto the least distance so far
-                dmin = warp_min(dmin);
-                if (lane == 0) red_s[warp] = dmin;
+                least = warp_min(least);
+                if (lane == 0) red_s[warp] = least;
                 bar_own(own);
-                for (int w = 0; w < own / 32; ++w) dmin = fminf(dmin, red_s[w]);
-                if (dmin < m_own) {
-                    const float f = m_own == INFINITY ? 0.f : expf((dmin - m_own) * inv_g2);
-#pragma unroll
-                    for (int e = 0; e < NA; ++e) acc[e] = mul2(acc[e], dup2(f));
-                    sum *= f;
-                    m_own = dmin;
-                }
-                for (int r = tid; r < n; r += own) {
-                    const float w = row_sh[r] >= 0 ? weight_of<kWSoftmax>(w_sh[r], m_own, inv_g2) : 0.f;
-                    w_sh[r] = w;
-                    sum += w;
-                }
+                for (int w = 0; w < own / 32; ++w) least = fminf(least, red_s[w]);
+                shift_down(least);
+                soften(w_sh, n, own);
             }
             bar_own(own);
-            stream(row_sh, w_sh, n, groups, buf, true);
-            if (j0 + kSeg < k1) bar_own(own);                    // the arrays are free again
+            auto use = [&](P (&buf)[U][NP], int r0) {            // add a batch, ask for the one after the next
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int r = r0 + u * RPI + grp;
+                    const float w = r < n ? w_sh[r] : 0.f;
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) buf[u][p].add(acc[p], w);
+                }
+                if (r0 + 2 * step < n) ask(buf, j0 + r0 + 2 * step);
+            };
+            for (int r0 = r1; r0 < n; r0 += 2 * step) {
+                use(buf, r0);
+                if (r0 + step < n) use(buf2, r0 + step);
+            }
+            if (j0 + kSeg < k1) bar_own(own);                    // the array is free again
         }
     }
     if (!window && g.idx && cr == 0)
-        for (int slot = tid; slot < g.k; slot += NT) g.idx[(int64_t)rid * g.k + slot] = -1;
+        for (int slot = tid; slot < g.k; slot += NT) g.idx[rid * g.k + slot] = -1;
 
-    // The window, by all threads; for the softmax everything onto one shift.
+    // The window, by all warps; for the softmax everything onto one shift.
     if (win_here) {
         if (soft && lane == 0 && !searcher) red_m[warp] = m_own;
         __syncthreads();
         const int st = st_sh;
-        float m = m_own;
         if (soft) {
-            for (int w = 0; w < NW; ++w) m = fminf(m, red_m[w]);
-            if (tid < kWin) {
-                const float w = wr_sh[tid] >= 0 ? weight_of<kWSoftmax>(ww_sh[tid], m, inv_g2) : 0.f;
-                const float f = m_own == INFINITY ? 0.f : expf((m - m_own) * inv_g2);
-                sum = sum * f + w;
-                ww_sh[tid] = w;
-            } else if (m_own != INFINITY) {
-                sum *= expf((m - m_own) * inv_g2);
-            }
-            const float f = m_own == INFINITY ? 0.f : m_own == m ? 1.f : expf((m - m_own) * inv_g2);
-#pragma unroll
-            for (int e = 0; e < NA; ++e) acc[e] = mul2(acc[e], dup2(f));
-            m_own = m;
+            float least = INFINITY;
+            for (int w = 0; w < NW; ++w) least = fminf(least, red_m[w]);
+            shift_down(least);
+            soften(ww_sh, min(kWin, g.k), NT);
             __syncthreads();
         }
-        stream(wr_sh, ww_sh, min(kWin, g.k), NT / LPR, buf, false);
+        stream(wr_sh, ww_sh, min(kWin, g.k));
         for (int t0 = kWin; t0 < g.k; t0 += kSeg) {              // windows of more entries
             const int n = min(kSeg, g.k - t0);
-            float dmin = INFINITY;
+            float least = INFINITY;
             __syncthreads();
-            for (int r = tid; r < n; r += NT) {
-                const int row = window_row(st, t0 + r, true);
-                const float d2 = dist(max(row, 0)), x2 = row >= 0 ? d2 : INFINITY;
-                row_sh[r] = row;
-                dmin = fminf(dmin, x2);
-                const float w = row >= 0 && !soft ? weight_rt(g.wk, x2, 0.f, inv_g2) : 0.f;
-                w_sh[r] = soft ? x2 : w;
-                sum += w;
+            for (int r0 = tid; r0 < n; r0 += UK * NT) {
+                int slot[UK], row[UK];
+                float d2[UK];
+#pragma unroll
+                for (int u = 0; u < UK; ++u) slot[u] = r0 + u * NT < n ? t0 + r0 + u * NT : g.k;
+                window_rows(st, slot, row);
+                dists(row, d2);
+#pragma unroll
+                for (int u = 0; u < UK; ++u)
+                    if (r0 + u * NT < n) row_sh[r0 + u * NT] = row[u];
+                least = fminf(least, weigh(row, d2, r0, NT, n, w_sh));
             }
             if (soft) {
-                dmin = warp_min(dmin);
-                if (lane == 0) red_m[warp] = dmin;
+                least = warp_min(least);
+                if (lane == 0) red_m[warp] = least;
                 __syncthreads();
-                for (int w = 0; w < NW; ++w) dmin = fminf(dmin, red_m[w]);
-                if (dmin < m_own) {
-                    const float f = m_own == INFINITY ? 0.f : expf((dmin - m_own) * inv_g2);
-#pragma unroll
-                    for (int e = 0; e < NA; ++e) acc[e] = mul2(acc[e], dup2(f));
-                    sum *= f;
-                    m_own = dmin;
-                }
-                for (int r = tid; r < n; r += NT) {
-                    const float w = row_sh[r] >= 0 ? weight_of<kWSoftmax>(w_sh[r], m_own, inv_g2) : 0.f;
-                    w_sh[r] = w;
-                    sum += w;
-                }
+                for (int w = 0; w < NW; ++w) least = fminf(least, red_m[w]);
+                shift_down(least);
+                soften(w_sh, n, NT);
             }
             __syncthreads();
-            stream(row_sh, w_sh, n, NT / LPR, buf, false);
+            stream(row_sh, w_sh, n);
         }
     }
 
-    // Join the threads of a column, the warps, the blocks.
+    // Join the lanes of a column, the warps, the blocks.
     sum = warp_sum(sum);
-    if constexpr (LPR < 32) {
 #pragma unroll
-        for (int o = 16; o >= LPR; o >>= 1)
+    for (int o = 16; o >= LPR; o >>= 1)
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
 #pragma unroll
             for (int e = 0; e < NA; ++e) {
-                acc[e].x += __shfl_xor_sync(kFull, acc[e].x, o);
-                acc[e].y += __shfl_xor_sync(kFull, acc[e].y, o);
+                acc[p][e].x += __shfl_xor_sync(kFull, acc[p][e].x, o);
+                if (P::N > 1) acc[p][e].y += __shfl_xor_sync(kFull, acc[p][e].y, o);
             }
-    }
-    if (LPR >= 32 || lane < LPR) {
+    if (lane < LPR) {
 #pragma unroll
-        for (int e = 0; e < P::N; ++e) part[warp][(lane % (LPR < 32 ? LPR : 32)) * P::N + e] = e & 1 ? acc[e / 2].y : acc[e / 2].x;
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+            for (int e = 0; e < P::N; ++e)
+                part[warp][(lane + p * LPR) * P::N + e] = e & 1 ? acc[p][e / 2].y : acc[p][e / 2].x;
     }
     __syncthreads();                                             // red_s may still be read above
     if (lane == 0) red_s[warp] = sum;
     __syncthreads();
     float total = 0.f;
+#pragma unroll
     for (int w = 0; w < NW; ++w) total += red_s[w];
-    constexpr int WPR = LPR <= 32 ? 1 : LPR / 32;                // warps that share a row
     auto column = [&](int d) {
         float o = 0.f;
-        const int piece = d / P::N, at = (piece % 32) * P::N + d % P::N;
-        for (int w = piece / 32; w < NW; w += WPR) o += part[w][LPR <= 32 ? d : at];
+#pragma unroll
+        for (int w = 0; w < NW; ++w) o += part[w][d];
         return o;
     };
     if (cs == 1) {
-        for (int d = tid; d < g.dV; d += NT) VT<V>::st(out + (int64_t)rid * g.dV + d, __fdiv_rn(column(d), total));
+        for (int d = tid; d < g.dV; d += NT) VT<V>::st(out + rid * g.dV + d, __fdiv_rn(column(d), total));
         if (tid == 0) g.rowsum[rid] = total;
         return;
     }
@@ -429,25 +491,25 @@ cache_rows_kernel(const __grid_constant__ Args g, const K *__restrict__ order_co
 #pragma unroll
             for (int p = 0; p < 8; ++p)
                 if (p < cs) o = __fmaf_rn(f[p], cl.map_shared_rank(&tot, p)->acc[d], o);
-            VT<V>::st(out + (int64_t)rid * g.dV + d, __fdiv_rn(o, ssum));
+            VT<V>::st(out + rid * g.dV + d, __fdiv_rn(o, ssum));
         }
         if (tid == 0) g.rowsum[rid] = ssum;
     }
     cl.sync();                                                   // read before any block ends
 }
 
-template <typename K, typename V, bool WIDE, int LPR, int NT = 256>
+template <typename K, typename V, bool WIDE, int LPR, int NP>
 cudaError_t run_rows(const Args &g, const Prob &p, const void *order_codes, const void *v_pages,
                      void *out, int ppr, cudaStream_t st) {
     const int64_t rows = p.S * g.c.n;
-    // Blocks per token: split where the tokens alone leave SMs idle, as far as the own
-    // chunk has a key per thread, beside the block of the window.
-    const int most = p.C <= NT ? 2 : p.C <= 3 * NT ? 4 : 8;
+    // Blocks per token: split where the tokens alone leave SMs idle and the own chunk
+    // has work for more than four warps (a cluster's joins cost 1.3 us).
+    const int most = p.C <= 256 ? 1 : p.C <= 512 ? 2 : p.C <= 1024 ? 4 : 8;
     int cs = 1;
-    while (cs < most && rows * cs * 2 <= 152 * 4) cs *= 2;
+    while (cs < most && rows * cs * 2 <= 152 * 8) cs *= 2;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(rows * cs));
-    cfg.blockDim = dim3(NT);
+    cfg.gridDim = dim3((unsigned)(g.c.n * cs), (unsigned)p.H, (unsigned)p.B);
+    cfg.blockDim = dim3(128);
     cfg.stream = st;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
@@ -455,10 +517,12 @@ cudaError_t run_rows(const Args &g, const Prob &p, const void *order_codes, cons
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = cs > 1 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, cache_rows_kernel<K, V, WIDE, LPR, NT>, g,
-                                             static_cast<const K *>(order_codes),
-                                             static_cast<const V *>(v_pages),
-                                             static_cast<V *>(out), cs, ppr);
+    const K *oc = static_cast<const K *>(order_codes);
+    const V *vp = static_cast<const V *>(v_pages);
+    V *o = static_cast<V *>(out);
+    const cudaError_t e =
+        p.dK <= 4 ? cudaLaunchKernelEx(&cfg, cache_rows_kernel<K, V, WIDE, LPR, NP, true>, g, oc, vp, o, cs, ppr)
+                  : cudaLaunchKernelEx(&cfg, cache_rows_kernel<K, V, WIDE, LPR, NP, false>, g, oc, vp, o, cs, ppr);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -468,16 +532,14 @@ cudaError_t dispatch_rows(const Args &g, const Prob &p, const void *order_codes,
     const int bytes = p.dV * (int)sizeof(V);
     const bool wide = bytes % 16 == 0;
     const int ppr = wide ? bytes / 16 : p.dV;
-#define ZETA_ROWS(WIDE, LPR) run_rows<K, V, WIDE, LPR>(g, p, order_codes, v_pages, out, ppr, st)
-    if (!wide && ppr <= 32) return ZETA_ROWS(false, 32);
-    if (!wide && ppr <= 64) return ZETA_ROWS(false, 64);
-    if (!wide)                     // 512 threads: a row group beside the searching warp
-        return run_rows<K, V, false, 256, 512>(g, p, order_codes, v_pages, out, ppr, st);
-    if (ppr <= 4) return ZETA_ROWS(true, 4);
-    if (ppr <= 8) return ZETA_ROWS(true, 8);
-    if (ppr <= 16) return ZETA_ROWS(true, 16);
-    if (ppr <= 32) return ZETA_ROWS(true, 32);
-    return ZETA_ROWS(true, 64);
+#define ZETA_ROWS(WIDE, LPR, NP) run_rows<K, V, WIDE, LPR, NP>(g, p, order_codes, v_pages, out, ppr, st)
+    if (!wide) return ppr <= 64 ? ZETA_ROWS(false, 32, 2) : ZETA_ROWS(false, 32, 8);
+    if (ppr <= 4) return ZETA_ROWS(true, 4, 1);
+    if (ppr <= 8) return ZETA_ROWS(true, 8, 1);
+    if (ppr <= 16) return ZETA_ROWS(true, 16, 1);
+    if (ppr <= 32) return ZETA_ROWS(true, 32, 1);
+    if constexpr (sizeof(V) == 4) return ZETA_ROWS(true, 32, 2);
+    return cudaErrorInvalidValue;      // bf16 rows have at most 32 pieces
 #undef ZETA_ROWS
 }
 
