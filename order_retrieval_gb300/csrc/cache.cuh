@@ -83,6 +83,10 @@ __device__ __forceinline__ void load_point(float (&x)[kMaxDK], const float *p, i
     for (int d = 0; d < kMaxDK; ++d) x[d] = d < dK ? p[d] : 0.f;
 }
 
+__device__ __forceinline__ float4 ld_key(const float *p, int dK) {
+    return make_float4(p[0], dK > 1 ? p[1] : 0.f, dK > 2 ? p[2] : 0.f, dK > 3 ? p[3] : 0.f);
+}
+
 // 16 bytes through the read-only path, zeros where `ok` is false: one predicated
 // load.  (Written as a branch, the loads of a row's pieces wait for one another:
 // 7 us per gathered row instead of one memory latency.)

@@ -35,7 +35,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kTileRows = 4;           // rows of a call from which the tile kernel runs
 constexpr int kSeg = 1024;             // keys weighed at a time
 constexpr int kWin = 64;               // window entries that the searching warp prepares
 
@@ -551,12 +550,19 @@ cudaError_t launch_cache_attend(const Prob &p, const Cache &c, const float *q, c
                                 float *rowsum, int32_t *idx, int32_t *status, cudaStream_t st) {
     const Args g{c, q, gamma, k_pages, order_idx, rowsum, idx, status,
                  p.N, p.H, p.dK, p.dV, p.k, p.C, p.bits, p.wk};
-    if (p.vdt == ZETA_BF16 && p.dV % 8 == 0 && p.dV <= 128 && p.dK <= 4 && c.n >= kTileRows) {
+    // Many rows per sequence share their own chunk's tiles.  Measured against the row
+    // kernel, which reads the own chunk once per row: 8 sequences of 16 rows (C 1024) 24
+    // against 16 us, of 64 rows 23 against 38; 64 of 8 rows 50 against 49, of 16 rows 59
+    // against 82; C 256, 64 of 16 rows 40 against 41.
+    const bool tile = c.n >= 8 && p.S * c.n * p.C > (int64_t)1 << 21;
+    if (tile && p.vdt == ZETA_BF16 && p.dV % 8 == 0 && p.dV <= 128 && p.dK <= 4) {
         const TileArgs t{c, q, gamma, k_pages, static_cast<const __nv_bfloat16 *>(v_pages),
                          order_codes, order_idx, static_cast<__nv_bfloat16 *>(out), rowsum, idx,
                          status, p.N, p.H, p.dK, p.dV, p.k, p.C, p.bits, p.wk, p.code64};
-        // Sixteen rows a block until the rows fill the SMs 128 at a time.
-        const bool wide = p.S * c.n >= 152 * 128;
+        // Sixteen rows a block; 128 where long pieces fill the SMs that way and have the
+        // rows to be dealt by code (8 pieces of 1024: 115 against 152 us, 2 of them 58
+        // against 43; 32 of 256 228 against 194).
+        const bool wide = p.S * c.n >= 152 * 128 && c.n >= 512;
         return p.dV <= 64 ? launch_cache_tile64(p, t, wide, st) : launch_cache_tile128(p, t, wide, st);
     }
     if (p.vdt == ZETA_BF16) {

@@ -8,26 +8,27 @@
 //    block's entries with one coalesced read of up to 64.
 //  * Own chunk: key tiles staged by cp.async through the page table into
 //    swizzled shared memory; weights are built straight in mma A fragments and
-//    rounded to bf16 once, products accumulate in float32, row sums come from the
-//    unrounded weights.  NW / WM warps split each tile's keys and join at the end.
-//  * Window, rows that have little in common (GATHER): a warp takes one row at a
-//    time; 64 gathered value rows are in flight, four lanes per row, and the
-//    weighted sum V^T w runs on the tensor cores (8x8 blocks transposed in
-//    registers, w in column 0 of B).
+//    rounded to bf16 once, two keys of a row to an instruction (the coordinates are
+//    staged apart, so that a pair of keys is one operand); products accumulate in
+//    float32, row sums come from the unrounded weights.  NW / WM warps split each tile's keys and join at the end.
+//  * Window, rows that have little in common: a warp takes two rows at a time; their
+//    entries are looked up and weighed a lane each (four in flight), then the value
+//    rows are streamed and summed on the FMA pipes.
 //  * Window, many rows per prefix entry (BAND): the up to 1024 rows of a piece are
 //    dealt to the warps in the order of their codes (a counting sort on the codes'
 //    top ten bits), so that the 16 windows of a warp overlap.  The warp walks the
-//    prefix positions that any of them covers, 16 at a time through a ring of
-//    cp.async stages, as an mma tile whose weights are masked to each row's
-//    window: a value row is read once for all rows that take it, and no row pays
-//    for its own gather.  The own chunk then takes the block's rows in the order
-//    of their positions, so that a warp stops at its last row's causal limit.
+//    prefix positions that any of them covers, 32 at a time through two cp.async
+//    stages, as an mma tile whose weights are masked to each row's window: a value
+//    row is read once for all rows that take it, and no row pays for its own gather.
+//    The own chunk then takes the block's rows in the order of their positions, so
+//    that a warp stops at its last row's causal limit.
 //    Dealing changes no row's arithmetic.
 //  * A masked weight of zero times a value that is not finite would be NaN: a row
 //    whose result is not finite is taken again, key by key, without the others.
 #pragma once
 
-#include "cache_gather.cuh"
+#include "cache.cuh"
+#include "mma.cuh"
 
 namespace zeta {
 
@@ -50,7 +51,7 @@ namespace {
 
 constexpr int kSortRows = 1024, kBuckets = 1024;
 constexpr int kFences = 1024;
-constexpr int kRing = 4;               // stages of 16 prefix entries per warp
+constexpr int kRing = 2;               // stages of 32 prefix entries per warp
 constexpr int kBandRatio = 40;         // prefix entries per row below which rows are dealt
 
 template <int DVP, int WM, int NW>
@@ -60,24 +61,33 @@ struct TileSmem {
     static constexpr bool BAND = WM == NW;
     struct Own {
         __nv_bfloat16 v[3][TK * DVP];  // 16-byte chunk c of row r at c ^ (r & 7)
-        float4 kt[3][TK];
+        float k[3][4][TK];             // coordinates apart
     };
     struct Band {
-        __nv_bfloat16 v[NW][kRing][16 * DVP];
-        float4 kt[NW][kRing][16];
+        __nv_bfloat16 v[NW][kRing][32 * DVP];
+        float k[NW][kRing][4][32];
     };
     struct Deal {
         int cnt[kBuckets];
         int cuts[2][kSortRows / 32];
         int scan[NW];
+        unsigned bits[kSortRows / 32]; // the block's rows
+    };
+    struct Gather {                    // a warp's two rows
+        float w[NW][2][64];
+        int row[NW][2][64];
     };
     union {
         Own own;
         Band band[BAND ? 1 : 0];
         Deal deal;
-        uint64_t fence[kFences];
+        uint64_t fence_in[BAND ? kFences : 0];
+        Gather gather_in[BAND ? 1 : 0];
         float join[WM * (NW / WM - 1) * 16 * (DVP + 4) + 1];
     };
+    // Beside the tiles where there is room, so that the first ones arrive meanwhile.
+    uint64_t fence_by[BAND ? 0 : kFences];
+    Gather gather_by[BAND ? 0 : 1];
     float win[TQ][DVP + 4];            // window sums
     int rows[4][TK];                   // pool rows of the tile's keys, -1: none
     float swin[TQ], mwin[TQ];
@@ -86,7 +96,24 @@ struct TileSmem {
     int perm[TQ];                      // query of own-chunk row r (by position)
     int wst[TQ];                       // window start of query l
     int bad;                           // a key of the own chunk has no page
+    int top;                           // the block's last row
 };
+
+// Weights of two keys (the reciprocals by the approximate instructions, 1 ulp).
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <int WK>
+__device__ __forceinline__ float2 weight_pair(float2 d2, float m, float2 ig2) {
+    if constexpr (WK == kWCauchy) {
+        const float2 t = fma2(d2, ig2, dup2(1.0f));
+        return make_float2(rcp_approx(t.x), rcp_approx(t.y));
+    } else {
+        return weight_fast2<WK>(d2, dup2(m), ig2);
+    }
+}
 
 __device__ __forceinline__ uint64_t order_code(const TileArgs &g, int64_t at) {
     return g.code64 ? __ldg(static_cast<const unsigned long long *>(g.order_codes) + at)
@@ -150,7 +177,6 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
     constexpr int TQ = Sm::TQ, TK = Sm::TK, KS = NW / WM;    // KS warps share a row group's keys
     constexpr int kTileThreads = NW * 32;
     constexpr int QW = TQ / NW;                              // window rows per warp
-    constexpr int CB = DVP / 64;                             // 64-column blocks
     constexpr int NT = DVP / 8;
     extern __shared__ __align__(16) unsigned char raw[];
     Sm &sm = *reinterpret_cast<Sm *>(raw);
@@ -194,6 +220,7 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
     const bool deal = band && bn > nq;
     if (deal) {
         int *cnt = sm.deal.cnt;
+        if (tid < kSortRows / 32) sm.deal.bits[tid] = 0u;
         for (int i = tid; i < kBuckets; i += kTileThreads) cnt[i] = 0;
         __syncthreads();
         const int sh = max(0, g.dK * g.bits - 10);
@@ -259,7 +286,10 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
                     }
                 }
                 const int p = cnt[bk] + place - lo;
-                if (p >= 0 && p < nq) sm.qrow[p] = p0 + blk + l;
+                if (p >= 0 && p < nq) {
+                    sm.qrow[p] = p0 + blk + l;
+                    atomicOr(&sm.deal.bits[l >> 5], 1u << (l & 31));
+                }
             }
         }
     } else if (tid < nq) {
@@ -268,17 +298,68 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
     if (tid == 0) sm.bad = 0;
     __syncthreads();
     if (tid < TQ) {                                          // order by position
-        if (tid < nq) {
-            int r = tid;
-            if (deal) {
-                const int t = sm.qrow[tid];
-                r = 0;
-                for (int j = 0; j < nq; ++j) r += sm.qrow[j] < t;
-            }
-            sm.perm[r] = tid;
-        } else {
-            sm.perm[tid] = -1;
+        int r = tid;
+        if (deal && tid < nq) {
+            const int l = sm.qrow[tid] - p0 - blk;
+            r = __popc(sm.deal.bits[l >> 5] & ((1u << (l & 31)) - 1u));
+            for (int w = 0; w < l >> 5; ++w) r += __popc(sm.deal.bits[w]);
         }
+        sm.perm[r] = tid < nq ? tid : -1;
+        if (tid < nq && r == nq - 1) sm.top = sm.qrow[tid];
+    }
+    __syncthreads();
+    // Own-chunk tiles: keys cC .. last row's position (they all exist).
+    const int kend = seq.start + sm.top + 1 - cC;            // keys of the chunk that matter
+    const int nkt = (kend + TK - 1) / TK;
+    auto ask_rows = [&](int kt) {                            // page of the thread's key of tile kt
+        return tid < TK && kt * TK + tid < kend ? page_id(ptab, cC + kt * TK + tid, g.c.psh) : -1;
+    };
+    auto put_rows = [&](int kt, int id) {                    // its pool row, for every thread to see
+        if (tid < TK && kt < nkt) {
+            const int row = pool_row(id, cC + kt * TK + tid);
+            if (row < 0 && kt * TK + tid < kend) {
+                set_status(g.status, ZETA_ERR_BOUNDS);
+                sm.bad = 1;
+            }
+            sm.rows[kt & 3][tid] = row;
+        }
+    };
+    const int ppr = g.dV >> 3;                               // 16-byte pieces per value row
+    auto load_tile = [&](int kt) {                           // into stage kt % 3, asynchronously
+        if (kt < nkt) {
+            const int bf = kt % 3;
+            const int *rows = sm.rows[kt & 3];
+#pragma unroll
+            for (int i = 0; i < TK * (DVP / 8) / kTileThreads; ++i) {
+                const int id = i * kTileThreads + tid;
+                const int row = id / (DVP / 8), ch = id % (DVP / 8);
+                if (ch < ppr) {
+                    const int pr = rows[row];
+                    cp_async16(smem_u32(&sm.own.v[bf][row * DVP + ((ch ^ (row & 7)) * 8)]),
+                               g.v_pages + (int64_t)max(pr, 0) * g.dV + ch * 8, pr >= 0 ? 16 : 0);
+                }
+            }
+            for (int id = tid; id < TK * DK; id += kTileThreads) {
+                const int d = id / TK, row = id % TK;
+                const int pr = rows[row];
+                const bool ok = pr >= 0 && d < g.dK;
+                cp_async4(smem_u32(&sm.own.k[bf][d][row]),
+                          g.k_pages + (ok ? (int64_t)pr * g.dK + d : 0), ok ? 4 : 0);
+            }
+        }
+        cp_async_commit();
+    };
+    int kid = ask_rows(3);
+    {
+        const int i0 = ask_rows(0), i1 = ask_rows(1), i2 = ask_rows(2);
+        put_rows(0, i0);
+        put_rows(1, i1);
+        put_rows(2, i2);
+    }
+    if constexpr (!BAND) {
+        __syncthreads();
+        load_tile(0);
+        load_tile(1);
     }
 
     // ------------------------------------------------------ window part ---
@@ -286,7 +367,7 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
     const int wl0 = warp * QW, nqw = chunk > 0 ? max(0, min(QW, nq - wl0)) : 0;
     int wst = 0;                                             // lane r < nqw: start of row wl0 + r
     if (chunk > 0) {
-        uint64_t *fence = sm.fence;
+        uint64_t *fence = BAND ? sm.fence_in : sm.fence_by;
         int fsh = 5;
         while ((cC >> fsh) >= kFences) ++fsh;
         const int nf = (cC + (1 << fsh) - 1) >> fsh;
@@ -375,20 +456,23 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
         __syncthreads();                                     // fences read before the tiles arrive
     }
     // Weights in A fragments and products of KN steps of 16 keys: lane (g4, s4) has
-    // rows g4 (qab .x) and g4 + 8 (.y) of its group and keys 2 s4, +1, +8, +9 of a
-    // step; mask(key, x, none) puts `none` where a row does not take the key.
+    // rows g4 (a) and g4 + 8 (b) of its group and the key pairs 2 s4, +1 and +8, +9 of
+    // a step; mask(a or b, key, pair, none) puts `none` where the row does not take a
+    // key.  Ks: [4][stride] coordinates.
     const int tig = s4;
     const float2 ig2 = dup2(inv_g2);
     const int nc = (g.dV + 15) >> 4;                         // 16-column pairs in use
-    float2 qab[DK], sab, mab;
+    float2 qa[DK], qb[DK];                                   // each coordinate twice
+    float2 sa2, sb2;                                         // row sums, over the first and second keys of the pairs
+    float ma, mb;                                            // softmax shifts
     float acc[NT][4];
     auto clear = [&] {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
-        sab = make_float2(0.f, 0.f);
-        mab = make_float2(INFINITY, INFINITY);
+        sa2 = sb2 = make_float2(0.f, 0.f);
+        ma = mb = INFINITY;
     };
     auto take_rows = [&](int ta, int tb) {                   // the call's rows, -1: none
         const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -396,39 +480,43 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
         const float4 c = tb >= 0 ? ld_key(qs + (int64_t)tb * g.dK, g.dK) : z;
         const float av[4] = {a.x, a.y, a.z, a.w}, cv[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-        for (int d = 0; d < DK; ++d) qab[d] = make_float2(av[d], cv[d]);
+        for (int d = 0; d < DK; ++d) {
+            qa[d] = dup2(av[d]);
+            qb[d] = dup2(cv[d]);
+        }
     };
-    auto d2ab = [&](const float4 *Ks, int kl) {
-        const float4 kv = Ks[kl];
-        const float kc[4] = {kv.x, kv.y, kv.z, kv.w};
-        float2 d2 = make_float2(0.f, 0.f);
+    auto dist_pair = [&](const float *Ks, int stride, int kl, float2 &da, float2 &db) {
+        da = db = make_float2(0.f, 0.f);
 #pragma unroll
         for (int d = 0; d < DK; ++d) {
-            const float2 e = sub2(qab[d], dup2(kc[d]));
-            d2 = fma2(e, e, d2);
+            const float2 kc = *reinterpret_cast<const float2 *>(Ks + d * stride + kl);
+            const float2 ea = sub2(qa[d], kc), eb = sub2(qb[d], kc);
+            da = fma2(ea, ea, da);
+            db = fma2(eb, eb, db);
         }
-        return d2;
     };
-    auto steps = [&](auto kn, const float4 *Ks, const __nv_bfloat16 *Vs, int kb0, auto mask) {
+    auto steps = [&](auto kn, const float *Ks, int stride, const __nv_bfloat16 *Vs, int kb0, auto mask) {
         constexpr int KN = decltype(kn)::value;
-        if constexpr (WK == kWSoftmax) {                     // move the shift to the least d2
-            float2 tm = make_float2(INFINITY, INFINITY);
+        if constexpr (WK == kWSoftmax) {                     // move the shifts to the least d2
+            float la = INFINITY, lb = INFINITY;
 #pragma unroll
-            for (int ks = 0; ks < KN; ++ks)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int kl = kb0 + ks * 16 + 2 * tig + (e & 1) + (e >> 1) * 8;
-                    const float2 d2 = mask(kl, d2ab(Ks, kl), INFINITY);
-                    tm = make_float2(fminf(tm.x, d2.x), fminf(tm.y, d2.y));
-                }
+            for (int e = 0; e < 2 * KN; ++e) {
+                const int kl = kb0 + e * 8 + 2 * tig;
+                float2 da, db;
+                dist_pair(Ks, stride, kl, da, db);
+                da = mask(std::false_type{}, kl, da, INFINITY);
+                db = mask(std::true_type{}, kl, db, INFINITY);
+                la = fminf(la, fminf(da.x, da.y));
+                lb = fminf(lb, fminf(db.x, db.y));
+            }
 #pragma unroll
             for (int o = 1; o <= 2; o <<= 1) {
-                tm.x = fminf(tm.x, __shfl_xor_sync(kFull, tm.x, o));
-                tm.y = fminf(tm.y, __shfl_xor_sync(kFull, tm.y, o));
+                la = fminf(la, __shfl_xor_sync(kFull, la, o));
+                lb = fminf(lb, __shfl_xor_sync(kFull, lb, o));
             }
-            const float2 mn = make_float2(fminf(mab.x, tm.x), fminf(mab.y, tm.y));
-            const float fa = mn.x == mab.x ? 1.f : mab.x == INFINITY ? 0.f : __expf((mn.x - mab.x) * inv_g2);
-            const float fb = mn.y == mab.y ? 1.f : mab.y == INFINITY ? 0.f : __expf((mn.y - mab.y) * inv_g2);
+            const float na = fminf(ma, la), nb = fminf(mb, lb);
+            const float fa = na == ma ? 1.f : ma == INFINITY ? 0.f : __expf((na - ma) * inv_g2);
+            const float fb = nb == mb ? 1.f : mb == INFINITY ? 0.f : __expf((nb - mb) * inv_g2);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 acc[nt][0] *= fa;
@@ -436,27 +524,30 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
                 acc[nt][2] *= fb;
                 acc[nt][3] *= fb;
             }
-            sab = mul2(sab, make_float2(fa, fb));
-            mab = mn;
+            sa2 = mul2(sa2, dup2(fa));
+            sb2 = mul2(sb2, dup2(fb));
+            ma = na;
+            mb = nb;
         }
-        float2 sh = mab;                                     // finite even where no key is taken yet
-        if constexpr (WK == kWSoftmax)
-            sh = make_float2(mab.x == INFINITY ? 0.f : mab.x, mab.y == INFINITY ? 0.f : mab.y);
+        // Finite even where no key is taken yet.
+        const float xa = ma == INFINITY ? 0.f : ma, xb = mb == INFINITY ? 0.f : mb;
         const uint32_t vbase = smem_u32(Vs);
 #pragma unroll
         for (int ks = 0; ks < KN; ++ks) {
             const int kb = kb0 + ks * 16;
-            float wv[8];
+            uint32_t a[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int kl = kb + 2 * tig + (e & 1) + (e >> 1) * 8;
-                const float2 w = mask(kl, weight_fast2<WK>(d2ab(Ks, kl), sh, ig2), 0.f);
-                wv[e] = w.x;
-                wv[4 + e] = w.y;
-                sab = add2(sab, w);
+            for (int e = 0; e < 2; ++e) {
+                const int kl = kb + e * 8 + 2 * tig;
+                float2 da, db;
+                dist_pair(Ks, stride, kl, da, db);
+                const float2 wa = mask(std::false_type{}, kl, weight_pair<WK>(da, xa, ig2), 0.f);
+                const float2 wb = mask(std::true_type{}, kl, weight_pair<WK>(db, xb, ig2), 0.f);
+                sa2 = add2(sa2, wa);
+                sb2 = add2(sb2, wb);
+                a[2 * e] = pack_bf16(wa.x, wa.y);
+                a[2 * e + 1] = pack_bf16(wb.x, wb.y);
             }
-            const uint32_t a[4] = {pack_bf16(wv[0], wv[1]), pack_bf16(wv[4], wv[5]),
-                                   pack_bf16(wv[2], wv[3]), pack_bf16(wv[6], wv[7])};
             const int m = lane >> 3, key = kb + (m & 1) * 8 + (lane & 7);
 #pragma unroll
             for (int n2 = 0; n2 < NT / 2; ++n2) {
@@ -469,7 +560,6 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
             }
         }
     };
-    const int ppr = g.dV >> 3;                               // 16-byte pieces per value row
 
     if constexpr (BAND) if (band) {
         // ------------------------------------ windows walked together ------
@@ -483,22 +573,19 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
             const int c = p < cC && lane < nqw && wst + g.k > p ? max(wst, p) : none;
             return __reduce_min_sync(kFull, c);
         };
-        const int l16 = lane & 15;
-        auto entry = [&](int bp) { return min(bp == none ? 0 : bp + l16, cC - 1); };   // lane's entry of a block
+        auto entry = [&](int bp) { return min(bp == none ? 0 : bp + lane, cC - 1); };   // lane's entry of a block
         auto &ring = sm.band[0];
         auto copy = [&](int stage, int row) {                // an entry without a row: infinitely far
             const float *kp = g.k_pages + (int64_t)max(row, 0) * g.dK;
-            if (lane < 16) {
-                float *kd = reinterpret_cast<float *>(&ring.kt[warp][stage][lane]);
 #pragma unroll
-                for (int d = 0; d < DK; ++d) {
-                    if (row < 0) kd[d] = INFINITY;
-                    else if (d < g.dK) cp_async4(smem_u32(kd + d), kp + d, 4);
-                    else kd[d] = 0.f;
-                }
+            for (int d = 0; d < DK; ++d) {
+                float *kd = &ring.k[warp][stage][d][lane];
+                if (row < 0) *kd = INFINITY;
+                else if (d < g.dK) cp_async4(smem_u32(kd), kp + d, 4);
+                else *kd = 0.f;
             }
 #pragma unroll
-            for (int i = 0; i < DVP / 16; ++i) {
+            for (int i = 0; i < DVP / 8; ++i) {
                 const int id = i * 32 + lane, r = id / (DVP / 8), ch = id % (DVP / 8);
                 const int pr = __shfl_sync(kFull, row, r);
                 if (ch < ppr)
@@ -507,16 +594,6 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
             }
             cp_async_commit();
         };
-        // Block i is walked while blocks i+1, i+2 arrive and i+3 is asked for; the
-        // pages of the tokens of i+4, the tokens of i+5 and the pages of the entries of
-        // i+6 are on their way, each looked at one turn later.
-        int bp[7];
-        bp[0] = next(0);
-#pragma unroll
-        for (int i = 1; i < 7; ++i) bp[i] = bp[i - 1] == none ? none : next(bp[i - 1] + 16);
-        int oid[7], tok[6], tid_[5];
-#pragma unroll
-        for (int i = 0; i < 7; ++i) oid[i] = page_id(otab, entry(bp[i]), g.c.psh);
         bool lost = false;
         auto ask_tok = [&](int id, int block) {              // the token of the lane's entry
             const int row = order_row(id, entry(block));
@@ -525,39 +602,52 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
         };
         auto ask_page = [&](int j) { return page_id(ptab, (unsigned)j < (unsigned)cC ? j : 0, g.c.psh); };
         auto got_row = [&](int id, int j, int block) {       // -1: no entry, or dropped
-            if (block == none || block + l16 >= cC) return -1;
+            if (block == none || block + lane >= cC) return -1;
             const int row = (unsigned)j < (unsigned)cC ? pool_row(id, j) : -1;
             lost |= row < 0;
             return row;
         };
+        // Block i is walked while block i+1 arrives; the pages of the tokens of i+2, the
+        // tokens of i+3 and the pages of the entries of i+4 are on their way, each looked
+        // at one turn later.
+        int bp[5];
+        bp[0] = next(0);
 #pragma unroll
-        for (int i = 0; i < 6; ++i) tok[i] = ask_tok(oid[i], bp[i]);
-#pragma unroll
-        for (int i = 0; i < 5; ++i) tid_[i] = ask_page(tok[i]);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) copy(i, got_row(tid_[i], tok[i], bp[i]));
-        int id3 = tid_[3], j3 = tok[3], id4 = tid_[4], j4 = tok[4], j5 = tok[5], o6 = oid[6];
+        for (int i = 1; i < 5; ++i) bp[i] = bp[i - 1] == none ? none : next(bp[i - 1] + 32);
+        int row1, id2, j2, j3, o4;
+        {
+            const int a0 = page_id(otab, entry(bp[0]), g.c.psh), a1 = page_id(otab, entry(bp[1]), g.c.psh);
+            const int a2 = page_id(otab, entry(bp[2]), g.c.psh), a3 = page_id(otab, entry(bp[3]), g.c.psh);
+            o4 = page_id(otab, entry(bp[4]), g.c.psh);
+            const int t0 = ask_tok(a0, bp[0]), t1 = ask_tok(a1, bp[1]);
+            j2 = ask_tok(a2, bp[2]);
+            j3 = ask_tok(a3, bp[3]);
+            const int i0 = ask_page(t0), i1 = ask_page(t1);
+            id2 = ask_page(j2);
+            copy(0, got_row(i0, t0, bp[0]));
+            row1 = got_row(i1, t1, bp[1]);
+        }
         for (int i = 0; bp[0] != none; ++i) {
-            const int row = got_row(id3, j3, bp[3]);
-            cp_async_wait<2>();
-            __syncwarp();                                    // block i is here, i - 1 used up
-            copy((i + 3) & 3, row);
-            const int nb = bp[6] == none ? none : next(bp[6] + 16);
-            id3 = id4;
-            j3 = j4;
-            id4 = ask_page(j5);
-            j4 = j5;
-            j5 = ask_tok(o6, bp[6]);
-            o6 = page_id(otab, entry(nb), g.c.psh);
+            copy((i + 1) & 1, row1);
+            row1 = got_row(id2, j2, bp[2]);
+            const int nb = bp[4] == none ? none : next(bp[4] + 32);
+            j2 = j3;
+            id2 = ask_page(j3);
+            j3 = ask_tok(o4, bp[4]);
+            o4 = page_id(otab, entry(nb), g.c.psh);
+            cp_async_wait<1>();
+            __syncwarp();                                    // block i is here
             const int base = bp[0];
-            steps(std::integral_constant<int, 1>{}, ring.kt[warp][i & 3], ring.v[warp][i & 3], 0,
-                  [&](int kl, float2 x, float no) {
-                      return make_float2((unsigned)(base + kl - sta) < (unsigned)g.k ? x.x : no,
-                                         (unsigned)(base + kl - stb) < (unsigned)g.k ? x.y : no);
+            steps(std::integral_constant<int, 2>{}, &ring.k[warp][i & 1][0][0], 32, ring.v[warp][i & 1], 0,
+                  [&](auto second_row, int kl, float2 x, float no) {
+                      const int from = base + kl - (decltype(second_row)::value ? stb : sta);
+                      return make_float2((unsigned)from < (unsigned)g.k ? x.x : no,
+                                         (unsigned)(from + 1) < (unsigned)g.k ? x.y : no);
                   });
+            __syncwarp();                                    // its stage may be filled again
 #pragma unroll
-            for (int e = 0; e < 6; ++e) bp[e] = bp[e + 1];
-            bp[6] = nb;
+            for (int e = 0; e < 4; ++e) bp[e] = bp[e + 1];
+            bp[4] = nb;
         }
         if (lost) set_status(g.status, ZETA_ERR_BOUNDS);
         cp_async_wait<0>();
@@ -577,7 +667,7 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
                 *reinterpret_cast<float2 *>(&sm.win[wl0 + g4][nt * 8 + 2 * tig]) = make_float2(acc[nt][0], acc[nt][1]);
                 *reinterpret_cast<float2 *>(&sm.win[wl0 + g4 + 8][nt * 8 + 2 * tig]) = make_float2(acc[nt][2], acc[nt][3]);
             }
-        float sa = sab.x, sb = sab.y;
+        float sa = sa2.x + sa2.y, sb = sb2.x + sb2.y;
 #pragma unroll
         for (int o = 1; o <= 2; o <<= 1) {
             sa += __shfl_xor_sync(kFull, sa, o);
@@ -586,192 +676,197 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
         if (tig == 0) {
             sm.swin[wl0 + g4] = sa;
             sm.swin[wl0 + g4 + 8] = sb;
-            sm.mwin[wl0 + g4] = mab.x;
-            sm.mwin[wl0 + g4 + 8] = mab.y;
+            sm.mwin[wl0 + g4] = ma;
+            sm.mwin[wl0 + g4 + 8] = mb;
         }
         __syncthreads();                                     // the ring's space goes to the tiles
     }
 
-    // Own-chunk tiles: keys cC .. last row's position (they all exist).
-    int tmax = 0;
-    for (int l = 0; l < nq; ++l) tmax = max(tmax, sm.qrow[l]);
-    const int kend = seq.start + tmax + 1 - cC;              // keys of the chunk that matter
-    const int nkt = (kend + TK - 1) / TK;
-    auto ask_rows = [&](int kt) {                            // page of the thread's key of tile kt
-        return tid < TK && kt * TK + tid < kend ? page_id(ptab, cC + kt * TK + tid, g.c.psh) : -1;
-    };
-    auto put_rows = [&](int kt, int id) {                    // its pool row, for every thread to see
-        if (tid < TK && kt < nkt) {
-            const int row = pool_row(id, cC + kt * TK + tid);
-            if (row < 0 && kt * TK + tid < kend) {
-                set_status(g.status, ZETA_ERR_BOUNDS);
-                sm.bad = 1;
-            }
-            sm.rows[kt & 3][tid] = row;
-        }
-    };
-    auto load_tile = [&](int kt) {                           // into stage kt % 3, asynchronously
-        if (kt < nkt) {
-            const int bf = kt % 3;
-            const int *rows = sm.rows[kt & 3];
-#pragma unroll
-            for (int i = 0; i < TK * (DVP / 8) / kTileThreads; ++i) {
-                const int id = i * kTileThreads + tid;
-                const int row = id / (DVP / 8), ch = id % (DVP / 8);
-                if (ch < ppr) {
-                    const int pr = rows[row];
-                    cp_async16(smem_u32(&sm.own.v[bf][row * DVP + ((ch ^ (row & 7)) * 8)]),
-                               g.v_pages + (int64_t)max(pr, 0) * g.dV + ch * 8, pr >= 0 ? 16 : 0);
+    if (!band) {
+        // ---------------------------------------- windows row by row --------
+        typename Sm::Gather &ga = BAND ? sm.gather_in[0] : sm.gather_by[0];
+        constexpr int LPR = DVP / 8, RPI = 32 / LPR;         // lanes per value row, rows per load
+        const int grp = lane / LPR, sub = lane % LPR;
+        bool lost = false;
+        // Items of two rows and up to 64 of their entries.  Entries are looked up in four
+        // dependent steps (page of the entry, token, page of the token, key); those of the
+        // next item run between the four batches of value rows of this one.
+        const int np64 = (g.k + 63) >> 6, items = (nqw + 1) / 2 * np64;
+        int it = -1, r0 = -2, t0 = 0;                        // the item being looked up
+        int t[2] = {0, 0}, st[2], j[4], row[4];
+        float q[2][DK], x[4][DK];
+        auto slot = [&](int v) { return t0 + (v & 1) * 32 + lane; };
+        auto there = [&](int v) { return it < items && r0 + (v >> 1) < nqw && slot(v) < g.k; };
+        auto look = [&](int step) {
+            if (step == 0) {
+                ++it;
+                t0 += 64;
+                if (t0 >= g.k || r0 < 0) {
+                    t0 = 0;
+                    r0 += 2;
                 }
-            }
-            for (int id = tid; id < TK * DK; id += kTileThreads) {
-                const int row = id / DK, d = id - row * DK;
-                const int pr = rows[row];
-                const bool ok = pr >= 0 && d < g.dK;
-                cp_async4(smem_u32(reinterpret_cast<float *>(&sm.own.kt[bf][row]) + d),
-                          g.k_pages + (ok ? (int64_t)pr * g.dK + d : 0), ok ? 4 : 0);
-            }
-        }
-        cp_async_commit();
-    };
-    int kid = ask_rows(3);
-    {
-        const int i0 = ask_rows(0), i1_ = ask_rows(1), i2 = ask_rows(2);
-        put_rows(0, i0);
-        put_rows(1, i1_);
-        put_rows(2, i2);
-    }
-    __syncthreads();
-    load_tile(0);
-    load_tile(1);
-
-    // Window entries come in passes of up to 64 (item it: pass it % np64 of row
-    // it / np64).  While pass i is weighted, the pages of the tokens of i+1, the
-    // tokens of i+2 and the pages of the entries of i+3 are on their way, each looked
-    // at one turn later.
-    const int np64 = (g.k + 63) >> 6, items = band ? 0 : nqw * np64;
-    bool lost = false;
-    struct Two { int u[2]; };
-    auto entries = [&](int it, Two &e) {                     // the lane's two entries, -1: none
-        const int r = it / np64, t0 = (it - r * np64) << 6;
-        const int st = __shfl_sync(kFull, wst, r);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int t = t0 + u * 32 + lane;
-            e.u[u] = it < items && t < g.k ? st + t : -1;
-        }
-    };
-    auto ask_oid = [&](const Two &e, Two &id) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) id.u[u] = page_id(otab, max(e.u[u], 0), g.c.psh);
-    };
-    auto ask_tok = [&](const Two &e, const Two &id, Two &j) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int row = order_row(id.u[u], max(e.u[u], 0));
-            j.u[u] = ldi_if(g.order_idx + plane + row, row >= 0);
-        }
-    };
-    auto ask_page = [&](const Two &j, Two &id) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-            id.u[u] = page_id(ptab, (unsigned)j.u[u] < (unsigned)cC ? j.u[u] : 0, g.c.psh);
-    };
-    Two e0, e1, e2, e3, o1, j0, j1, i1;
-    if (items > 0) {
-        Two o0, o2;
-        entries(0, e0);
-        entries(1, e1);
-        entries(2, e2);
-        ask_oid(e0, o0);
-        ask_oid(e1, o1);
-        ask_oid(e2, o2);
-        ask_tok(e0, o0, j0);
-        ask_tok(e1, o1, j1);
-        ask_page(j0, i1);
-        o1 = o2;
-    }
-    int it = 0;
-    for (int r = 0; r < (band ? 0 : QW); ++r) {
-        const int l = wl0 + r;
-        GatherSum<CB> sum;
-        sum.zero();
-        float sw = 0.f, mrun = INFINITY;
-        if (r < nqw) {
-            const int t = sm.qrow[l];
-            const float4 qi = ld_key(qs + (int64_t)t * g.dK, g.dK);
-            const float qa[4] = {qi.x, qi.y, qi.z, qi.w};
-            for (int t0 = 0; t0 < g.k; t0 += 64) {
-                // e0: this pass's entries, j0 its tokens, i1 their pages; e1, j1 the next
-                // pass's; e2 and o1 entries and pages of the one after.
-                float d2v[2];
-                int pcur[2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    if ((unsigned)j0.u[u] >= (unsigned)cC) j0.u[u] = -1;
-                    pcur[u] = e0.u[u] >= 0 && j0.u[u] >= 0 ? pool_row(i1.u[u], j0.u[u]) : -1;
-                    lost |= e0.u[u] >= 0 && pcur[u] < 0;
-                    if (g.idx && e0.u[u] >= 0) g.idx[(row0 + t) * g.k + t0 + u * 32 + lane] = j0.u[u];
+                    t[u] = wl0 + r0 + u < nq ? sm.qrow[wl0 + r0 + u] : 0;
+                    st[u] = __shfl_sync(kFull, wst, (r0 + u) & 31);
+                    const float4 q4 = ld_key(qs + (int64_t)t[u] * g.dK, g.dK);
+                    const float qq[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                    for (int d = 0; d < DK; ++d) q[u][d] = qq[d];
                 }
-                float4 kk[2];
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    kk[u] = ld_key(g.k_pages + (int64_t)max(pcur[u], 0) * g.dK, g.dK);
-                gather64<CB>(sum, g.v_pages, g.dV, ppr, pcur, min(4, (g.k - t0 + 15) >> 4), lane, [&] {
-                    ask_page(j1, i1);
-                    j0 = j1;
-                    ask_tok(e2, o1, j1);                     // into j1: a copy would wait for it
-                    entries(it + 3, e3);
-                    ask_oid(e3, o1);
-                    e0 = e1;
-                    e1 = e2;
-                    e2 = e3;
-                    ++it;
+                for (int v = 0; v < 4; ++v) j[v] = page_id(otab, min(st[v >> 1] + slot(v), cC - 1), g.c.psh);
+            } else if (step == 1) {
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float kc[4] = {kk[u].x, kk[u].y, kk[u].z, kk[u].w};
-                        float d2 = 0.f;
+                for (int v = 0; v < 4; ++v) {
+                    const int orow = order_row(j[v], st[v >> 1] + slot(v));
+                    j[v] = ldi_if(g.order_idx + plane + orow, there(v) && orow >= 0);
+                }
+            } else if (step == 2) {
 #pragma unroll
-                        for (int d = 0; d < DK; ++d) {
-                            const float e = qa[d] - kc[d];
-                            d2 = __fmaf_rn(e, e, d2);
-                        }
-                        d2v[u] = pcur[u] >= 0 ? d2 : INFINITY;
+                for (int v = 0; v < 4; ++v) row[v] = page_id(ptab, (unsigned)j[v] < (unsigned)cC ? j[v] : 0, g.c.psh);
+            } else {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    row[v] = (unsigned)j[v] < (unsigned)cC ? pool_row(row[v], j[v]) : -1;
+                    const float *kp = g.k_pages + (int64_t)max(row[v], 0) * g.dK;
+#pragma unroll
+                    for (int d = 0; d < DK; ++d) x[v][d] = d < g.dK ? __ldg(kp + d) : 0.f;
+                }
+            }
+        };
+        float2 o[2][4];
+        float sw[2], mr[2];
+        if (items > 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) look(e);
+        }
+        for (int i = 0; i < items; ++i) {
+            const int row0_ = r0, ent0 = t0;                 // this item's rows and entries
+            if (ent0 == 0) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    sw[u] = 0.f;
+                    mr[u] = INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[u][e] = make_float2(0.f, 0.f);
+                }
+            }
+            float d2[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                d2[v] = 0.f;
+#pragma unroll
+                for (int d = 0; d < DK; ++d) {
+                    const float e = q[v >> 1][d] - x[v][d];
+                    d2[v] = __fmaf_rn(e, e, d2[v]);
+                }
+                if (row[v] < 0) d2[v] = INFINITY;
+                lost |= there(v) && row[v] < 0;
+                if (g.idx && there(v))
+                    g.idx[(row0 + t[v >> 1]) * g.k + slot(v)] = (unsigned)j[v] < (unsigned)cC ? j[v] : -1;
+            }
+            if constexpr (WK == kWSoftmax) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float least = fminf(d2[2 * u], d2[2 * u + 1]);
+#pragma unroll
+                    for (int e = 16; e > 0; e >>= 1) least = fminf(least, __shfl_xor_sync(kFull, least, e));
+                    if (least < mr[u]) {
+                        const float f = mr[u] == INFINITY ? 0.f : __expf((least - mr[u]) * inv_g2);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[u][e] = mul2(o[u][e], dup2(f));
+                        sw[u] *= f;
+                        mr[u] = least;
                     }
-                    if constexpr (WK == kWSoftmax) {
-                        float pm = fminf(d2v[0], d2v[1]);
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) pm = fminf(pm, __shfl_xor_sync(kFull, pm, o));
-                        if (pm < mrun) {
-                            const float sc = mrun == INFINITY ? 0.f : __expf((pm - mrun) * inv_g2);
-                            sum.scale(sc);
-                            sw *= sc;
-                            mrun = pm;
-                        }
-                    }
-                    float w[2];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        w[u] = pcur[u] >= 0 ? weight_fast<WK>(d2v[u], mrun, inv_g2) : 0.f;
-                        sw += w[u];
-                    }
-                    return make_float2(w[0], w[1]);
-                });
+                }
             }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sw += __shfl_xor_sync(kFull, sw, o);
-        } else if (l < nq && g.idx) {                        // chunk 0 selects nothing
-            const int t = sm.qrow[l];
-            for (int u = lane; u < g.k; u += 32) g.idx[(row0 + t) * g.k + u] = -1;
+            for (int v = 0; v < 4; ++v) {
+                const float w = row[v] >= 0 ? weight_fast<WK>(d2[v], mr[v >> 1], inv_g2) : 0.f;
+                sw[v >> 1] += w;
+                ga.w[warp][v >> 1][(v & 1) * 32 + lane] = w;
+                ga.row[warp][v >> 1][(v & 1) * 32 + lane] = row[v];
+            }
+            __syncwarp();
+            // Value rows in batches of 4 RPI entries of both rows, two batches in flight.
+            constexpr int EB = 4 * RPI, NB = 64 / EB;
+            uint4 bufs[2][2][4];
+            auto load = [&](uint4 (&buf)[2][4], int e0) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const int pr = ga.row[warp][u][e0 + grp + v * RPI];
+                        buf[u][v] = ld16_if(g.v_pages + (int64_t)max(pr, 0) * g.dV + sub * 8, pr >= 0 && sub < ppr);
+                    }
+            };
+            auto add = [&](const uint4 (&buf)[2][4], int e0) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const float2 w = dup2(ga.w[warp][u][e0 + grp + v * RPI]);
+                        const uint32_t b4[4] = {buf[u][v].x, buf[u][v].y, buf[u][v].z, buf[u][v].w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            o[u][c] = fma2(w, make_float2(__uint_as_float(b4[c] << 16),
+                                                          __uint_as_float(b4[c] & 0xffff0000u)), o[u][c]);
+                    }
+            };
+            load(bufs[0], 0);
+            load(bufs[1], EB);
+            const bool more = i + 1 < items;
+#pragma unroll
+            for (int e = 0; e < NB; ++e) {
+                if (more && e * 4 % NB == 0) look(e * 4 / NB);
+                add(bufs[e & 1], e * EB);
+                if (e + 2 < NB) load(bufs[e & 1], (e + 2) * EB);
+            }
+            __syncwarp();                                    // the weights have been read
+            if (ent0 + 64 < g.k) continue;                   // more entries of these rows
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float ssum = sw[u];
+#pragma unroll
+                for (int e = 16; e > 0; e >>= 1) ssum += __shfl_xor_sync(kFull, ssum, e);
+#pragma unroll
+                for (int e = 16; e >= LPR; e >>= 1)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        o[u][c].x += __shfl_xor_sync(kFull, o[u][c].x, e);
+                        o[u][c].y += __shfl_xor_sync(kFull, o[u][c].y, e);
+                    }
+                const int l = wl0 + row0_ + u;
+                if (lane < LPR) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) *reinterpret_cast<float2 *>(&sm.win[l][sub * 8 + 2 * c]) = o[u][c];
+                }
+                if (lane == 0) {
+                    sm.swin[l] = ssum;
+                    sm.mwin[l] = mr[u];
+                }
+            }
         }
-        sum.each(lane, [&](int d, float x) { sm.win[l][d] = x; });
-        if (lane == 0) {
-            sm.swin[l] = sw;
-            sm.mwin[l] = mrun;
+        if (chunk == 0) {                                    // nothing selected
+            for (int r = 0; r < QW; ++r) {
+                const int l = wl0 + r;
+                for (int e = lane; e < DVP; e += 32) sm.win[l][e] = 0.f;
+                if (lane == 0) {
+                    sm.swin[l] = 0.f;
+                    sm.mwin[l] = INFINITY;
+                }
+                if (g.idx && l < nq)
+                    for (int e = lane; e < g.k; e += 32) g.idx[(row0 + sm.qrow[l]) * g.k + e] = -1;
+            }
         }
+        if (lost) set_status(g.status, ZETA_ERR_BOUNDS);
     }
-    if (lost) set_status(g.status, ZETA_ERR_BOUNDS);
     __syncthreads();
+    if constexpr (BAND) {                                    // (else they are on their way)
+        load_tile(0);
+        load_tile(1);
+    }
 
     // --------------------------------------------------- own-chunk part ---
     const int rg = warp / KS, kg = warp % KS;                // row group, key split
@@ -783,8 +878,10 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
     const int wmin = __reduce_min_sync(kFull, min(lim_a, lim_b));
     const int wmax = __reduce_max_sync(kFull, max(lim_a, lim_b));
     clear();
-    if (WK == kWSoftmax && kg == 0)                          // from the window's shift
-        mab = make_float2(la >= 0 ? sm.mwin[la] : INFINITY, lb >= 0 ? sm.mwin[lb] : INFINITY);
+    if (WK == kWSoftmax && kg == 0) {                        // from the window's shift
+        ma = la >= 0 ? sm.mwin[la] : INFINITY;
+        mb = lb >= 0 ? sm.mwin[lb] : INFINITY;
+    }
     using KSteps = std::integral_constant<int, TK / 16 / KS>;   // this warp's steps per tile
     for (int kt = 0; kt < nkt; ++kt) {
         cp_async_wait<1>();
@@ -795,22 +892,25 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
         const int key0 = kt * TK, bf = kt % 3, kb = kg * KSteps::value * 16;
         if (key0 + kb <= wmax) {                             // else every weight of this warp is 0
             if (!sm.bad && key0 + TK - 1 <= wmin) {
-                steps(KSteps{}, sm.own.kt[bf], sm.own.v[bf], kb,
-                      [](int, float2 x, float) { return x; });
+                steps(KSteps{}, &sm.own.k[bf][0][0], TK, sm.own.v[bf], kb,
+                      [](auto, int, float2 x, float) { return x; });
             } else {
                 const int *rows = sm.rows[kt & 3];
-                steps(KSteps{}, sm.own.kt[bf], sm.own.v[bf], kb, [&](int kl, float2 x, float no) {
-                    const bool there = rows[kl] >= 0;
-                    return make_float2(there && key0 + kl <= lim_a ? x.x : no,
-                                       there && key0 + kl <= lim_b ? x.y : no);
-                });
+                steps(KSteps{}, &sm.own.k[bf][0][0], TK, sm.own.v[bf], kb,
+                      [&](auto second_row, int kl, float2 x, float no) {
+                          const int2 r = *reinterpret_cast<const int2 *>(rows + kl);
+                          const int lim = decltype(second_row)::value ? lim_b : lim_a;
+                          return make_float2(r.x >= 0 && key0 + kl <= lim ? x.x : no,
+                                             r.y >= 0 && key0 + kl + 1 <= lim ? x.y : no);
+                      });
             }
         }
     }
     __syncthreads();
 
     // --------------------------------------------------------- epilogue ---
-    float sa = sab.x, sb = sab.y;
+    float2 mab = make_float2(ma, mb);
+    float sa = sa2.x + sa2.y, sb = sb2.x + sb2.y;
 #pragma unroll
     for (int o = 1; o <= 2; o <<= 1) {
         sa += __shfl_xor_sync(kFull, sa, o);
@@ -879,9 +979,9 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
     }
     float fa = 1.f, fb = 1.f;                                // window sums onto the final shift
     if constexpr (WK == kWSoftmax) {
-        const float ma = la >= 0 ? sm.mwin[la] : INFINITY, mb = lb >= 0 ? sm.mwin[lb] : INFINITY;
-        fa = ma == INFINITY ? 0.f : shift_scale(mab.x, ma, inv_g2);
-        fb = mb == INFINITY ? 0.f : shift_scale(mab.y, mb, inv_g2);
+        const float wa = la >= 0 ? sm.mwin[la] : INFINITY, wb = lb >= 0 ? sm.mwin[lb] : INFINITY;
+        fa = wa == INFINITY ? 0.f : shift_scale(mab.x, wa, inv_g2);
+        fb = wb == INFINITY ? 0.f : shift_scale(mab.y, wb, inv_g2);
     }
     const float tta = la >= 0 ? __fmaf_rn(sm.swin[la], fa, sa) : 1.f;
     const float ttb = lb >= 0 ? __fmaf_rn(sm.swin[lb], fb, sb) : 1.f;

@@ -89,15 +89,16 @@ class Serving:
                 self.got[b][int(self.len[b]) + t] = (i[:, t], o[:, t], r[:, t])
             self.len[b] += c
 
-    def check(self, rows=None):
-        """Every collected row (or the positions in rows) against the plain form."""
+    def check(self, rows=None, heads=None):
+        """Every collected row (or the positions in rows, of the given heads) against the
+        plain form."""
         w = self.w
         half_w, half_out = (2.0 ** -8, 2.0 ** -8) if w.v_dtype == "bf16" else (0.0, EPS)
 
         def one(bi):
             b, i = bi
             idx, out, rs = self.got[b][i]
-            for h in range(w.H):
+            for h in range(w.H) if heads is None else heads:
                 win, o, s, bo, bs = self.seqs[b].row(h, i, half_w, half_out)
                 want = win if len(win) else np.full(w.k, -1)
                 assert np.array_equal(idx[h], want), (b, h, i)
@@ -184,6 +185,66 @@ def test_pieces_then_tokens(kw, page):
     sv.check()
 
 
+# Pieces large enough for the tile kernel (sequences x heads x rows x C above 2^21),
+# 16 rows a block (5 x 2 x 512) and 128 (5 x 8 x 512), windows row by row and together.
+TILES = [
+    dict(), dict(H=8), dict(d_V=40), dict(d_V=96, k=65), dict(d_V=128, H=8, k=100),
+    dict(d_K=1, bits=21, d_V=32), dict(d_K=2, bits=21, H=8), dict(d_K=4, bits=8, d_V=128),
+    dict(bits=1, H=8), dict(dist="clusters", bits=12, H=8), dict(C=500, N=2000, H=8, k=33),
+    dict(C=500, N=2000, k=7), dict(k=130, H=8), dict(N=20480, H=8, B=5, k=16),
+]
+
+
+@pytest.mark.parametrize("weight", ["cauchy", "softmax", "inv_euclid"])
+@pytest.mark.parametrize("kw", TILES, ids=lambda x: "-".join(f"{a}{b}" for a, b in x.items())
+                         or "base")
+def test_large_pieces(kw, weight):
+    """The first pieces (no window), pieces across chunk ends of unequal length with an
+    idle sequence, whole pieces; rows of every kind against the plain form."""
+    w = _work(**{**dict(B=5, N=2048, C=512, k=24, gamma=(0.3, 1.0)), **kw})
+    sv = Serving(w, 64, weight)
+    stop = w.N - 3 * w.C
+    while sv.len[0] < stop:                              # up to the last four chunks
+        sv.got = [dict() for _ in range(w.B)]
+        sv.step([w.C] * w.B)
+    c = w.C
+    sv.step([c, c - 100, 17, 0, c - 1], n=c)
+    sv.step([c, c, c - 60, 90, 1], n=c)
+    sv.step([c] * 4 + [c - 3], n=c)
+    sv.check_order()
+    rng = np.random.default_rng(11)
+    first = stop - c
+    rows = set(rng.integers(first, w.N, 60).tolist()) | {first, stop, stop + c - 1, stop + c}
+    sv.check(rows, heads=(0, w.H - 1))
+
+
+@pytest.mark.parametrize("H", [2, 8])
+def test_large_pieces_with_values_that_are_not_finite(H):
+    """Infinities and NaN in later tokens of the own chunk and in keys of other rows'
+    windows reach only the rows that attend to them."""
+    w = _work(B=5, H=H, N=1536, C=512, k=24)
+    sv = Serving(w, 64)
+    bad = {0: 700, 1: 1200, 2: 100}                       # sequence: token
+    for b, t in bad.items():
+        sv.v[b, :, t] = float("inf") if b else float("nan")
+    plain = sv.v.clone()
+    for _ in range(3):
+        sv.step([512] * 5, n=512)
+    for b, t in bad.items():
+        for i in range(0, w.N, 7):
+            win, o, r = (x[0] for x in sv.got[b][i])
+            sees = t in win.tolist() or (t // 512 == i // 512 and t <= i)
+            assert np.isfinite(o).all() != sees, (b, i)
+            assert np.isfinite(r)
+    # finite rows are what they would be with any other value there
+    sv.seqs = [Sequence(s.q, s.k, np.nan_to_num(s.v, nan=0.0, posinf=0.0), s.C, s.ksel, w.bits,
+                        s.gamma, "cauchy") for s in sv.seqs]
+    for b, t in bad.items():
+        sv.got[b] = {i: x for i, x in sv.got[b].items() if np.isfinite(x[1]).all()}
+    sv.check(set(range(0, w.N, 11)), heads=(0, H - 1))
+    assert torch.equal(plain.nan_to_num(), sv.v.nan_to_num())
+
+
 @pytest.mark.parametrize("weight", ["softmax", "inv_euclid"])
 @pytest.mark.parametrize("v_dtype,d_V", [("bf16", 64), ("f32", 64), ("bf16", 24)])
 def test_weight_kernels(weight, v_dtype, d_V):
@@ -210,11 +271,11 @@ def test_single_tokens_from_the_first(B, v_dtype):
     sv.check(rows=None if B < 10 else {0, 31, 32, 33, 50, 58})
 
 
-@pytest.mark.parametrize("n", [1, 5, 64, 200, 1024])
-def test_long_context(n):
+@pytest.mark.parametrize("n,H", [(1, 2), (5, 2), (64, 2), (200, 2), (1024, 2), (1024, 5)])
+def test_long_context(n, H):
     """The efficiency workload's shape, chunks of 1024 and windows of 64, the call's
     last rows against the plain form."""
-    w = W.EFFICIENCY.replace(name="cache_long", B=1, H=2, N=16384, seed=17)
+    w = W.EFFICIENCY.replace(name="cache_long", B=1, H=H, N=16384, seed=17)
     sv = Serving(w, 64)
     stop = w.N - n
     while sv.len[0] < stop:
@@ -425,11 +486,11 @@ def test_the_binding_runs_the_same_calls():
     assert torch.equal(out, out2) and torch.equal(rs, rs2)
 
 
-@pytest.mark.parametrize("B,n", [(2, 1), (160, 1), (2, 24)])
-def test_captured_steps_equal_eager_ones(B, n):
+@pytest.mark.parametrize("B,n,C", [(2, 1, 32), (160, 1, 32), (2, 24, 32), (5, 500, 512)])
+def test_captured_steps_equal_eager_ones(B, n, C):
     """One graph of the three calls replayed over many steps, start advanced on the
     device, against eager calls on a second cache; on a stream of its own."""
-    w = _work(B=B, N=192, C=32, k=5, H=2)
+    w = _work(B=B, N=6 * C, C=C, k=5, H=2)
     one, two = Serving(w, 16), Serving(w, 16)
     st = torch.zeros(B, dtype=torch.int32, device="cuda")
     ct = torch.full((B,), n, dtype=torch.int32, device="cuda")
