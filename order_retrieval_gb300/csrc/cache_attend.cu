@@ -559,10 +559,10 @@ cudaError_t launch_cache_attend(const Prob &p, const Cache &c, const float *q, c
         const TileArgs t{c, q, gamma, k_pages, static_cast<const __nv_bfloat16 *>(v_pages),
                          order_codes, order_idx, static_cast<__nv_bfloat16 *>(out), rowsum, idx,
                          status, p.N, p.H, p.dK, p.dV, p.k, p.C, p.bits, p.wk, p.code64};
-        // Sixteen rows a block; 128 where long pieces fill the SMs that way and have the
-        // rows to be dealt by code (8 pieces of 1024: 115 against 152 us, 2 of them 58
-        // against 43; 32 of 256 228 against 194).
-        const bool wide = p.S * c.n >= 152 * 128 && c.n >= 512;
+        // Sixteen rows a block; 128, dealt by code, where enough rows come in long pieces
+        // (16 sequences of up to 1024: 211 against 314 us, 32 of 256 152 against 195, 64 of
+        // 128 186 against 191; but one of 1024 74 against 46, 64 of 64 136 against 112).
+        const bool wide = c.n >= 128 && p.S * c.n >= 152 * 160;
         return p.dV <= 64 ? launch_cache_tile64(p, t, wide, st) : launch_cache_tile128(p, t, wide, st);
     }
     if (p.vdt == ZETA_BF16) {

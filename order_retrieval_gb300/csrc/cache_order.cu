@@ -321,26 +321,27 @@ cache_order_kernel(Cache c, const float *__restrict__ k_pages, K *codes, int32_t
         lost |= cur.lost;
         const int e = i + 4 * lane, cnt = min(kStep, M - i), mine = min(4, M - e);
         const bool last = i + kStep >= M;
-        const uint64_t run_z = lo + lane < C ? run.code(lo + lane) : ~0ull;
-        const uint64_t zn = __shfl_sync(kFull, (uint64_t)cur.z[3], 31);
+        const K run_z = lo + lane < C ? (K)run.code(lo + lane) : K(0);
+        const K zn = __shfl_sync(kFull, cur.z[3], 31);
         const unsigned in = __ballot_sync(kFull, lo + lane < C && (last || run_z < zn));
         const int few = __popc(in);
         int hi = lo + few;
         if (few <= kFew) {                                 // one at a time, through the stage
             int place[4] = {0, 0, 0, 0};
+            const int token = M + run.place(min(lo + lane, C - 1));
             for (int j = 0; j < few; ++j) {
-                const uint64_t z = __shfl_sync(kFull, run_z, j);
-                int le = 0;
+                const K z = __shfl_sync(kFull, run_z, j);
+                int after = 0;                             // of the lane's entries
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const bool after = (uint64_t)cur.z[k] > z;
-                    place[k] += after;
-                    le += k < mine && !after;
+                    const bool a = k < mine && cur.z[k] > z;
+                    place[k] += a;
+                    after += a;
                 }
-                le = __reduce_add_sync(kFull, le);
+                const int le = cnt - (int)__reduce_add_sync(kFull, (unsigned)after);
                 if (lane == j) {
-                    out.z[j + le] = (K)z;
-                    out.token[j + le] = M + run.place(lo + j);
+                    out.z[j + le] = z;
+                    out.token[j + le] = token;
                 }
             }
 #pragma unroll
@@ -351,14 +352,18 @@ cache_order_kernel(Cache c, const float *__restrict__ k_pages, K *codes, int32_t
                 }
             __syncwarp();
             const int total = cnt + few;
-            int pid[5];
+            int pid[4];
 #pragma unroll
-            for (int u = 0; u < 5; ++u)
+            for (int u = 0; u < 4; ++u)
                 pid[u] = page_id(otab, min(i + lo + u * 32 + lane, M + C - 1), c.psh);
 #pragma unroll
-            for (int u = 0; u < 5; ++u) {
+            for (int u = 0; u < 4; ++u) {
                 const int o = u * 32 + lane;
                 if (o < total) put(pid[u], i + lo + o, out.z[o], out.token[o]);
+            }
+            if (kStep + lane < total) {
+                const int o = kStep + lane, e = i + lo + o;
+                put(page_id(otab, e, c.psh), e, out.z[o], out.token[o]);
             }
             __syncwarp();
         } else {                                           // many: by binary search

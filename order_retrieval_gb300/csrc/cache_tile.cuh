@@ -11,10 +11,10 @@
 //    rounded to bf16 once, two keys of a row to an instruction (the coordinates are
 //    staged apart, so that a pair of keys is one operand); products accumulate in
 //    float32, row sums come from the unrounded weights.  NW / WM warps split each tile's keys and join at the end.
-//  * Window, rows that have little in common: a warp takes two rows at a time; their
+//  * Window, few rows (16 a block): a warp takes two rows at a time; their
 //    entries are looked up and weighed a lane each (four in flight), then the value
 //    rows are streamed and summed on the FMA pipes.
-//  * Window, many rows per prefix entry (BAND): the up to 1024 rows of a piece are
+//  * Window, many rows (BAND: 16 a warp): the up to 1024 rows of a piece are
 //    dealt to the warps in the order of their codes (a counting sort on the codes'
 //    top ten bits), so that the 16 windows of a warp overlap.  The warp walks the
 //    prefix positions that any of them covers, 32 at a time through two cp.async
@@ -52,7 +52,6 @@ namespace {
 constexpr int kSortRows = 1024, kBuckets = 1024;
 constexpr int kFences = 1024;
 constexpr int kRing = 2;               // stages of 32 prefix entries per warp
-constexpr int kBandRatio = 40;         // prefix entries per row below which rows are dealt
 
 template <int DVP, int WM, int NW>
 struct TileSmem {
@@ -82,7 +81,6 @@ struct TileSmem {
         Band band[BAND ? 1 : 0];
         Deal deal;
         uint64_t fence_in[BAND ? kFences : 0];
-        Gather gather_in[BAND ? 1 : 0];
         float join[WM * (NW / WM - 1) * 16 * (DVP + 4) + 1];
     };
     // Beside the tiles where there is room, so that the first ones arrive meanwhile.
@@ -214,10 +212,8 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
     auto pool_row = [&](int id, int t) { return row_in(id, t, h, g.H, g.c.psh, g.c.pmask, g.c.pages); };
 
     // ---------------------------------------------------- which rows -------
-    // Where the prefix has less than kBandRatio entries per row, the windows are
-    // walked together, and the rows dealt by code if there is more than one block.
-    const bool band = BAND && chunk > 0 && (int64_t)bn * kBandRatio >= cC;
-    const bool deal = band && bn > nq;
+    const bool band = BAND && chunk > 0;
+    const bool deal = band && bn > nq;                       // more blocks than this one
     if (deal) {
         int *cnt = sm.deal.cnt;
         if (tid < kSortRows / 32) sm.deal.bits[tid] = 0u;
@@ -682,9 +678,9 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
         __syncthreads();                                     // the ring's space goes to the tiles
     }
 
-    if (!band) {
+    if constexpr (!BAND) {
         // ---------------------------------------- windows row by row --------
-        typename Sm::Gather &ga = BAND ? sm.gather_in[0] : sm.gather_by[0];
+        typename Sm::Gather &ga = sm.gather_by[0];
         constexpr int LPR = DVP / 8, RPI = 32 / LPR;         // lanes per value row, rows per load
         const int grp = lane / LPR, sub = lane % LPR;
         bool lost = false;
@@ -848,19 +844,19 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
                 }
             }
         }
-        if (chunk == 0) {                                    // nothing selected
-            for (int r = 0; r < QW; ++r) {
-                const int l = wl0 + r;
-                for (int e = lane; e < DVP; e += 32) sm.win[l][e] = 0.f;
-                if (lane == 0) {
-                    sm.swin[l] = 0.f;
-                    sm.mwin[l] = INFINITY;
-                }
-                if (g.idx && l < nq)
-                    for (int e = lane; e < g.k; e += 32) g.idx[(row0 + sm.qrow[l]) * g.k + e] = -1;
-            }
-        }
         if (lost) set_status(g.status, ZETA_ERR_BOUNDS);
+    }
+    if (chunk == 0) {                                    // nothing selected
+        for (int r = 0; r < QW; ++r) {
+            const int l = wl0 + r;
+            for (int e = lane; e < DVP; e += 32) sm.win[l][e] = 0.f;
+            if (lane == 0) {
+                sm.swin[l] = 0.f;
+                sm.mwin[l] = INFINITY;
+            }
+            if (g.idx && l < nq)
+                for (int e = lane; e < g.k; e += 32) g.idx[(row0 + sm.qrow[l]) * g.k + e] = -1;
+        }
     }
     __syncthreads();
     if constexpr (BAND) {                                    // (else they are on their way)
