@@ -559,11 +559,13 @@ cudaError_t launch_cache_attend(const Prob &p, const Cache &c, const float *q, c
         const TileArgs t{c, q, gamma, k_pages, static_cast<const __nv_bfloat16 *>(v_pages),
                          order_codes, order_idx, static_cast<__nv_bfloat16 *>(out), rowsum, idx,
                          status, p.N, p.H, p.dK, p.dV, p.k, p.C, p.bits, p.wk, p.code64};
-        // Sixteen rows a block; 128, dealt by code, where enough rows come in long pieces
-        // (16 sequences of up to 1024: 211 against 314 us, 32 of 256 152 against 195, 64 of
-        // 128 186 against 191; but one of 1024 74 against 46, 64 of 64 136 against 112).
-        const bool wide = c.n >= 128 && p.S * c.n >= 152 * 160;
-        return p.dV <= 64 ? launch_cache_tile64(p, t, wide, st) : launch_cache_tile128(p, t, wide, st);
+        // Sixteen rows a block; 32 and 64, which share tiles and set-up, where that many
+        // rows fill the SMs: 8,192 rows of one piece 46, 38, 45 us; 64 sequences of 64 rows
+        // 112, 101, 103 us, of 128 rows 190, 159, 145 us; 16 pieces of up to 1024 rows 314,
+        // 243, 204 us; 8 sequences of 64 rows 23, 33, 43 us.
+        const int64_t rows = p.S * c.n;
+        const int wm = c.n >= 128 && rows >= 65536 ? 4 : c.n >= 32 && rows >= 152 * 48 ? 2 : 1;
+        return p.dV <= 64 ? launch_cache_tile64(p, t, wm, st) : launch_cache_tile128(p, t, wm, st);
     }
     if (p.vdt == ZETA_BF16) {
         if (p.code64)

@@ -10,19 +10,14 @@
 //    swizzled shared memory; weights are built straight in mma A fragments and
 //    rounded to bf16 once, two keys of a row to an instruction (the coordinates are
 //    staged apart, so that a pair of keys is one operand); products accumulate in
-//    float32, row sums come from the unrounded weights.  NW / WM warps split each tile's keys and join at the end.
-//  * Window, few rows (16 a block): a warp takes two rows at a time; their
-//    entries are looked up and weighed a lane each (four in flight), then the value
-//    rows are streamed and summed on the FMA pipes.
-//  * Window, many rows (BAND: 16 a warp): the up to 1024 rows of a piece are
-//    dealt to the warps in the order of their codes (a counting sort on the codes'
-//    top ten bits), so that the 16 windows of a warp overlap.  The warp walks the
-//    prefix positions that any of them covers, 32 at a time through two cp.async
-//    stages, as an mma tile whose weights are masked to each row's window: a value
-//    row is read once for all rows that take it, and no row pays for its own gather.
-//    The own chunk then takes the block's rows in the order of their positions, so
-//    that a warp stops at its last row's causal limit.
-//    Dealing changes no row's arithmetic.
+//    float32, row sums come from the unrounded weights.  NW / WM warps split each
+//    tile's keys and join at the end.
+//  * Window: a warp takes two rows at a time; their entries are looked up and weighed
+//    a lane each, the four dependent lookups of the next two rows run between the
+//    batches of value rows of these two, which are streamed and summed on the FMA
+//    pipes.  (Dealing the rows of a piece to the warps by their codes, so that their
+//    windows overlap, and walking them as masked mma tiles was built too: 210 against
+//    204 us for 16 pieces of up to 1024 rows, 64 against 82 us for 4 whole ones.)
 //  * A masked weight of zero times a value that is not finite would be NaN: a row
 //    whose result is not finite is taken again, key by key, without the others.
 #pragma once
@@ -44,33 +39,21 @@ struct TileArgs {
     int N, H, dK, dV, k, C, bits, wk, code64;
 };
 
-cudaError_t launch_cache_tile64(const Prob &p, const TileArgs &g, bool wide, cudaStream_t st);
-cudaError_t launch_cache_tile128(const Prob &p, const TileArgs &g, bool wide, cudaStream_t st);
+// wm: 1, 2 or 4, for 16 wm rows a block.
+cudaError_t launch_cache_tile64(const Prob &p, const TileArgs &g, int wm, cudaStream_t st);
+cudaError_t launch_cache_tile128(const Prob &p, const TileArgs &g, int wm, cudaStream_t st);
 
 namespace {
 
-constexpr int kSortRows = 1024, kBuckets = 1024;
 constexpr int kFences = 1024;
-constexpr int kRing = 2;               // stages of 32 prefix entries per warp
 
 template <int DVP, int WM, int NW>
 struct TileSmem {
     static constexpr int TQ = 16 * WM;
     static constexpr int TK = DVP == 64 && NW / WM >= 4 ? 128 : 64;
-    static constexpr bool BAND = WM == NW;
     struct Own {
         __nv_bfloat16 v[3][TK * DVP];  // 16-byte chunk c of row r at c ^ (r & 7)
         float k[3][4][TK];             // coordinates apart
-    };
-    struct Band {
-        __nv_bfloat16 v[NW][kRing][32 * DVP];
-        float k[NW][kRing][4][32];
-    };
-    struct Deal {
-        int cnt[kBuckets];
-        int cuts[2][kSortRows / 32];
-        int scan[NW];
-        unsigned bits[kSortRows / 32]; // the block's rows
     };
     struct Gather {                    // a warp's two rows
         float w[NW][2][64];
@@ -78,23 +61,16 @@ struct TileSmem {
     };
     union {
         Own own;
-        Band band[BAND ? 1 : 0];
-        Deal deal;
-        uint64_t fence_in[BAND ? kFences : 0];
         float join[WM * (NW / WM - 1) * 16 * (DVP + 4) + 1];
     };
-    // Beside the tiles where there is room, so that the first ones arrive meanwhile.
-    uint64_t fence_by[BAND ? 0 : kFences];
-    Gather gather_by[BAND ? 0 : 1];
+    uint64_t fence[kFences];
+    Gather gather;
     float win[TQ][DVP + 4];            // window sums
     int rows[4][TK];                   // pool rows of the tile's keys, -1: none
     float swin[TQ], mwin[TQ];
     float lsum[NW][16], lmin[NW][16];  // the key splits' row sums and shifts
-    int qrow[TQ];                      // the call's row of query l
-    int perm[TQ];                      // query of own-chunk row r (by position)
-    int wst[TQ];                       // window start of query l
+    int wst[TQ];                       // window start of a row
     int bad;                           // a key of the own chunk has no page
-    int top;                           // the block's last row
 };
 
 // Weights of two keys (the reciprocals by the approximate instructions, 1 ulp).
@@ -168,10 +144,9 @@ __device__ __noinline__ void slow_row(const TileArgs &g, int64_t row0, int t, in
 }
 
 template <int DVP, int DK, int WK, int WM, int NW>
-__global__ void __launch_bounds__(NW * 32, (DVP == 64 ? 16 : 12) / NW)
+__global__ void __launch_bounds__(NW * 32, DVP == 64 ? 2 : 3)
 cache_tile_kernel(const __grid_constant__ TileArgs g) {
     using Sm = TileSmem<DVP, WM, NW>;
-    constexpr bool BAND = Sm::BAND;
     constexpr int TQ = Sm::TQ, TK = Sm::TK, KS = NW / WM;    // KS warps share a row group's keys
     constexpr int kTileThreads = NW * 32;
     constexpr int QW = TQ / NW;                              // window rows per warp
@@ -192,8 +167,7 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
     const int p0 = second ? nA : 0, np = second ? seq.count - nA : nA;
     if (x * TQ >= np) return;
     const int chunk = c0 + (second ? 1 : 0), cC = chunk * g.C;
-    const int blk = x * TQ / kSortRows * kSortRows;          // rows dealt together
-    const int bn = min(kSortRows, np - blk), lo = x * TQ - blk, nq = min(TQ, bn - lo);
+    const int f0 = p0 + x * TQ, nq = min(TQ, np - x * TQ);   // the call's rows f0 .. f0 + nq - 1
     const int32_t *ptab = g.c.ptab + (int64_t)b * g.c.tlen, *otab = g.c.otab + (int64_t)b * g.c.tlen;
     const int64_t row0 = (int64_t)s * g.c.n;                 // the call's row 0 of this slice
     const float *qs = g.q + row0 * g.dK;
@@ -211,101 +185,10 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
     auto order_row = [&](int id, int e) { return row_in(id, e, h, g.H, g.c.psh, g.c.pmask, g.c.opages); };
     auto pool_row = [&](int id, int t) { return row_in(id, t, h, g.H, g.c.psh, g.c.pmask, g.c.pages); };
 
-    // ---------------------------------------------------- which rows -------
-    const bool band = BAND && chunk > 0;
-    const bool deal = band && bn > nq;                       // more blocks than this one
-    if (deal) {
-        int *cnt = sm.deal.cnt;
-        if (tid < kSortRows / 32) sm.deal.bits[tid] = 0u;
-        for (int i = tid; i < kBuckets; i += kTileThreads) cnt[i] = 0;
-        __syncthreads();
-        const int sh = max(0, g.dK * g.bits - 10);
-        int at[kSortRows / kTileThreads];                    // bucket << 16 | place in it
-#pragma unroll
-        for (int u = 0; u < kSortRows / kTileThreads; ++u) {
-            const int l = u * kTileThreads + tid;
-            at[u] = 0;
-            if (l < bn) {
-                const int bk = (int)(code_at(p0 + blk + l) >> sh);
-                at[u] = bk << 16 | atomicAdd(&cnt[bk], 1);
-            }
-        }
-        __syncthreads();
-        constexpr int PER = kBuckets / kTileThreads;
-        int loc[PER], sum = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            loc[i] = sum;
-            sum += cnt[tid * PER + i];
-        }
-        int inc = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kFull, inc, o);
-            if (lane >= o) inc += y;
-        }
-        if (lane == 31) sm.deal.scan[warp] = inc;
-        __syncthreads();
-        int before = inc - sum;
-        for (int w = 0; w < warp; ++w) before += sm.deal.scan[w];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) cnt[tid * PER + i] = before + loc[i];
-        __syncthreads();
-        // Every block of the piece has to deal alike: the places that the atomics
-        // gave out differ from block to block, which matters only in the bucket that
-        // this block shares with the one before and in the one it shares with the
-        // next.  Rows of those two are placed in row order.
-        constexpr int NU = kSortRows / kTileThreads;
-        unsigned cut[2][NU];                                 // the warp's rows of the two buckets
-#pragma unroll
-        for (int u = 0; u < NU; ++u) {
-            const int l = u * kTileThreads + tid, bk = at[u] >> 16;
-            const int first = cnt[bk], last = bk + 1 < kBuckets ? cnt[bk + 1] : bn;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int edge = lo + e * nq;
-                cut[e][u] = __ballot_sync(kFull, l < bn && first < edge && last > edge);
-                if (lane == 0) sm.deal.cuts[e][u * NW + warp] = __popc(cut[e][u]);
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < NU; ++u) {
-            const int l = u * kTileThreads + tid, bk = at[u] >> 16;
-            if (l < bn) {
-                int place = at[u] & 0xffff;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (cut[e][u] >> lane & 1) {
-                        place = __popc(cut[e][u] & lanemask_lt());
-                        for (int i = 0; i < u * NW + warp; ++i) place += sm.deal.cuts[e][i];
-                    }
-                }
-                const int p = cnt[bk] + place - lo;
-                if (p >= 0 && p < nq) {
-                    sm.qrow[p] = p0 + blk + l;
-                    atomicOr(&sm.deal.bits[l >> 5], 1u << (l & 31));
-                }
-            }
-        }
-    } else if (tid < nq) {
-        sm.qrow[tid] = p0 + blk + lo + tid;
-    }
     if (tid == 0) sm.bad = 0;
     __syncthreads();
-    if (tid < TQ) {                                          // order by position
-        int r = tid;
-        if (deal && tid < nq) {
-            const int l = sm.qrow[tid] - p0 - blk;
-            r = __popc(sm.deal.bits[l >> 5] & ((1u << (l & 31)) - 1u));
-            for (int w = 0; w < l >> 5; ++w) r += __popc(sm.deal.bits[w]);
-        }
-        sm.perm[r] = tid < nq ? tid : -1;
-        if (tid < nq && r == nq - 1) sm.top = sm.qrow[tid];
-    }
-    __syncthreads();
     // Own-chunk tiles: keys cC .. last row's position (they all exist).
-    const int kend = seq.start + sm.top + 1 - cC;            // keys of the chunk that matter
+    const int kend = seq.start + f0 + nq - cC;               // keys of the chunk that matter
     const int nkt = (kend + TK - 1) / TK;
     auto ask_rows = [&](int kt) {                            // page of the thread's key of tile kt
         return tid < TK && kt * TK + tid < kend ? page_id(ptab, cC + kt * TK + tid, g.c.psh) : -1;
@@ -352,22 +235,19 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
         put_rows(1, i1);
         put_rows(2, i2);
     }
-    if constexpr (!BAND) {
-        __syncthreads();
-        load_tile(0);
-        load_tile(1);
-    }
+    __syncthreads();
+    load_tile(0);
+    load_tile(1);
 
     // ------------------------------------------------------ window part ---
     const int g4 = lane >> 2, s4 = lane & 3;
     const int wl0 = warp * QW, nqw = chunk > 0 ? max(0, min(QW, nq - wl0)) : 0;
     int wst = 0;                                             // lane r < nqw: start of row wl0 + r
     if (chunk > 0) {
-        uint64_t *fence = BAND ? sm.fence_in : sm.fence_by;
+        uint64_t *fence = sm.fence;
         int fsh = 5;
         while ((cC >> fsh) >= kFences) ++fsh;
         const int nf = (cC + (1 << fsh) - 1) >> fsh;
-        __syncthreads();                                     // the counters have been read
         {
             constexpr int NF = kFences / kTileThreads;
             int fr[NF];
@@ -393,7 +273,7 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
         uint64_t z = 0;
         int lo_f = 0;
         if (lane < nqw) {
-            z = code_at(sm.qrow[wl0 + lane]);
+            z = code_at(f0 + wl0 + lane);
             int hi = nf;
             while (lo_f < hi) {                              // fences with code <= z
                 const int mid = (lo_f + hi) >> 1;
@@ -449,7 +329,6 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
                 if (lane == r0 + i) wst = min(max(a[i] - (g.k + 1) / 2, 0), cC - g.k);
         }
         if (lane < nqw) sm.wst[wl0 + lane] = wst;
-        __syncthreads();                                     // fences read before the tiles arrive
     }
     // Weights in A fragments and products of KN steps of 16 keys: lane (g4, s4) has
     // rows g4 (a) and g4 + 8 (b) of its group and the key pairs 2 s4, +1 and +8, +9 of
@@ -557,130 +436,8 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
         }
     };
 
-    if constexpr (BAND) if (band) {
-        // ------------------------------------ windows walked together ------
-        clear();
-        const int none = INT_MAX;
-        take_rows(g4 < nqw ? sm.qrow[wl0 + g4] : -1, g4 + 8 < nqw ? sm.qrow[wl0 + g4 + 8] : -1);
-        const int far = -(1 << 30);                          // no position is within k of it
-        const int wa = __shfl_sync(kFull, wst, g4), wb = __shfl_sync(kFull, wst, g4 + 8);
-        const int sta = g4 < nqw ? wa : far, stb = g4 + 8 < nqw ? wb : far;
-        auto next = [&](int p) {                             // first position >= p that a row takes
-            const int c = p < cC && lane < nqw && wst + g.k > p ? max(wst, p) : none;
-            return __reduce_min_sync(kFull, c);
-        };
-        auto entry = [&](int bp) { return min(bp == none ? 0 : bp + lane, cC - 1); };   // lane's entry of a block
-        auto &ring = sm.band[0];
-        auto copy = [&](int stage, int row) {                // an entry without a row: infinitely far
-            const float *kp = g.k_pages + (int64_t)max(row, 0) * g.dK;
-#pragma unroll
-            for (int d = 0; d < DK; ++d) {
-                float *kd = &ring.k[warp][stage][d][lane];
-                if (row < 0) *kd = INFINITY;
-                else if (d < g.dK) cp_async4(smem_u32(kd), kp + d, 4);
-                else *kd = 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < DVP / 8; ++i) {
-                const int id = i * 32 + lane, r = id / (DVP / 8), ch = id % (DVP / 8);
-                const int pr = __shfl_sync(kFull, row, r);
-                if (ch < ppr)
-                    cp_async16(smem_u32(&ring.v[warp][stage][r * DVP + ((ch ^ (r & 7)) * 8)]),
-                               g.v_pages + (int64_t)max(pr, 0) * g.dV + ch * 8, pr >= 0 ? 16 : 0);
-            }
-            cp_async_commit();
-        };
-        bool lost = false;
-        auto ask_tok = [&](int id, int block) {              // the token of the lane's entry
-            const int row = order_row(id, entry(block));
-            lost |= block != none && row < 0;
-            return ldi_if(g.order_idx + plane + row, row >= 0);
-        };
-        auto ask_page = [&](int j) { return page_id(ptab, (unsigned)j < (unsigned)cC ? j : 0, g.c.psh); };
-        auto got_row = [&](int id, int j, int block) {       // -1: no entry, or dropped
-            if (block == none || block + lane >= cC) return -1;
-            const int row = (unsigned)j < (unsigned)cC ? pool_row(id, j) : -1;
-            lost |= row < 0;
-            return row;
-        };
-        // Block i is walked while block i+1 arrives; the pages of the tokens of i+2, the
-        // tokens of i+3 and the pages of the entries of i+4 are on their way, each looked
-        // at one turn later.
-        int bp[5];
-        bp[0] = next(0);
-#pragma unroll
-        for (int i = 1; i < 5; ++i) bp[i] = bp[i - 1] == none ? none : next(bp[i - 1] + 32);
-        int row1, id2, j2, j3, o4;
-        {
-            const int a0 = page_id(otab, entry(bp[0]), g.c.psh), a1 = page_id(otab, entry(bp[1]), g.c.psh);
-            const int a2 = page_id(otab, entry(bp[2]), g.c.psh), a3 = page_id(otab, entry(bp[3]), g.c.psh);
-            o4 = page_id(otab, entry(bp[4]), g.c.psh);
-            const int t0 = ask_tok(a0, bp[0]), t1 = ask_tok(a1, bp[1]);
-            j2 = ask_tok(a2, bp[2]);
-            j3 = ask_tok(a3, bp[3]);
-            const int i0 = ask_page(t0), i1 = ask_page(t1);
-            id2 = ask_page(j2);
-            copy(0, got_row(i0, t0, bp[0]));
-            row1 = got_row(i1, t1, bp[1]);
-        }
-        for (int i = 0; bp[0] != none; ++i) {
-            copy((i + 1) & 1, row1);
-            row1 = got_row(id2, j2, bp[2]);
-            const int nb = bp[4] == none ? none : next(bp[4] + 32);
-            j2 = j3;
-            id2 = ask_page(j3);
-            j3 = ask_tok(o4, bp[4]);
-            o4 = page_id(otab, entry(nb), g.c.psh);
-            cp_async_wait<1>();
-            __syncwarp();                                    // block i is here
-            const int base = bp[0];
-            steps(std::integral_constant<int, 2>{}, &ring.k[warp][i & 1][0][0], 32, ring.v[warp][i & 1], 0,
-                  [&](auto second_row, int kl, float2 x, float no) {
-                      const int from = base + kl - (decltype(second_row)::value ? stb : sta);
-                      return make_float2((unsigned)from < (unsigned)g.k ? x.x : no,
-                                         (unsigned)(from + 1) < (unsigned)g.k ? x.y : no);
-                  });
-            __syncwarp();                                    // its stage may be filled again
-#pragma unroll
-            for (int e = 0; e < 4; ++e) bp[e] = bp[e + 1];
-            bp[4] = nb;
-        }
-        if (lost) set_status(g.status, ZETA_ERR_BOUNDS);
-        cp_async_wait<0>();
-        if (g.idx) {
-            for (int r = 0; r < nqw; ++r) {
-                const int st = __shfl_sync(kFull, wst, r);
-                for (int u = lane; u < g.k; u += 32) {
-                    const int row = page_row(otab, st + u, h, g.H, g.c.psh, g.c.pmask, g.c.opages);
-                    const int j = row >= 0 ? __ldg(g.order_idx + plane + row) : -1;
-                    g.idx[(row0 + sm.qrow[wl0 + r]) * g.k + u] = (unsigned)j < (unsigned)cC ? j : -1;
-                }
-            }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            if (nt < 2 * nc) {
-                *reinterpret_cast<float2 *>(&sm.win[wl0 + g4][nt * 8 + 2 * tig]) = make_float2(acc[nt][0], acc[nt][1]);
-                *reinterpret_cast<float2 *>(&sm.win[wl0 + g4 + 8][nt * 8 + 2 * tig]) = make_float2(acc[nt][2], acc[nt][3]);
-            }
-        float sa = sa2.x + sa2.y, sb = sb2.x + sb2.y;
-#pragma unroll
-        for (int o = 1; o <= 2; o <<= 1) {
-            sa += __shfl_xor_sync(kFull, sa, o);
-            sb += __shfl_xor_sync(kFull, sb, o);
-        }
-        if (tig == 0) {
-            sm.swin[wl0 + g4] = sa;
-            sm.swin[wl0 + g4 + 8] = sb;
-            sm.mwin[wl0 + g4] = ma;
-            sm.mwin[wl0 + g4 + 8] = mb;
-        }
-        __syncthreads();                                     // the ring's space goes to the tiles
-    }
-
-    if constexpr (!BAND) {
-        // ---------------------------------------- windows row by row --------
-        typename Sm::Gather &ga = sm.gather_by[0];
+    if (chunk > 0) {
+        typename Sm::Gather &ga = sm.gather;
         constexpr int LPR = DVP / 8, RPI = 32 / LPR;         // lanes per value row, rows per load
         const int grp = lane / LPR, sub = lane % LPR;
         bool lost = false;
@@ -703,7 +460,7 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    t[u] = wl0 + r0 + u < nq ? sm.qrow[wl0 + r0 + u] : 0;
+                    t[u] = min(f0 + wl0 + r0 + u, f0 + nq - 1);
                     st[u] = __shfl_sync(kFull, wst, (r0 + u) & 31);
                     const float4 q4 = ld_key(qs + (int64_t)t[u] * g.dK, g.dK);
                     const float qq[4] = {q4.x, q4.y, q4.z, q4.w};
@@ -845,29 +602,24 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
             }
         }
         if (lost) set_status(g.status, ZETA_ERR_BOUNDS);
-    }
-    if (chunk == 0) {                                    // nothing selected
-        for (int r = 0; r < QW; ++r) {
-            const int l = wl0 + r;
+    } else {                                                 // nothing selected
+        for (int l = wl0; l < wl0 + QW; ++l) {
             for (int e = lane; e < DVP; e += 32) sm.win[l][e] = 0.f;
             if (lane == 0) {
                 sm.swin[l] = 0.f;
                 sm.mwin[l] = INFINITY;
             }
             if (g.idx && l < nq)
-                for (int e = lane; e < g.k; e += 32) g.idx[(row0 + sm.qrow[l]) * g.k + e] = -1;
+                for (int e = lane; e < g.k; e += 32) g.idx[(row0 + f0 + l) * g.k + e] = -1;
         }
     }
     __syncthreads();
-    if constexpr (BAND) {                                    // (else they are on their way)
-        load_tile(0);
-        load_tile(1);
-    }
 
     // --------------------------------------------------- own-chunk part ---
     const int rg = warp / KS, kg = warp % KS;                // row group, key split
-    const int la = sm.perm[rg * 16 + g4], lb = sm.perm[rg * 16 + 8 + g4];
-    const int ta = la >= 0 ? sm.qrow[la] : -1, tb = lb >= 0 ? sm.qrow[lb] : -1;
+    const int la = rg * 16 + g4 < nq ? rg * 16 + g4 : -1;    // the thread's two rows, -1: none
+    const int lb = rg * 16 + 8 + g4 < nq ? rg * 16 + 8 + g4 : -1;
+    const int ta = la >= 0 ? f0 + la : -1, tb = lb >= 0 ? f0 + lb : -1;
     const int lim_a = ta >= 0 ? seq.start + ta - cC : -1;    // last key of the chunk row a sees
     const int lim_b = tb >= 0 ? seq.start + tb - cC : -1;
     take_rows(ta, tb);
@@ -1011,9 +763,9 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
         while (again[e]) {
             const int r = (__ffs(again[e]) - 1) >> 2;
             again[e] &= ~(15u << (4 * r));
-            const int l = sm.perm[rg * 16 + 8 * e + r];
+            const int l = rg * 16 + 8 * e + r;
             __syncwarp();                                    // the fast result is written first
-            slow_row<DVP, DK, WK>(g, row0, sm.qrow[l], h, seq.start, cC, cC > 0 ? sm.wst[l] : 0, ptab,
+            slow_row<DVP, DK, WK>(g, row0, f0 + l, h, seq.start, cC, cC > 0 ? sm.wst[l] : 0, ptab,
                                   otab, plane, inv_g2);
         }
     }

@@ -3,8 +3,10 @@
 
 namespace zeta {
 
-cudaError_t launch_cache_tile64(const Prob &p, const TileArgs &g, bool wide, cudaStream_t st) {
-    return wide ? dispatch_tile<64, 8, 8>(p, g, st) : dispatch_tile<64, 1, 8>(p, g, st);
+cudaError_t launch_cache_tile64(const Prob &p, const TileArgs &g, int wm, cudaStream_t st) {
+    if (wm == 1) return dispatch_tile<64, 1, 8>(p, g, st);
+    if (wm == 2) return dispatch_tile<64, 2, 8>(p, g, st);
+    return dispatch_tile<64, 4, 8>(p, g, st);
 }
 
 }  // namespace zeta

@@ -9,7 +9,7 @@ from order_retrieval_gb300 import ZetaCache, ZetaError, zeta_attention
 from order_retrieval_gb300 import binding as zb
 from order_retrieval_gb300 import workloads as W
 
-from cache_util import EPS, Sequence
+from cache_util import EPS, Sequence, window
 from gpu_util import in_threads
 
 pytestmark = [
@@ -299,6 +299,57 @@ def test_equals_the_training_forward():
     size = np.abs(sv.seqs[0].v).max()
     assert np.abs(got - whole[0]).max() <= 4 * 2.0 ** -8 * size
     sv.check(set(range(0, w.N, 37)))
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(v_dtype="f32", d_V=24), dict(d_K=8, bits=8)],
+                         ids=["bf16", "f32", "dk8"])
+def test_longest_chunks_and_long_prefixes(kw):
+    """Chunks of 8192, the longest that are sorted in shared memory, under a prefix of
+    more than 65,536 entries; pieces of a chunk, a short piece, a token."""
+    w = _work(**{**dict(B=1, H=1, N=81920, C=8192, k=40, seed=5), **kw})
+    sv = Serving(w, 256)
+    for _ in range(9):
+        sv.got = [dict()]
+        sv.step([8192])
+    sv.step([8000])
+    sv.step([100])
+    sv.step([1])
+    sv.check_order()
+    sv.check({73728 - 8192, 73727, 73728, 73728 + 4000, 81727, 81728, 81800, 81828})
+
+
+@pytest.mark.parametrize("H", [2, 8])
+def test_bad_pages_of_large_pieces(H):
+    """The tile kernel's share of bad tables: keys on pages out of range are left out of
+    the own chunk and of the windows, everything else stays."""
+    w = _work(B=5, H=H, N=1536, C=512, k=24)
+    sv = Serving(w, 64)
+    sv.step([512] * 5)
+    start, count, q, k, v = sv.batch([512] * 5, 512)
+    sv.cache.append(k, v, start, count, sv.table)
+    bad = sv.table.clone()
+    bad[0, 3] = -1                             # tokens 192..255: in the prefix
+    bad[1, 8] = 10 ** 6                        # tokens 512..575: in the own chunk
+    out = torch.full((5, H, 512, 64), PAD, dtype=torch.bfloat16, device="cuda")
+    rs = torch.full((5, H, 512), PAD, device="cuda")
+    sv.cache.attend(q, sv.gamma, start, count, bad, out, rs, sv.table)
+    assert int(sv.cache.status.item()) == 6
+    out, rs = out.double().cpu().numpy(), rs.cpu().numpy()
+    for b in (0, 1, 2):
+        s = sv.seqs[b]
+        gone = {0: range(192, 256), 1: range(512, 576), 2: ()}[b]
+        for t in (0, 63, 64, 300, 511):
+            i = 512 + t
+            win = window(s.qc[0, i], s.kc[0], i, w.C, w.k)
+            j = np.array([x for x in [*win, *range(512, i + 1)] if x not in gone])
+            if len(j) == 0:
+                continue
+            d2 = ((s.q[0, i].astype(np.float64) - s.k[0][j]) ** 2).sum(1)
+            wt = 1 / (1 + d2 / float(s.gamma[0]) ** 2)
+            size = (wt @ np.abs(s.v[0][j])) / wt.sum()
+            assert abs(rs[b, 0, t] - wt.sum()) <= 1e-5 * wt.sum()
+            # weight and result rounded to bf16 once each
+            assert (np.abs(out[b, 0, t] - (wt @ s.v[0][j]) / wt.sum()) <= 2.1 * 2.0 ** -8 * size).all()
 
 
 def test_order_tables_of_their_own_and_shared_prompt_pages():
