@@ -5,7 +5,13 @@
 // pieces, one thread each (single values where the row is no multiple of 16
 // bytes); the row's first threads also carry its d_K coordinates.  The rows of
 // all slices are one list, so a batch of single tokens fills its blocks as well
-// as a long piece does.
+// as a long piece does.  A block takes whole rows, so that the row a thread works
+// for needs divisions of 32 bits only.
+//
+// 9,900 tokens in 16 sequences, 8 heads, 12 bytes a key and 128 a value: 7.4 us for
+// 22 MB, 3.0 TB/s (8.0 us with the pieces of all rows as one list and a division of
+// 64 bits).  What bounds it is finding the row: four pieces a thread, loads ahead of
+// stores, took 10 us, for that arithmetic then has fewer warps to hide in.
 #include "cache.cuh"
 
 namespace zeta {
@@ -17,12 +23,12 @@ template <typename Piece>
 __global__ void __launch_bounds__(kThreads)
 cache_append_kernel(const float *__restrict__ k, const Piece *__restrict__ v,
                     float *__restrict__ k_pages, Piece *__restrict__ v_pages, Cache c,
-                    int32_t *status, unsigned rows, int N, int H, int dK, int ppr) {
-    const uint64_t id = blockIdx.x * (uint64_t)kThreads + threadIdx.x;
-    const uint64_t r64 = id / (unsigned)ppr;
-    if (r64 >= rows) return;
+                    int32_t *status, unsigned rows, int N, int H, int dK, int ppr, int rpb) {
+    const unsigned in = threadIdx.x / (unsigned)ppr;             // row of the block
+    const int ch = (int)(threadIdx.x - in * (unsigned)ppr);
+    const uint64_t r64 = (uint64_t)blockIdx.x * (unsigned)rpb + in;
+    if (in >= (unsigned)rpb || r64 >= rows) return;
     const unsigned r = (unsigned)r64;
-    const int ch = (int)(id - r64 * (unsigned)ppr);
     const unsigned s = r / (unsigned)c.n;
     const int t = (int)(r - s * (unsigned)c.n);
     const int b = (int)(s / (unsigned)H), h = (int)(s - (unsigned)b * (unsigned)H);
@@ -48,11 +54,10 @@ cudaError_t launch_cache_append(const Prob &p, const Cache &c, const float *k, c
 #define ZETA_APPEND(Piece)                                                                     \
     do {                                                                                       \
         const int ppr = bytes / (int)sizeof(Piece);                                            \
-        const uint64_t blocks = ((uint64_t)rows * ppr + kThreads - 1) / kThreads;              \
-        if (blocks > 0x7fffffffull) return cudaErrorInvalidConfiguration;                      \
-        cache_append_kernel<Piece><<<(unsigned)blocks, kThreads, 0, st>>>(                     \
+        const int rpb = kThreads / ppr;      /* at most 256 pieces a row: at least one */      \
+        cache_append_kernel<Piece><<<(rows + rpb - 1) / rpb, kThreads, 0, st>>>(               \
             k, static_cast<const Piece *>(v), k_pages, static_cast<Piece *>(v_pages), c,       \
-            status, rows, p.N, p.H, p.dK, ppr);                                                \
+            status, rows, p.N, p.H, p.dK, ppr, rpb);                                           \
     } while (0)
     if (bytes % 16 == 0) ZETA_APPEND(uint4);
     else if (esz == 4) ZETA_APPEND(uint32_t);

@@ -541,7 +541,7 @@ def test_the_binding_runs_the_same_calls():
 def test_captured_steps_equal_eager_ones(B, n, C):
     """One graph of the three calls replayed over many steps, start advanced on the
     device, against eager calls on a second cache; on a stream of its own."""
-    w = _work(B=B, N=6 * C, C=C, k=5, H=2)
+    w = _work(B=B, N=5 * C, C=C, k=5, H=2)
     one, two = Serving(w, 16), Serving(w, 16)
     st = torch.zeros(B, dtype=torch.int32, device="cuda")
     ct = torch.full((B,), n, dtype=torch.int32, device="cuda")
