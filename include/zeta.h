@@ -438,7 +438,8 @@ zeta_status_t zeta_cache_order(const zeta_problem_t *p, const zeta_cache_t *cc,
  *   idx       out: int32 [B, H, n, k], the window's tokens (-1 in chunk 0), or
  *             null
  *   dev_status  optional int32 device word; an order entry outside [0, cC) or a
- *             page out of range drops its key and records ZETA_ERR_BOUNDS.
+ *             page out of range drops its key and records ZETA_ERR_BOUNDS (a row
+ *             that loses all of them: rowsum 0, out NaN).
  * Errors: ZETA_ERR_INVALID_ARG, ZETA_ERR_UNSUPPORTED.
  */
 zeta_status_t zeta_cache_attend(const zeta_problem_t *p, const zeta_cache_t *cc, const float *q,
