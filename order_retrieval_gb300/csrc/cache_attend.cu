@@ -15,27 +15,26 @@
 //    of four 16-byte pieces in flight per lane.  A warp's rows follow one another in
 //    their page, so a batch needs one address; its first batch is asked for before the
 //    weights.
-//  * Meanwhile one warp searches the rank (32 P probes a step instead of one), looks
-//    up the window's rows and weighs them; when it is done, all warps stream them.
+//  * Meanwhile one warp searches the rank (32 probes a step instead of one), looks up
+//    the window's rows and weighs them; when it is done, all warps stream them.
 //    In a cluster the last block takes the window and the others the own chunk.
-//  * Blocks of four warps and at most 64 registers, eight to an SM, so that one
-//    block's search and joins hide behind the others' loads.  (A warp per row with
-//    its rows in flight through shared memory, summed on the tensor cores, needs
-//    fewer instructions but waits for each of its steps alone: 100 us for these
-//    3,784 rows.  Eight warps a block spend most of theirs on setting up and
-//    joining: 81 us; the figures of this kernel are below.)
+//  * Blocks of four warps and at most 72 registers, seven to an SM, so that one
+//    block's search and joins hide behind the others' loads.  Taken for the 3,784 rows
+//    measured below: 69 us; six blocks to an SM 72, eight (64 registers) 73, nine 75;
+//    batches of half or twice as many pieces 80 and 77; weights made 32 at a time by
+//    the warp that streams those rows, without barriers, 88; eight warps a block 81; a
+//    warp per row with its rows through shared memory onto the tensor cores 100.
 //  * Sums of weights and of weighted values are held in float32 per thread and
 //    joined in a fixed order, in shared memory and across the cluster through
 //    distributed shared memory: no workspace, one launch, the same bits each run.
 //
 // 473 sequences with one new token, 8 heads, 9 K tokens before each and 522 in its
-// chunk of 1024 on average, windows of 48, 128-byte value rows: 72 us for 300 MB, 4.2
-// TB/s (61 % of the measured HBM rate; DRAM reads 343 MB, the rank probes and table
-// sectors among them).  48 % of the issue slots are used and 43 % of the warps active;
-// the warps wait for loads (6.3 stalls per issue) and at the block's barriers (2.7).
-// 59 sequences with 37 K tokens before each: 20 us, the time of one row's chain (rank
-// search, window lookups, join) beside the longest own chunk.  One sequence, one head,
-// a chunk of 128: 4.9 us.
+// chunk of 1024 on average, windows of 48, 128-byte value rows: 69 us for 300 MB, 4.4
+// TB/s (64 % of the measured HBM rate; DRAM reads 343 MB, the rank probes and table
+// sectors among them).  Half of the issue slots are used; the warps wait for loads and
+// at the block's barriers.  59 sequences with 37 K tokens before each: 16 us, one row's
+// chain (rank search, window lookups, join) beside the longest own chunk, all blocks at
+// once.  One sequence, one head, a chunk of 128: 4.3 us.
 #include <cooperative_groups.h>
 
 #include "cache_tile.cuh"
@@ -45,6 +44,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+constexpr int kPerSM = 7;              // blocks of four warps to an SM
 constexpr int kSeg = 1024;             // keys weighed at a time
 constexpr int kWin = 64;               // window entries that the searching warp prepares
 
@@ -110,30 +110,20 @@ __device__ __forceinline__ float warp_sum(float x) {
 // Barrier of the first `n` threads, the warps that take the own chunk.
 __device__ __forceinline__ void bar_own(int n) { asm volatile("bar.sync 1, %0;\n" ::"r"(n) : "memory"); }
 
-// Entries of the prefix with a code <= z: a warp probes 32 P of them per step.
-template <typename K, int P, typename Page>
+// Entries of the prefix with a code <= z: a warp probes 32 per step.  (64, 128 or 256
+// probes take a step less and no less time, and their sectors come out of the other
+// blocks' HBM time: 64 tokens under 64 K entries 18.1 us with 32, then 18.4, 19.2, 20.7.)
+template <typename K, typename Page>
 __device__ __forceinline__ int rank_of(const Args &g, Page page, int h, const K *codes, K z, int M,
                                        int lane) {
     int lo = 0, hi = M;
     while (lo < hi) {
-        const int step = (hi - lo + 32 * P - 1) / (32 * P);
-        auto at = [&](int p) { return lo + (p * 32 + lane + 1) * step - 1; };
-        int row[P];
-        K c[P];
-#pragma unroll
-        for (int p = 0; p < P; ++p) row[p] = page(min(at(p), M - 1));
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            row[p] = row_in(row[p], at(p), h, g.H, g.c.psh, g.c.pmask, g.c.opages);
-            c[p] = __ldg(codes + max(row[p], 0));
-        }
-        int le = 0;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const bool open = at(p) < hi;
-            if (open && row[p] < 0) set_status(g.status, ZETA_ERR_BOUNDS);
-            le += __popc(__ballot_sync(kFull, open && row[p] >= 0 && c[p] <= z));
-        }
+        const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step - 1;
+        const int row = row_in(page(min(at, M - 1)), at, h, g.H, g.c.psh, g.c.pmask, g.c.opages);
+        const K c = __ldg(codes + max(row, 0));
+        const bool open = at < hi;
+        if (open && row < 0) set_status(g.status, ZETA_ERR_BOUNDS);
+        const int le = __popc(__ballot_sync(kFull, open && row >= 0 && c <= z));
         lo = min(lo + le * step, hi);
         hi = min(hi, lo + step - 1);
     }
@@ -147,7 +137,7 @@ struct Total {
 
 // V: value type; LPR lanes per value row, NP pieces per lane; LOW: d_K <= 4.
 template <typename K, typename V, bool WIDE, int LPR, int NP, bool LOW>
-__global__ void __launch_bounds__(128, 8)
+__global__ void __launch_bounds__(128, kPerSM)
 cache_rows_kernel(const __grid_constant__ Args g, const K *__restrict__ order_codes,
                   const V *__restrict__ v_pages, V *__restrict__ out, int cs, int ppr) {
     using P = Piece<V, WIDE>;
@@ -328,11 +318,7 @@ cache_rows_kernel(const __grid_constant__ Args g, const K *__restrict__ order_co
 #pragma unroll
         for (int d = 0; d < kMaxDK; ++d) x[d] = d < DM ? q[d < DM ? d : 0] : 0.f;
         const K z = (K)code_of(x, g.dK, g.bits);
-        // Many probes a step where latency counts; few where every probe's sector comes
-        // out of the HBM time of the others (256 probes: 124 MB more for 4,096 rows).
-        const int rk = cs > 1 || gridDim.z * gridDim.y * gridDim.x < 152 * 2
-                           ? rank_of<K, 8>(g, opage, h, order_codes + plane, z, cC, lane)
-                           : rank_of<K, 1>(g, opage, h, order_codes + plane, z, cC, lane);
+        const int rk = rank_of<K>(g, opage, h, order_codes + plane, z, cC, lane);
         const int st = min(max(rk - (g.k + 1) / 2, 0), cC - g.k);
         int slot[UK];                                            // two a lane
 #pragma unroll
@@ -511,11 +497,12 @@ template <typename K, typename V, bool WIDE, int LPR, int NP>
 cudaError_t run_rows(const Args &g, const Prob &p, const void *order_codes, const void *v_pages,
                      void *out, int ppr, cudaStream_t st) {
     const int64_t rows = p.S * g.c.n;
-    // Blocks per token: split where the tokens alone leave SMs idle and the own chunk
-    // has work for more than four warps (a cluster's joins cost 1.3 us).
+    // Blocks per token: split as far as all blocks run at once and the own chunk has
+    // work for more than four warps (a cluster's joins cost 1.3 us).  64 tokens of 8
+    // heads, C 1024: one block each 21 us, two 16, four 26.
     const int most = p.C <= 256 ? 1 : p.C <= 512 ? 2 : p.C <= 1024 ? 4 : 8;
     int cs = 1;
-    while (cs < most && rows * cs * 2 <= 152 * 8) cs *= 2;
+    while (cs < most && rows * cs * 2 <= 152 * kPerSM) cs *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(g.c.n * cs), (unsigned)p.H, (unsigned)p.B);
     cfg.blockDim = dim3(128);
