@@ -120,11 +120,14 @@ struct Old {
     bool lost;
 };
 
-// One warp's output stage.
+// One warp's output stage: entry e of the new prefix at e % kRing.  At most kKeep
+// entries stay when a step ends, so that the next one's kStep + kFew fit.
+constexpr int kRing = 256;
+constexpr int kKeep = kRing - kStep - kFew;
 template <typename K>
 struct Stage {
-    K z[kStep + 32];
-    int token[kStep + 32];
+    K z[kRing];
+    int token[kRing];
 };
 
 template <typename K, bool PACK>
@@ -319,6 +322,37 @@ cache_order_kernel(Cache c, const float *__restrict__ k_pages, K *codes, int32_t
         const int row = order_row(page_id(otab, i0 - 1, c.psh), i0 - 1);
         lo = row >= 0 ? run.below((uint64_t)__ldg(src_z + row), 0, C) : 0;
     }
+    // Entries head .. tail - 1 of the new prefix wait in the stage.  They leave four a
+    // lane, on 16-byte boundaries, until no more than kKeep are left (or none: `all`).
+    int head = i0 + lo;
+    auto flush = [&](int tail, bool all) {
+        auto singly = [&](int to) {
+            for (int e = head + lane; e < to; e += 32)
+                put(page_id(otab, e, c.psh), e, out.z[e & (kRing - 1)], out.token[e & (kRing - 1)]);
+            head = max(head, to);
+        };
+        if (all || !quad) {
+            singly(tail);
+        } else {
+            singly(min((head + 3) & ~3, tail));
+            while (tail - head > kKeep) {
+                const int nq = min(32, (tail - head) >> 2);
+                if (lane < nq) {
+                    const int e = head + 4 * lane;
+                    const int row = order_row(page_id(otab, e, c.psh), e);
+                    lost |= row < 0;
+                    if (row >= 0) {
+                        const int at = e & (kRing - 1);
+                        *reinterpret_cast<int4 *>(dst_i + row) = *reinterpret_cast<const int4 *>(out.token + at);
+                        *reinterpret_cast<uint4 *>(dst_z + row) = *reinterpret_cast<const uint4 *>(out.z + at);
+                        if constexpr (sizeof(K) == 8)
+                            *reinterpret_cast<uint4 *>(dst_z + row + 2) = *reinterpret_cast<const uint4 *>(out.z + at + 2);
+                    }
+                }
+                head += 4 * nq;
+            }
+        }
+    };
     // Two sets of registers in turn: copying the next entries would wait for them.
     int i = i0;
     auto turn = [&](const Old<K> &cur, Old<K> &nxt) {
@@ -346,34 +380,24 @@ cache_order_kernel(Cache c, const float *__restrict__ k_pages, K *codes, int32_t
                 }
                 const int le = cnt - (int)__reduce_add_sync(kFull, (unsigned)after);
                 if (lane == j) {
-                    out.z[j + le] = z;
-                    out.token[j + le] = token;
+                    out.z[(i + lo + j + le) & (kRing - 1)] = z;
+                    out.token[(i + lo + j + le) & (kRing - 1)] = token;
                 }
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (k < mine) {
-                    out.z[4 * lane + k + place[k]] = cur.z[k];
-                    out.token[4 * lane + k + place[k]] = cur.token[k];
+                    const int at = (e + k + lo + place[k]) & (kRing - 1);
+                    out.z[at] = cur.z[k];
+                    out.token[at] = cur.token[k];
                 }
             __syncwarp();
-            const int total = cnt + few;
-            int pid[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                pid[u] = page_id(otab, min(i + lo + u * 32 + lane, M + C - 1), c.psh);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int o = u * 32 + lane;
-                if (o < total) put(pid[u], i + lo + o, out.z[o], out.token[o]);
-            }
-            if (kStep + lane < total) {
-                const int o = kStep + lane, e = i + lo + o;
-                put(page_id(otab, e, c.psh), e, out.z[o], out.token[o]);
-            }
+            flush(i + lo + cnt + few, false);
             __syncwarp();
         } else {                                           // many: by binary search
             if (in == kFull) hi = last ? C : run.below(zn, lo, C);
+            flush(i + lo, true);
+            __syncwarp();
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (k < mine) {
@@ -391,6 +415,7 @@ cache_order_kernel(Cache c, const float *__restrict__ k_pages, K *codes, int32_t
                 }
                 put(page_id(otab, i + j + a, c.psh), i + j + a, (K)z, M + run.place(j));
             }
+            head = i + cnt + hi;
             __syncwarp();
         }
         lo = hi;
@@ -401,6 +426,7 @@ cache_order_kernel(Cache c, const float *__restrict__ k_pages, K *codes, int32_t
         if (i >= i1) break;
         turn(two, one);
     }
+    if (i0 < i1) flush(min(i, M) + lo, true);
     if (lost) set_status(status, ZETA_ERR_BOUNDS);
 }
 
