@@ -19,15 +19,16 @@
 // lane) with the next ones on their way: the run entries that fall among them are
 // found from where the last ones ended, counted into the old entries' places (one
 // by one, or by binary search where there are many), and old and new go out
-// through a stage in shared memory, so that the stores are whole sectors.  Several
+// through a ring in shared memory, so that the stores are whole 16-byte quads.  Several
 // blocks share a slice when there are few slices; each sorts the run for itself,
 // which costs less than a second launch and a round trip of the run through memory.
 //
 // 27 of 32 sequences completing a chunk of 1024 under prefixes of 36 K entries on
-// average, 8 heads: 67 us for 128 MB, 1.9 TB/s; one sequence, 64 K entries, 8 heads:
-// 10.5 us, the chain of sort, search and one or two steps.  Bound by issue (64 % of the
-// slots, 147 instructions an entry with the sorts) and behind it the loads.  A bitonic
-// sort and a merge of the entries one by one took 190 and 38 us.
+// average, 8 heads: 57 us for 128 MB, 2.2 TB/s; one sequence, 64 K entries, 8 heads:
+// 9.9 us, the chain of sort, search and one or two steps.  Bound by issue (61 % of the
+// slots, 119 instructions for an entry of each lane with the sorts) and behind it the
+// loads.  Stores entry by entry took 67 us, a bitonic sort and a merge of the entries
+// one by one 190 and 38 us.
 #include "cache.cuh"
 
 namespace zeta {
@@ -35,7 +36,8 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kStep = 128;              // old entries a warp takes at a time
-constexpr int kFew = 8;                 // run entries among them up to which they go one by one
+constexpr int kFew = 16;                // run entries among them up to which they go one by one
+                                        // (64 sequences under 32 K entries 65 us; 8: 68, 5: 74)
 constexpr int kCrowd = 48;              // keys of a bucket above which the bitonic sort runs
 constexpr int kLocBits = 13;            // a place in the chunk: C <= 8192
 
@@ -450,9 +452,10 @@ cudaError_t run_order(const Prob &p, const Cache &c, const float *k_pages, void 
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most_smem);
     });
     if (e != cudaSuccess) return e;
-    // Blocks per slice: enough for two on each of the 152 SMs (what fits at once); the
-    // kernel leaves out those that its prefix has no entries for.
-    int64_t g = (152 * 2 + p.S - 1) / p.S;
+    // Blocks per slice: as many as fit at once, two on each of the 152 SMs; the kernel
+    // leaves out those that its prefix has no entries for.  (Rounded up instead, 16
+    // sequences under 64 K entries take 44 us instead of 36, 32 under 36 K 56 instead of 57.)
+    int64_t g = 152 * 2 / p.S;
     const int64_t most = p.N / (kStep * kThreads / 32) + 1;
     g = g < most ? g : most;
     const dim3 grid((unsigned)(g < 1 ? 1 : g), (unsigned)p.S);
