@@ -25,8 +25,8 @@
 //
 // 27 of 32 sequences completing a chunk of 1024 under prefixes of 36 K entries on
 // average, 8 heads: 57 us for 128 MB, 2.2 TB/s; one sequence, 64 K entries, 8 heads:
-// 9.9 us, the chain of sort, search and one or two steps.  Bound by issue (61 % of the
-// slots, 119 instructions for an entry of each lane with the sorts) and behind it the
+// 9.9 us, the chain of sort, search and one or two steps.  Bound by issue (58 % of the
+// slots, 101 instructions for an entry of each lane with the sorts) and behind it the
 // loads.  Stores entry by entry took 67 us, a bitonic sort and a merge of the entries
 // one by one 190 and 38 us.
 #include "cache.cuh"
