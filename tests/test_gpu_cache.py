@@ -642,3 +642,42 @@ def test_empty_calls():
     c.attend(x, torch.ones(2, device="cuda"), z, z, tb, v, torch.zeros(0, 2, 1, device="cuda"))
     torch.cuda.synchronize()
     assert int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("d_K,bits,page", [(3, 10, 64), (3, 10, 2), (3, 12, 4), (2, 21, 1),
+                                           (8, 8, 16)])
+@pytest.mark.parametrize("B", [3, 40])
+def test_order_of_many_short_chunks(d_K, bits, page, B):
+    """Runs of 64 keys into prefixes of up to 8128 entries, many steps a warp: keys all
+    over the box (a few among 128 old entries), in one corner of it (many) and equal."""
+    H, C, N = 8, 64, 8192
+    width = N // page
+    cache = ZetaCache.empty(B * width, page, H, d_K, 8, N, C, 8, bits)
+    gen = torch.Generator(device="cuda").manual_seed(page)
+    table = torch.randperm(B * width, device="cuda", generator=gen).int().view(B, width)
+    k = torch.rand(B, H, N // C, C, d_K, device="cuda", generator=gen) * 2 - 1
+    k[:, :, 1::3] = k[:, :, 1::3] * 0.02 + 0.5
+    k[:, :, 5::9] = k[:, :, 5::9, :1].clone()
+    k = k.view(B, H, N, d_K).contiguous()
+    v = torch.zeros(B, H, N, 8, dtype=torch.bfloat16, device="cuda")
+    p = zb.zeta_problem_t(B, H, N, d_K, 8, 8, C, bits, zb.ZETA_BF16, 0)
+    codes = torch.empty(B, H, N, dtype=zb.code_dtype(p), device="cuda")
+    zb.zeta_encode(p, k, codes)
+    key = codes.cpu().numpy().view(np.uint64 if codes.dtype == torch.int64 else np.uint32)
+    count = torch.full((B,), C, dtype=torch.int32, device="cuda")
+    rows = table.long().repeat_interleave(page, 1), torch.arange(N, device="cuda") % page
+    for c in range(N // C):
+        start = torch.full((B,), c * C, dtype=torch.int32, device="cuda")
+        at = slice(c * C, c * C + C)
+        cache.append(k[:, :, at].contiguous(), v[:, :, at].contiguous(), start, count, table)
+        cache.order(start, count, table)
+        if c % 25 != 2 and c < N // C - 2:
+            continue
+        M = c * C + C
+        for got, want in ((cache.order_idx, None), (cache.order_codes, key)):
+            got = got[(c + 1) & 1][rows[0][:, :M], :, rows[1][:M]]      # [B, M, H]
+            got = got.permute(0, 2, 1).contiguous().cpu().numpy()
+            order = np.argsort(key[:, :, :M], axis=2, kind="stable")
+            want = order if want is None else np.take_along_axis(want[:, :, :M], order, 2)
+            assert np.array_equal(got.view(want.dtype) if want is not order else got, want), c
+    assert int(cache.status.item()) == 0
