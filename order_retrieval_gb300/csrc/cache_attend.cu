@@ -548,10 +548,10 @@ cudaError_t launch_cache_attend(const Prob &p, const Cache &c, const float *q, c
     const Args g{c, q, gamma, k_pages, order_idx, rowsum, idx, status,
                  p.N, p.H, p.dK, p.dV, p.k, p.C, p.bits, p.wk};
     // Many rows per sequence share their own chunk's tiles.  Measured against the row
-    // kernel, which reads the own chunk once per row: 8 sequences of 16 rows (C 1024) 24
-    // against 16 us, of 64 rows 23 against 38; 64 of 8 rows 50 against 49, of 16 rows 59
-    // against 82; C 256, 64 of 16 rows 40 against 41.
-    const bool tile = c.n >= 8 && p.S * c.n * p.C > (int64_t)1 << 21;
+    // kernel, which reads the own chunk once per row (8 heads, C 1024): 8 sequences of 16
+    // rows 18 against 15 us, 16 of 16 rows 24 against 21, 32 of 8 rows 26 against 33, 64 of
+    // 5 rows 42 against 36, of 8 rows 44 against 48, of 16 rows 49 against 82.
+    const bool tile = c.n >= 8 && p.S * c.n * p.C >= (int64_t)1 << 21;
     if (tile && p.vdt == ZETA_BF16 && p.dV % 8 == 0 && p.dV <= 128 && p.dK <= 4) {
         const TileArgs t{c, q, gamma, k_pages, static_cast<const __nv_bfloat16 *>(v_pages),
                          order_codes, order_idx, static_cast<__nv_bfloat16 *>(out), rowsum, idx,
