@@ -7,11 +7,12 @@
 //    shared memory; a warp finds a row's block there and its rank among the
 //    block's entries with one coalesced read of up to 64.
 //  * Own chunk: key tiles staged by cp.async through the page table into
-//    swizzled shared memory; weights are built straight in mma A fragments and
-//    rounded to bf16 once, two keys of a row to an instruction (the coordinates are
-//    staged apart, so that a pair of keys is one operand); products accumulate in
-//    float32, row sums come from the unrounded weights.  NW / WM warps split each
-//    tile's keys and join at the end.
+//    swizzled shared memory; weights are built straight in mma A fragments, two keys of
+//    a row to an instruction (the coordinates are staged apart, so that a pair of keys
+//    is one operand).  A weight enters as a bf16 half and the bf16 of what that leaves,
+//    two products into one float32 accumulator: within 2^-16 of the weight, so that a
+//    row's result does not tell which kernel the size of its batch chose.  Row sums come
+//    from the float32 weights.  NW / WM warps split each tile's keys and join at the end.
 //  * Window: a warp takes two rows at a time; their entries are looked up and weighed
 //    a lane each, the four dependent lookups of the next two rows run between the
 //    batches of value rows of these two, which are streamed and summed on the FMA
@@ -95,6 +96,12 @@ __device__ __forceinline__ float2 weight_pair(float2 d2, float m, float2 ig2) {
     } else {
         return weight_fast2<WK>(d2, dup2(m), ig2);
     }
+}
+
+// What two weights' bf16 halves (pack_bf16) leave of them, as bf16 again.
+__device__ __forceinline__ uint32_t pack_rest(float2 w, uint32_t half) {
+    const float2 r = sub2(w, make_float2(__uint_as_float(half << 16), __uint_as_float(half & 0xffff0000u)));
+    return pack_bf16(r.x, r.y);
 }
 
 __device__ __forceinline__ uint64_t order_code(const TileArgs &g, int64_t at) {
@@ -418,7 +425,7 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
 #pragma unroll
         for (int ks = 0; ks < KN; ++ks) {
             const int kb = kb0 + ks * 16;
-            uint32_t a[4];
+            uint32_t a[4], rest[4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int kl = kb + e * 8 + 2 * tig;
@@ -430,6 +437,8 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
                 sb2 = add2(sb2, wb);
                 a[2 * e] = pack_bf16(wa.x, wa.y);
                 a[2 * e + 1] = pack_bf16(wb.x, wb.y);
+                rest[2 * e] = pack_rest(wa, a[2 * e]);
+                rest[2 * e + 1] = pack_rest(wb, a[2 * e + 1]);
             }
             const int m = lane >> 3, key = kb + (m & 1) * 8 + (lane & 7);
 #pragma unroll
@@ -439,6 +448,8 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
                     ldsm_x4_trans(b, vbase + (uint32_t)(key * DVP + (((n2 * 2 + (m >> 1)) ^ (key & 7)) * 8)) * 2u);
                     mma16816(acc[2 * n2], a, b[0], b[1]);
                     mma16816(acc[2 * n2 + 1], a, b[2], b[3]);
+                    mma16816(acc[2 * n2], rest, b[0], b[1]);
+                    mma16816(acc[2 * n2 + 1], rest, b[2], b[3]);
                 }
             }
         }
