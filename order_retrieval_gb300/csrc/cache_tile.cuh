@@ -79,7 +79,6 @@ struct TileSmem {
     float swin[TQ], mwin[TQ];
     float lsum[NW][16], lmin[NW][16];  // the key splits' row sums and shifts
     int wst[TQ];                       // window start of a row
-    int bad;                           // a key of the own chunk has no page
 };
 
 // Weights of two keys (the reciprocals by the approximate instructions, 1 ulp).
@@ -200,23 +199,23 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
     auto order_row = [&](int id, int e) { return row_in(id, e, h, g.H, g.c.psh, g.c.pmask, g.c.opages); };
     auto pool_row = [&](int id, int t) { return row_in(id, t, h, g.H, g.c.psh, g.c.pmask, g.c.pages); };
 
-    if (tid == 0) sm.bad = 0;
-    __syncthreads();
     // Own-chunk tiles: keys cC .. last row's position (they all exist).
     const int kend = seq.start + f0 + nq - cC;               // keys of the chunk that matter
     const int nkt = (kend + TK - 1) / TK;
     auto ask_rows = [&](int kt) {                            // page of the thread's key of tile kt
         return tid < TK && kt * TK + tid < kend ? page_id(ptab, cC + kt * TK + tid, g.c.psh) : -1;
     };
+    bool lost_key = false;                                   // this thread met a key without a page
     auto put_rows = [&](int kt, int id) {                    // its pool row, for every thread to see
         if (tid < TK && kt < nkt) {
             const int row = pool_row(id, cC + kt * TK + tid);
             if (row < 0 && kt * TK + tid < kend) {
                 set_status(g.status, ZETA_ERR_BOUNDS);
-                sm.bad = 1;
+                lost_key = true;
             }
             sm.rows[kt & 3][tid] = row;
         }
+        __syncwarp();                                        // one branch again before the products
     };
     const int ppr = g.dV >> 3;                               // 16-byte pieces per value row
     auto load_tile = [&](int kt) {                           // into stage kt % 3, asynchronously
@@ -652,13 +651,15 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
     using KSteps = std::integral_constant<int, TK / 16 / KS>;   // this warp's steps per tile
     for (int kt = 0; kt < nkt; ++kt) {
         cp_async_wait<1>();
-        __syncthreads();                                     // tile kt is here, kt - 1 used up
+        // Tile kt is here, kt - 1 used up.  The barrier tells every thread alike whether a
+        // key up to tile kt + 2 has no page: the branch below holds warp-wide instructions.
+        const bool lost = __syncthreads_or(lost_key);
         load_tile(kt + 2);
         put_rows(kt + 3, kid);
         kid = ask_rows(kt + 4);
         const int key0 = kt * TK, bf = kt % 3, kb = kg * KSteps::value * 16;
         if (key0 + kb <= wmax) {                             // else every weight of this warp is 0
-            if (!sm.bad && key0 + TK - 1 <= wmin) {
+            if (!lost && key0 + TK - 1 <= wmin) {
                 steps(KSteps{}, &sm.own.k[bf][0][0], TK, sm.own.v[bf], kb,
                       [](auto, int, float2 x, float) { return x; });
             } else {
