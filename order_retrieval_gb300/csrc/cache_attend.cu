@@ -107,8 +107,12 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
-// Barrier of the first `n` threads, the warps that take the own chunk.
-__device__ __forceinline__ void bar_own(int n) { asm volatile("bar.sync 1, %0;\n" ::"r"(n) : "memory"); }
+// Barrier of the first `n` threads, the warps that take the own chunk.  It is one for
+// whole warps: lanes that recorded a missing page meet the others first.
+__device__ __forceinline__ void bar_own(int n) {
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;\n" ::"r"(n) : "memory");
+}
 
 // Entries of the prefix with a code <= z: a warp probes 32 per step.  (64, 128 or 256
 // probes take a step less and no less time, and their sectors come out of the other

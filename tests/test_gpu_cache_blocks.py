@@ -77,3 +77,34 @@ def test_pages_out_of_range_in_the_own_chunk(kw, weight):
 
     in_threads(one, [(b, t) for b in [*range(5), w.B - 1]
                      for t in (0, 15, 16, 63, 64, 100, 271, 290, 300, 495, 511)])
+
+
+@WEIGHTS
+@pytest.mark.parametrize("B,v_dtype", [(2, "bf16"), (2, "f32"), (600, "bf16")])
+def test_pages_out_of_range_under_single_tokens(B, v_dtype, weight):
+    """The row kernel, a cluster of blocks a token and one block a token: half a warp's
+    lanes meet a missing page in the own chunk, more than one segment of 1024 keys long."""
+    w = _work(B=2, H=2, N=4096, C=2048, k=24, v_dtype=v_dtype, gamma=(0.3, 1.0))
+    sv = Serving(w, 16, weight)
+    sv.step([2048] * 2)
+    sv.step([1500] * 2)
+    gone = {0: set(), 1: set()}
+    bad = sv.table.clone()
+    for b, t in ((0, 2048), (0, 2048 + 1040), (1, 2048 + 1488), (1, 304)):
+        bad[b, t // 16] = -1 if b else 10 ** 6
+        gone[b] |= set(range(t, t + 16))
+    start, count, q, k, v = sv.batch([1, 1], 1)
+    sv.cache.append(k, v, start, count, sv.table)
+    many = [x.repeat(B // 2, *[1] * (x.dim() - 1)) for x in (q, start, count, bad, sv.table)]
+    out = torch.full((B, w.H, 1, w.d_V), PAD, dtype=sv.vdt, device="cuda")
+    rs = torch.full((B, w.H, 1), PAD, device="cuda")
+    sv.cache.attend(many[0], sv.gamma, many[1], many[2], many[3], out, rs, many[4])
+    assert int(sv.cache.status.item()) == 6
+    for x in (out, rs):                                     # copies of two rows
+        assert torch.equal(x.view(B // 2, 2, -1), x[:2].reshape(1, 2, -1).expand(B // 2, -1, -1))
+    out, rs = out.double().cpu().numpy(), rs.cpu().numpy()
+    for b in range(2):
+        for h in range(w.H):
+            o, s, bo, bs = rows_without(sv, b, h, 3548, gone[b], weight)
+            assert abs(rs[b, h, 0] - s) <= bs
+            assert (np.abs(out[b, h, 0] - o) <= bo).all()
