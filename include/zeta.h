@@ -377,7 +377,8 @@ zeta_status_t zeta_attend_bwd(const zeta_problem_t *p, const float *q, const flo
  *
  * One step: zeta_cache_append, zeta_cache_order (needed in the calls in which
  * some sequence completes a chunk, a no-op for the others), zeta_cache_attend,
- * on one stream, with the same start and count.  As n <= C a call completes at
+ * on one stream, with the same n, start and count (another n would let one call
+ * take a sequence that another one skips).  As n <= C a call completes at
  * most one chunk per sequence, and the two planes hold the prefixes of both
  * chunks that its tokens lie in.
  *

@@ -144,10 +144,10 @@ class ZetaCache:
     Tables are int32 [B, table_len]: token t of sequence b is row t % page of page
     table[b, t // page]; which pages a sequence gets is the caller's business.
     Per step and batch, with the same start and count (int32 [B], tokens before
-    the step and tokens brought, count <= n <= C)::
+    the step and tokens brought, count <= n <= C; n is the rows of k, v and q)::
 
         cache.append(k, v, start, count, table)
-        cache.order(start, count, table)          # when a sequence completes a chunk
+        cache.order(start, count, table, n=n)     # when a sequence completes a chunk
         cache.attend(q, gamma, start, count, table, out, rowsum)
 
     The prefixes of completed chunks are kept in the order pools through
@@ -271,13 +271,16 @@ class ZetaCache:
                     take(page_table, "page_table", i32, (B, width)), self._kp, self._vp),
                    dev_status, stream)
 
-    def order(self, start, count, page_table, order_table=None, dev_status=None, stream=None):
-        """The sorted prefix of every sequence that completes a chunk with these tokens."""
+    def order(self, start, count, page_table, order_table=None, dev_status=None, stream=None,
+              n=None):
+        """The sorted prefix of every sequence that completes a chunk with these tokens.  n: the
+        step's rows per sequence (default C, the most there can be); a sequence that brings
+        more of them than that is skipped, as append and attend skip it."""
         B, width = self._table(page_table)
         take, i32 = self._take, torch.int32
         tp = take(page_table, "page_table", i32, (B, width))
         op = tp if order_table is None else take(order_table, "order_table", i32, (B, width))
-        self._call("zeta_cache_order", self._sizes(B, self.C, width),
+        self._call("zeta_cache_order", self._sizes(B, self.C if n is None else n, width),
                    (take(start, "start", i32, (B,)), take(count, "count", i32, (B,)), tp, self._kp,
                     op, self._ocp, self._oip), dev_status, stream)
 
