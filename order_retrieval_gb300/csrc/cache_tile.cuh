@@ -81,6 +81,12 @@ struct TileSmem {
     int wst[TQ];                       // window start of a row
 };
 
+// The 4-byte form of cp_async16, for single coordinates.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int src_bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src),
+                 "r"(src_bytes));
+}
+
 // Weights of two keys (the reciprocals by the approximate instructions, 1 ulp).
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
