@@ -155,7 +155,9 @@ class ZetaCache:
     Everything is enqueued on the given or current stream and allocates nothing,
     so a step can be captured into a CUDA graph.  Findings of the kernels (a
     length or page out of range) go to ``status``, one int32 word, unless
-    dev_status is given.  There is no backward.
+    dev_status is given.  There is no backward.  Pools and sizes are those the cache was
+    made with: they cannot be assigned, and a pool whose memory changes in place is taken
+    as it then lies, or refused where it no longer fits.
     """
 
     def __init__(self, k_pages, v_pages, order_codes, order_idx, N: int, C: int, k: int,
@@ -179,16 +181,32 @@ class ZetaCache:
             raise ValueError("ZETA tensors must be CUDA tensors")
         self._index = self.device.index
         self._vt = v_pages.dtype
-        self._kp = self._take(k_pages, "k_pages", torch.float32, tuple(k_pages.shape))
-        self._vp = self._take(v_pages, "v_pages", self._vt, tuple(v_pages.shape))
-        self._ocp = self._take(order_codes, "order_codes", zb.code_dtype(p), shape)
-        self._oip = self._take(order_idx, "order_idx", torch.int32, shape)
         self.k_pages, self.v_pages = k_pages, v_pages
         self.order_codes, self.order_idx = order_codes, order_idx
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
-        self._status_ptr = self.status.data_ptr()
-        self._lib = zb.lib()
+        self._pools = ((k_pages, "k_pages", torch.float32, tuple(k_pages.shape)),
+                       (v_pages, "v_pages", self._vt, tuple(v_pages.shape)),
+                       (order_codes, "order_codes", zb.code_dtype(p), shape),
+                       (order_idx, "order_idx", torch.int32, shape),
+                       (self.status, "status", torch.int32, (1,)))
+        self._where = tuple(t.data_ptr for t, *_ in self._pools)
+        self._ptrs = tuple(self._take(*x) for x in self._pools)
         self._structs = {}
+        self._lib = zb.lib()
+
+    def __setattr__(self, name, value):
+        # The structs of earlier calls and captured graphs hold the pools and sizes.
+        if "_lib" in self.__dict__:
+            raise AttributeError(f"{name}: a ZetaCache keeps the pools and sizes it was made "
+                                 "with; make another one")
+        super().__setattr__(name, value)
+
+    def _memory(self):
+        """Pointers of the four pools and the status word as they lie now; checked anew where
+        one has moved."""
+        a, b, c, d, e = self._where
+        now = a(), b(), c(), d(), e()
+        return now if now == self._ptrs else tuple(self._take(*x) for x in self._pools)
 
     @classmethod
     def empty(cls, pages: int, page: int, H: int, d_K: int, d_V: int, N: int, C: int, k: int,
@@ -239,19 +257,25 @@ class ZetaCache:
         return t.data_ptr()
 
     def _table(self, t):
-        if t.dim() != 2:
+        """Pointer and both sizes of a page table."""
+        shape = t.shape
+        if len(shape) != 2:
             raise ValueError(f"page_table: {t.dim()} dimensions, expected 2")
-        return t.shape
+        if (t.dtype is torch.int32 and t.get_device() == self._index and t.is_contiguous()
+                and not t.requires_grad):
+            return t.data_ptr(), *shape
+        return self._take(t, "page_table", torch.int32, shape), *shape
 
-    def _call(self, fn, pc, args, dev_status, stream):
-        st = self._status_ptr if dev_status is None else self._take(dev_status, "dev_status",
-                                                                    torch.int32, (1,))
+    def _call(self, fn, pc, args, status, dev_status, stream):
+        st = status if dev_status is None else self._take(dev_status, "dev_status", torch.int32,
+                                                          (1,))
+        c = torch._C
         if stream is None:
-            stream = torch._C._cuda_getCurrentRawStream(self._index)
+            stream = c._cuda_getCurrentRawStream(self._index)
         elif not isinstance(stream, int):
             stream = stream.cuda_stream
         f = getattr(self._lib, fn)
-        if torch._C._cuda_getDevice() == self._index:
+        if c._cuda_getDevice() == self._index:
             code = f(*pc, *args, st, stream)
         else:
             with torch.cuda.device(self._index):
@@ -262,41 +286,41 @@ class ZetaCache:
     def append(self, k, v, start, count, page_table, dev_status=None, stream=None):
         """k f32 [B,H,n,d_K], v [B,H,n,d_V]: rows 0 .. count[b]-1 of sequence b become its
         tokens start[b] .. start[b]+count[b]-1."""
-        B, width = self._table(page_table)
+        tp, B, width = self._table(page_table)
         n, take, i32 = k.shape[2], self._take, torch.int32
+        kp, vp, _, _, st = self._memory()
         self._call("zeta_cache_append", self._sizes(B, n, width),
                    (take(k, "k", torch.float32, (B, self.H, n, self.d_K)),
                     take(v, "v", self._vt, (B, self.H, n, self.d_V)),
                     take(start, "start", i32, (B,)), take(count, "count", i32, (B,)),
-                    take(page_table, "page_table", i32, (B, width)), self._kp, self._vp),
-                   dev_status, stream)
+                    tp, kp, vp), st, dev_status, stream)
 
     def order(self, start, count, page_table, order_table=None, dev_status=None, stream=None,
               n=None):
         """The sorted prefix of every sequence that completes a chunk with these tokens.  n: the
         step's rows per sequence (default C, the most there can be); a sequence that brings
         more of them than that is skipped, as append and attend skip it."""
-        B, width = self._table(page_table)
+        tp, B, width = self._table(page_table)
         take, i32 = self._take, torch.int32
-        tp = take(page_table, "page_table", i32, (B, width))
         op = tp if order_table is None else take(order_table, "order_table", i32, (B, width))
+        kp, _, ocp, oip, st = self._memory()
         self._call("zeta_cache_order", self._sizes(B, self.C if n is None else n, width),
-                   (take(start, "start", i32, (B,)), take(count, "count", i32, (B,)), tp, self._kp,
-                    op, self._ocp, self._oip), dev_status, stream)
+                   (take(start, "start", i32, (B,)), take(count, "count", i32, (B,)), tp,
+                    kp, op, ocp, oip), st, dev_status, stream)
 
     def attend(self, q, gamma, start, count, page_table, out, rowsum, order_table=None, idx=None,
                dev_status=None, stream=None):
         """q f32 [B,H,n,d_K], gamma f32 [H] -> out [B,H,n,d_V], rowsum f32 [B,H,n] and, where
         given, idx int32 [B,H,n,k]; rows count[b] .. n-1 stay as they were."""
-        B, width = self._table(page_table)
+        tp, B, width = self._table(page_table)
         H, n, take, f32, i32 = self.H, q.shape[2], self._take, torch.float32, torch.int32
-        tp = take(page_table, "page_table", i32, (B, width))
         op = tp if order_table is None else take(order_table, "order_table", i32, (B, width))
+        kp, vp, ocp, oip, st = self._memory()
         self._call("zeta_cache_attend", self._sizes(B, n, width),
                    (take(q, "q", f32, (B, H, n, self.d_K)), take(gamma, "gamma", f32, (H,)),
                     take(start, "start", i32, (B,)), take(count, "count", i32, (B,)), tp,
-                    self._kp, self._vp, op, self._ocp, self._oip,
+                    kp, vp, op, ocp, oip,
                     take(out, "out", self._vt, (B, H, n, self.d_V)),
                     take(rowsum, "rowsum", f32, (B, H, n)),
                     None if idx is None else take(idx, "idx", i32, (B, H, n, self.k))),
-                   dev_status, stream)
+                   st, dev_status, stream)

@@ -3,7 +3,7 @@ when its pools change under it."""
 import pytest
 import torch
 
-from order_retrieval_gb300 import ZetaError
+from order_retrieval_gb300 import ZetaCache, ZetaError
 from test_gpu_cache import PAD, _fresh, _small
 
 pytestmark = [
@@ -59,3 +59,67 @@ def test_order_takes_the_step_rows():
             c.order(st, ct, sv.table, n=bad)
         assert e.value.code == code
     assert int(c.status.item()) == 0
+
+
+def _step(w, sv, c, n, table):
+    start, count, q, k, v = sv.batch([n, n], n)
+    out, rs = _fresh(w, n)
+    c.append(k, v, start, count, table)
+    c.order(start, count, table, n=n)
+    c.attend(q, sv.gamma, start, count, table, out, rs)
+    return out, rs
+
+
+@pytest.mark.parametrize("name", ["k_pages", "v_pages", "order_codes", "order_idx", "status", "k",
+                                  "C", "N", "bits", "pages"])
+def test_pools_and_sizes_cannot_be_assigned(name):
+    """An assigned pool used to be ignored: the calls went on with the old memory."""
+    c = ZetaCache.empty(4, 16, 2, 3, 64, 64, 32, 4)
+    old = getattr(c, name)
+    with pytest.raises(AttributeError):
+        setattr(c, name, old.clone() if torch.is_tensor(old) else old + 1)
+    assert getattr(c, name) is old
+
+
+@pytest.mark.parametrize("how", ["data", "set_"])
+def test_pools_that_move_are_followed(how):
+    """New memory under the same tensors, as they hold it at the call: outputs and pools are
+    those of a cache that stayed."""
+    w, sv, n = _small()
+    c = sv.cache
+    twin = ZetaCache(*_pools(c), w.N, w.C, w.k, w.bits)
+    kept = []
+    for t in (c.k_pages, c.v_pages, c.order_codes, c.order_idx, c.status):
+        kept.append(t.detach().view(t.shape))                # the old memory, still there
+        new = t.clone()
+        if how == "data":
+            t.data = new
+        else:
+            t.set_(new)
+        kept[-1].zero_()
+    got, want = _step(w, sv, c, n, sv.table), _step(w, sv, twin, n, sv.table)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for a, b in zip(_pools(c), _pools(twin)):
+        assert torch.equal(a, b)
+    assert int(c.status.item()) == 0
+    for t in kept:
+        assert not t.any()                                   # nobody wrote there
+
+
+def test_pools_that_no_longer_fit_are_refused():
+    """Released or resized memory is an error of the call, on the host."""
+    w, sv, n = _small()
+    c = sv.cache
+    c.v_pages.untyped_storage().resize_(0)
+    with pytest.raises(ZetaError) as e:                      # no memory: a null pointer
+        _step(w, sv, c, n, sv.table)
+    assert e.value.code == 1
+    w, sv, n = _small()
+    sv.cache.k_pages.data = sv.cache.k_pages[:2].clone()
+    with pytest.raises(ValueError):
+        _step(w, sv, sv.cache, n, sv.table)
+    w, sv, n = _small()
+    sv.cache.order_idx.data = sv.cache.order_idx.cpu()
+    with pytest.raises(ValueError):
+        _step(w, sv, sv.cache, n, sv.table)
+    torch.cuda.synchronize()
