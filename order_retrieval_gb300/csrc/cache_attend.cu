@@ -35,6 +35,8 @@
 // at the block's barriers.  59 sequences with 37 K tokens before each: 16 us, one row's
 // chain (rank search, window lookups, join) beside the longest own chunk, all blocks at
 // once.  One sequence, one head, a chunk of 128: 4.3 us.
+#include <cmath>
+
 #include <cooperative_groups.h>
 
 #include "cache_tile.cuh"
@@ -543,6 +545,39 @@ cudaError_t dispatch_rows(const Args &g, const Prob &p, const void *order_codes,
 #undef ZETA_ROWS
 }
 
+// How many groups of 16 rows a block of the tile kernel takes for up to n rows of each
+// of the S slices (0: the row kernel).  The row kernel reads the own chunk once per row;
+// the tile kernel reads it once per block, but a block takes long and there are fewer.
+// Measured, row kernel : blocks of 16 rows in us, with 8 heads, d_V 64 and windows of 64:
+//  * The tile kernel takes rows enough to share (n sqrt(C) >= 220): 256 sequences of 8
+//    rows 85 : 106 for C 256, of 4 rows 87 : 126 for C 1024, of 2 rows 185 : 241 for
+//    C 4096; but of 16 rows 156 : 119, of 8 rows 151 : 130, of 4 rows 293 : 243.
+//  * And enough in all to fill the SMs (S n sqrt(C) >= 55000): 4 sequences of 64 rows
+//    14.5 : 15.9 for C 256, of 32 rows 14.2 : 17.0 for C 1024, of 16 rows 33 : 39 for
+//    C 4096; of twice as many 27 : 17, 23.7 : 19.0, 60 : 40.
+//  * Values wider than 64, whose tiles are half as long, want more of both: 16 sequences
+//    of 16 rows 38 : 48 for C 1024, of 32 rows 30 : 51 for C 256; 64 of 16 104 : 81 for
+//    C 1024, 64 of 4 166 : 129 for C 4096.
+// Larger blocks share tiles and set-up among more rows.  They are taken where the smaller
+// ones would not all run at once (two blocks an SM, three for values wider than 64; half
+// as many again before 64 rows, more under long chunks, which are most of a block): C
+// 1024, 4 sequences of 128 rows 20 us in blocks of 16, 27 in blocks of 32, of 256 rows 43
+// and 33; 64 sequences of 128 rows 160 in blocks of 32, 146 of 64; C 4096, 16 of 128 rows
+// 81 and 108.  For wider values blocks of 32 gain up to 1.1 in large calls, 64 never did.
+// Over 552 cases (half of them drawn: C 128 to 8192, 1 to 256 sequences of 1 to 32 heads,
+// 2 to 1024 rows, d_V 32 to 128, d_K 1 to 4, all weights) this takes the fastest form or
+// one within 10 % in 523, and 1.3 times its time at worst.
+int tile_groups(const Prob &p, int n) {
+    const double root = std::sqrt((double)p.C), rows = (double)p.S * n;
+    const bool wide = p.dV > 64;
+    if (n * root < 220 || rows * root < 55000) return 0;
+    if (wide && n * rows * p.C * root < 1.5e9) return 0;
+    auto blocks = [&](int r) { return p.S * ((n + r - 1) / r); };
+    if (wide) return n >= 48 && blocks(16) > 152 * 3 ? 2 : 1;
+    if (n >= 48 && (double)blocks(32) > 152 * 3 * (p.C > 1024 ? p.C / 1024. : 1.)) return 4;
+    return n > 16 && blocks(16) > 152 * 2 ? 2 : 1;
+}
+
 }  // namespace
 
 cudaError_t launch_cache_attend(const Prob &p, const Cache &c, const float *q, const float *gamma,
@@ -551,21 +586,12 @@ cudaError_t launch_cache_attend(const Prob &p, const Cache &c, const float *q, c
                                 float *rowsum, int32_t *idx, int32_t *status, cudaStream_t st) {
     const Args g{c, q, gamma, k_pages, order_idx, rowsum, idx, status,
                  p.N, p.H, p.dK, p.dV, p.k, p.C, p.bits, p.wk};
-    // Many rows per sequence share their own chunk's tiles.  Measured against the row
-    // kernel, which reads the own chunk once per row (8 heads, C 1024): 8 sequences of 16
-    // rows 18 against 15 us, 16 of 16 rows 24 against 21, 32 of 8 rows 26 against 33, 64 of
-    // 5 rows 42 against 36, of 8 rows 44 against 48, of 16 rows 49 against 82.
-    const bool tile = c.n >= 8 && p.S * c.n * p.C >= (int64_t)1 << 21;
-    if (tile && p.vdt == ZETA_BF16 && p.dV % 8 == 0 && p.dV <= 128 && p.dK <= 4) {
+    const int wm = p.vdt == ZETA_BF16 && p.dV % 8 == 0 && p.dV <= 128 && p.dK <= 4
+                       ? tile_groups(p, c.n) : 0;
+    if (wm > 0) {
         const TileArgs t{c, q, gamma, k_pages, static_cast<const __nv_bfloat16 *>(v_pages),
                          order_codes, order_idx, static_cast<__nv_bfloat16 *>(out), rowsum, idx,
                          status, p.N, p.H, p.dK, p.dV, p.k, p.C, p.bits, p.wk, p.code64};
-        // Sixteen rows a block; 32 and 64, which share tiles and set-up, where that many
-        // rows fill the SMs: 8,192 rows of one piece 46, 38, 45 us; 64 sequences of 64 rows
-        // 112, 101, 103 us, of 128 rows 190, 159, 145 us; 16 pieces of up to 1024 rows 314,
-        // 243, 204 us; 8 sequences of 64 rows 23, 33, 43 us.
-        const int64_t rows = p.S * c.n;
-        const int wm = c.n >= 128 && rows >= 65536 ? 4 : c.n >= 32 && rows >= 152 * 48 ? 2 : 1;
         return p.dV <= 64 ? launch_cache_tile64(p, t, wm, st) : launch_cache_tile128(p, t, wm, st);
     }
     if (p.vdt == ZETA_BF16) {

@@ -48,7 +48,7 @@ struct TileArgs {
     int N, H, dK, dV, k, C, bits, wk, code64;
 };
 
-// wm: 1, 2 or 4, for 16 wm rows a block.
+// wm: 1, 2 or (up to 64 wide) 4, for 16 wm rows a block.
 cudaError_t launch_cache_tile64(const Prob &p, const TileArgs &g, int wm, cudaStream_t st);
 cudaError_t launch_cache_tile128(const Prob &p, const TileArgs &g, int wm, cudaStream_t st);
 
@@ -70,7 +70,7 @@ struct TileSmem {
     };
     union {
         Own own;
-        float join[WM * (NW / WM - 1) * 16 * (DVP + 4) + 1];
+        float join[WM * (NW / WM - 1) * 16 * (DVP + 4)];
     };
     uint64_t fence[kFences];
     Gather gather;
@@ -690,67 +690,66 @@ cache_tile_kernel(const __grid_constant__ TileArgs g) {
         sa += __shfl_xor_sync(kFull, sa, o);
         sb += __shfl_xor_sync(kFull, sb, o);
     }
-    if constexpr (KS > 1) {                                  // join the key splits in order
-        constexpr int PW = DVP + 4;
-        float *part = sm.join;                                      // [WM][KS - 1][16][PW]
-        const int slot = rg * (KS - 1) - 1;                         // + split, from 1
-        if (kg > 0) {
+    static_assert(KS > 1);                                   // join the key splits in order
+    constexpr int PW = DVP + 4;
+    float *part = sm.join;                                      // [WM][KS - 1][16][PW]
+    const int slot = rg * (KS - 1) - 1;                         // + split, from 1
+    if (kg > 0) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                if (nt < 2 * nc) {
-                    float *pa = part + ((slot + kg) * 16 + g4) * PW + nt * 8 + 2 * tig;
-                    pa[0] = acc[nt][0];
-                    pa[1] = acc[nt][1];
-                    pa[8 * PW] = acc[nt][2];
-                    pa[8 * PW + 1] = acc[nt][3];
-                }
-            if (tig == 0) {
-                sm.lsum[warp][g4] = sa;
-                sm.lsum[warp][g4 + 8] = sb;
-                sm.lmin[warp][g4] = mab.x;
-                sm.lmin[warp][g4 + 8] = mab.y;
+        for (int nt = 0; nt < NT; ++nt)
+            if (nt < 2 * nc) {
+                float *pa = part + ((slot + kg) * 16 + g4) * PW + nt * 8 + 2 * tig;
+                pa[0] = acc[nt][0];
+                pa[1] = acc[nt][1];
+                pa[8 * PW] = acc[nt][2];
+                pa[8 * PW + 1] = acc[nt][3];
             }
+        if (tig == 0) {
+            sm.lsum[warp][g4] = sa;
+            sm.lsum[warp][g4 + 8] = sb;
+            sm.lmin[warp][g4] = mab.x;
+            sm.lmin[warp][g4 + 8] = mab.y;
         }
-        __syncthreads();
-        if (kg > 0) return;
-        float2 mall = mab;
-        if constexpr (WK == kWSoftmax) {
-#pragma unroll
-            for (int w = 1; w < KS; ++w)
-                mall = make_float2(fminf(mall.x, sm.lmin[warp + w][g4]), fminf(mall.y, sm.lmin[warp + w][g4 + 8]));
-        }
-        auto factor = [&](float mo, float mn) {
-            if (WK != kWSoftmax || mo == mn) return 1.f;
-            return mo == INFINITY ? 0.f : __expf((mn - mo) * inv_g2);
-        };
-        const float f0a = factor(mab.x, mall.x), f0b = factor(mab.y, mall.y);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            acc[nt][0] *= f0a;
-            acc[nt][1] *= f0a;
-            acc[nt][2] *= f0b;
-            acc[nt][3] *= f0b;
-        }
-        sa *= f0a;
-        sb *= f0b;
-#pragma unroll
-        for (int w = 1; w < KS; ++w) {
-            const float fa = factor(sm.lmin[warp + w][g4], mall.x);
-            const float fb = factor(sm.lmin[warp + w][g4 + 8], mall.y);
-            sa = __fmaf_rn(fa, sm.lsum[warp + w][g4], sa);
-            sb = __fmaf_rn(fb, sm.lsum[warp + w][g4 + 8], sb);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                if (nt < 2 * nc) {
-                    const float *pa = part + ((slot + w) * 16 + g4) * PW + nt * 8 + 2 * tig;
-                    acc[nt][0] = __fmaf_rn(fa, pa[0], acc[nt][0]);
-                    acc[nt][1] = __fmaf_rn(fa, pa[1], acc[nt][1]);
-                    acc[nt][2] = __fmaf_rn(fb, pa[8 * PW], acc[nt][2]);
-                    acc[nt][3] = __fmaf_rn(fb, pa[8 * PW + 1], acc[nt][3]);
-                }
-        }
-        mab = mall;
     }
+    __syncthreads();
+    if (kg > 0) return;
+    float2 mall = mab;
+    if constexpr (WK == kWSoftmax) {
+#pragma unroll
+        for (int w = 1; w < KS; ++w)
+            mall = make_float2(fminf(mall.x, sm.lmin[warp + w][g4]), fminf(mall.y, sm.lmin[warp + w][g4 + 8]));
+    }
+    auto factor = [&](float mo, float mn) {
+        if (WK != kWSoftmax || mo == mn) return 1.f;
+        return mo == INFINITY ? 0.f : __expf((mn - mo) * inv_g2);
+    };
+    const float f0a = factor(mab.x, mall.x), f0b = factor(mab.y, mall.y);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        acc[nt][0] *= f0a;
+        acc[nt][1] *= f0a;
+        acc[nt][2] *= f0b;
+        acc[nt][3] *= f0b;
+    }
+    sa *= f0a;
+    sb *= f0b;
+#pragma unroll
+    for (int w = 1; w < KS; ++w) {
+        const float fa = factor(sm.lmin[warp + w][g4], mall.x);
+        const float fb = factor(sm.lmin[warp + w][g4 + 8], mall.y);
+        sa = __fmaf_rn(fa, sm.lsum[warp + w][g4], sa);
+        sb = __fmaf_rn(fb, sm.lsum[warp + w][g4 + 8], sb);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            if (nt < 2 * nc) {
+                const float *pa = part + ((slot + w) * 16 + g4) * PW + nt * 8 + 2 * tig;
+                acc[nt][0] = __fmaf_rn(fa, pa[0], acc[nt][0]);
+                acc[nt][1] = __fmaf_rn(fa, pa[1], acc[nt][1]);
+                acc[nt][2] = __fmaf_rn(fb, pa[8 * PW], acc[nt][2]);
+                acc[nt][3] = __fmaf_rn(fb, pa[8 * PW + 1], acc[nt][3]);
+            }
+    }
+    mab = mall;
     float fa = 1.f, fb = 1.f;                                // window sums onto the final shift
     if constexpr (WK == kWSoftmax) {
         const float wa = la >= 0 ? sm.mwin[la] : INFINITY, wb = lb >= 0 ? sm.mwin[lb] : INFINITY;

@@ -4,9 +4,7 @@
 namespace zeta {
 
 cudaError_t launch_cache_tile128(const Prob &p, const TileArgs &g, int wm, cudaStream_t st) {
-    if (wm == 1) return dispatch_tile<128, 1, 4>(p, g, st);
-    if (wm == 2) return dispatch_tile<128, 2, 4>(p, g, st);
-    return dispatch_tile<128, 4, 4>(p, g, st);
+    return wm == 1 ? dispatch_tile<128, 1, 4>(p, g, st) : dispatch_tile<128, 2, 4>(p, g, st);
 }
 
 }  // namespace zeta

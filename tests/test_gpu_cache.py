@@ -185,8 +185,8 @@ def test_pieces_then_tokens(kw, page):
     sv.check()
 
 
-# Pieces large enough for the tile kernel (sequences x heads x rows x C above 2^21),
-# 16 rows a block (5 x 2 x 512) and 128 (5 x 8 x 512), windows row by row and together.
+# Pieces large enough for the tile kernel, 32 rows a block (5 sequences of 2 heads) and 64
+# (of 8 heads); blocks of 16 are in test_gpu_cache_blocks.py.
 TILES = [
     dict(), dict(H=8), dict(d_V=40), dict(d_V=96, k=65), dict(d_V=128, H=8, k=100),
     dict(d_K=1, bits=21, d_V=32), dict(d_K=2, bits=21, H=8), dict(d_K=4, bits=8, d_V=128),

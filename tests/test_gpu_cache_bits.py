@@ -44,10 +44,11 @@ def sampled(w, first, count, seed):
     return set(rng.integers(first, w.N, count).tolist()) | {first, w.N - 1}
 
 
-# Sequences x heads x rows x C above 2^21, in blocks of 16, 32 (8 heads) and 64 rows
-# (16 sequences of 8 heads).
+# Pieces of 512 rows: blocks of 16 rows (8 slices), 32 (10 slices) and 64 (32 for values
+# wider than 64).
 @pytest.mark.parametrize("weight", ["cauchy", "softmax", "inv_euclid"])
-@pytest.mark.parametrize("kw", [dict(H=2), dict(H=8), dict(B=16, H=8), dict(B=16, H=8, d_V=128)],
+@pytest.mark.parametrize("kw", [dict(B=8, H=1), dict(B=8, H=1, d_V=128), dict(H=2), dict(B=16, H=8),
+                                dict(B=16, H=8, d_V=128)],
                          ids=lambda x: "-".join(f"{a}{b}" for a, b in x.items()))
 def test_large_pieces_keep_the_weights_bits(kw, weight):
     w = _work(**{**dict(B=5, N=1536, C=512, k=24, gamma=(0.3, 1.0)), **kw})
