@@ -164,6 +164,8 @@ class ZetaCache:
                  bits: int = 10, weight: str = "cauchy"):
         if k_pages.dim() != 4 or v_pages.dim() != 4 or k_pages.shape[:3] != v_pages.shape[:3]:
             raise ValueError("k_pages and v_pages must be [pages, H, page, d] of the same pages")
+        if order_codes.dim() != 4:
+            raise ValueError("order_codes must be [2, order_pages, H, page]")
         self.pages, self.H, self.page, self.d_K = k_pages.shape
         self.d_V = v_pages.shape[3]
         if v_pages.dtype not in (torch.bfloat16, torch.float32):
@@ -266,6 +268,13 @@ class ZetaCache:
             return t.data_ptr(), *shape
         return self._take(t, "page_table", torch.int32, shape), *shape
 
+    @staticmethod
+    def _rows(t, name):
+        try:
+            return t.shape[2]
+        except IndexError:
+            raise ValueError(f"{name}: {t.dim()} dimensions, expected 4") from None
+
     def _call(self, fn, pc, args, status, dev_status, stream):
         st = status if dev_status is None else self._take(dev_status, "dev_status", torch.int32,
                                                           (1,))
@@ -287,7 +296,7 @@ class ZetaCache:
         """k f32 [B,H,n,d_K], v [B,H,n,d_V]: rows 0 .. count[b]-1 of sequence b become its
         tokens start[b] .. start[b]+count[b]-1."""
         tp, B, width = self._table(page_table)
-        n, take, i32 = k.shape[2], self._take, torch.int32
+        n, take, i32 = self._rows(k, "k"), self._take, torch.int32
         kp, vp, _, _, st = self._memory()
         self._call("zeta_cache_append", self._sizes(B, n, width),
                    (take(k, "k", torch.float32, (B, self.H, n, self.d_K)),
@@ -313,7 +322,8 @@ class ZetaCache:
         """q f32 [B,H,n,d_K], gamma f32 [H] -> out [B,H,n,d_V], rowsum f32 [B,H,n] and, where
         given, idx int32 [B,H,n,k]; rows count[b] .. n-1 stay as they were."""
         tp, B, width = self._table(page_table)
-        H, n, take, f32, i32 = self.H, q.shape[2], self._take, torch.float32, torch.int32
+        H, n, take = self.H, self._rows(q, "q"), self._take
+        f32, i32 = torch.float32, torch.int32
         op = tp if order_table is None else take(order_table, "order_table", i32, (B, width))
         kp, vp, ocp, oip, st = self._memory()
         self._call("zeta_cache_attend", self._sizes(B, n, width),

@@ -123,3 +123,16 @@ def test_pools_that_no_longer_fit_are_refused():
     with pytest.raises(ValueError):
         _step(w, sv, sv.cache, n, sv.table)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dims", [(64,), (2, 64), (2, 4, 3), (2, 2, 4, 3, 1)])
+def test_rows_of_other_dimensions_are_refused(dims):
+    w, sv, n = _small()
+    st = torch.zeros(2, dtype=torch.int32, device="cuda")
+    x = torch.zeros(dims, device="cuda")
+    out, rs = _fresh(w, n)
+    v = torch.zeros(2, w.H, n, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        sv.cache.append(x, v, st, st, sv.table)
+    with pytest.raises(ValueError):
+        sv.cache.attend(x, sv.gamma, st, st, sv.table, out, rs)

@@ -2,10 +2,12 @@
 pointers is refused before a launch, or does not run where there is a GPU."""
 import ctypes
 
+import pytest
 import torch
 
 import conftest
 import test_cache_cpu as host
+from order_retrieval_gb300 import ZetaCache
 from order_retrieval_gb300 import binding as zb
 
 
@@ -52,3 +54,10 @@ def test_no_other_host_check_reaches_the_runtime(monkeypatch):
     host.test_null_and_unaligned_pointers(Spy())
     host.test_empty_calls_are_no_ops(Spy())
     assert seen and 4 not in seen
+
+
+def test_pools_of_other_dimensions_are_refused():
+    k, v = torch.zeros(4, 2, 16, 3), torch.zeros(4, 2, 16, 64)
+    for codes in (torch.zeros(8), torch.zeros(2, 4, 2)):
+        with pytest.raises(ValueError):
+            ZetaCache(k, v, codes, codes, 64, 32, 4)
