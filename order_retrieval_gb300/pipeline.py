@@ -23,6 +23,8 @@ import torch
 
 from . import binding as zb
 
+_C, _F32, _I32 = torch._C, torch.float32, torch.int32
+
 
 class ZetaPlan:
     def __init__(self, p: zb.zeta_problem_t, device="cuda", backward: bool = True,
@@ -160,6 +162,8 @@ class ZetaCache:
     as it then lies, or refused where it no longer fits.
     """
 
+    _lib = None                          # set last; from then on nothing else is
+
     def __init__(self, k_pages, v_pages, order_codes, order_idx, N: int, C: int, k: int,
                  bits: int = 10, weight: str = "cauchy"):
         if k_pages.dim() != 4 or v_pages.dim() != 4 or k_pages.shape[:3] != v_pages.shape[:3]:
@@ -193,12 +197,13 @@ class ZetaCache:
                        (self.status, "status", torch.int32, (1,)))
         self._where = tuple(t.data_ptr for t, *_ in self._pools)
         self._ptrs = tuple(self._take(*x) for x in self._pools)
+        self._heads = (self.H,)
         self._structs = {}
         self._lib = zb.lib()
 
     def __setattr__(self, name, value):
         # The structs of earlier calls and captured graphs hold the pools and sizes.
-        if "_lib" in self.__dict__:
+        if self._lib is not None:
             raise AttributeError(f"{name}: a ZetaCache keeps the pools and sizes it was made "
                                  "with; make another one")
         super().__setattr__(name, value)
@@ -228,16 +233,19 @@ class ZetaCache:
                                  self.v_dtype, self.flags)
 
     def _sizes(self, B: int, n: int, width: int):
-        """References to the C structs of a batch size, made once per (B, n, width) and
+        """References to the C structs of a batch size and the shapes its tensors have
+        ([B], [B,H,n], [B,H,n,d_K], [B,H,n,d_V], [B,H,n,k]), made once per (B, n, width) and
         never changed (a step costs the host a few microseconds, of which building them
         would be a good part)."""
         got = self._structs.get((B, n, width))
         if got is None:
             if len(self._structs) >= 1024:
                 self._structs.clear()
+            rows = (B, self.H, n)
             got = (ctypes.byref(self._problem(B)),
                    ctypes.byref(zb.zeta_cache_t(n, self.page, self.pages, self.order_pages,
-                                                width)))
+                                                width)),
+                   (B,), rows, (*rows, self.d_K), (*rows, self.d_V), (*rows, self.k))
             self._structs[B, n, width] = got
         return got
 
@@ -263,10 +271,10 @@ class ZetaCache:
         shape = t.shape
         if len(shape) != 2:
             raise ValueError(f"page_table: {t.dim()} dimensions, expected 2")
-        if (t.dtype is torch.int32 and t.get_device() == self._index and t.is_contiguous()
+        if (t.dtype is _I32 and t.get_device() == self._index and t.is_contiguous()
                 and not t.requires_grad):
             return t.data_ptr(), *shape
-        return self._take(t, "page_table", torch.int32, shape), *shape
+        return self._take(t, "page_table", _I32, shape), *shape
 
     @staticmethod
     def _rows(t, name):
@@ -275,33 +283,30 @@ class ZetaCache:
         except IndexError:
             raise ValueError(f"{name}: {t.dim()} dimensions, expected 4") from None
 
-    def _call(self, fn, pc, args, status, dev_status, stream):
-        st = status if dev_status is None else self._take(dev_status, "dev_status", torch.int32,
-                                                          (1,))
-        c = torch._C
+    def _call(self, f, args, status, dev_status, stream):
+        st = status if dev_status is None else self._take(dev_status, "dev_status", _I32, (1,))
         if stream is None:
-            stream = c._cuda_getCurrentRawStream(self._index)
+            stream = _C._cuda_getCurrentRawStream(self._index)
         elif not isinstance(stream, int):
             stream = stream.cuda_stream
-        f = getattr(self._lib, fn)
-        if c._cuda_getDevice() == self._index:
-            code = f(*pc, *args, st, stream)
+        if _C._cuda_getDevice() == self._index:
+            code = f(*args, st, stream)
         else:
             with torch.cuda.device(self._index):
-                code = f(*pc, *args, st, stream)
+                code = f(*args, st, stream)
         if code != 0:
-            raise zb.ZetaError(fn, code)
+            raise zb.ZetaError(f.__name__, code)
 
     def append(self, k, v, start, count, page_table, dev_status=None, stream=None):
         """k f32 [B,H,n,d_K], v [B,H,n,d_V]: rows 0 .. count[b]-1 of sequence b become its
         tokens start[b] .. start[b]+count[b]-1."""
         tp, B, width = self._table(page_table)
-        n, take, i32 = self._rows(k, "k"), self._take, torch.int32
+        p, c, per_seq, _, k_shape, v_shape, _ = self._sizes(B, self._rows(k, "k"), width)
+        take = self._take
         kp, vp, _, _, st = self._memory()
-        self._call("zeta_cache_append", self._sizes(B, n, width),
-                   (take(k, "k", torch.float32, (B, self.H, n, self.d_K)),
-                    take(v, "v", self._vt, (B, self.H, n, self.d_V)),
-                    take(start, "start", i32, (B,)), take(count, "count", i32, (B,)),
+        self._call(self._lib.zeta_cache_append,
+                   (p, c, take(k, "k", _F32, k_shape), take(v, "v", self._vt, v_shape),
+                    take(start, "start", _I32, per_seq), take(count, "count", _I32, per_seq),
                     tp, kp, vp), st, dev_status, stream)
 
     def order(self, start, count, page_table, order_table=None, dev_status=None, stream=None,
@@ -310,27 +315,27 @@ class ZetaCache:
         step's rows per sequence (default C, the most there can be); a sequence that brings
         more of them than that is skipped, as append and attend skip it."""
         tp, B, width = self._table(page_table)
-        take, i32 = self._take, torch.int32
-        op = tp if order_table is None else take(order_table, "order_table", i32, (B, width))
+        p, c, per_seq, *_ = self._sizes(B, self.C if n is None else n, width)
+        take = self._take
+        op = tp if order_table is None else take(order_table, "order_table", _I32, (B, width))
         kp, _, ocp, oip, st = self._memory()
-        self._call("zeta_cache_order", self._sizes(B, self.C if n is None else n, width),
-                   (take(start, "start", i32, (B,)), take(count, "count", i32, (B,)), tp,
-                    kp, op, ocp, oip), st, dev_status, stream)
+        self._call(self._lib.zeta_cache_order,
+                   (p, c, take(start, "start", _I32, per_seq), take(count, "count", _I32, per_seq),
+                    tp, kp, op, ocp, oip), st, dev_status, stream)
 
     def attend(self, q, gamma, start, count, page_table, out, rowsum, order_table=None, idx=None,
                dev_status=None, stream=None):
         """q f32 [B,H,n,d_K], gamma f32 [H] -> out [B,H,n,d_V], rowsum f32 [B,H,n] and, where
         given, idx int32 [B,H,n,k]; rows count[b] .. n-1 stay as they were."""
         tp, B, width = self._table(page_table)
-        H, n, take = self.H, self._rows(q, "q"), self._take
-        f32, i32 = torch.float32, torch.int32
-        op = tp if order_table is None else take(order_table, "order_table", i32, (B, width))
+        p, c, per_seq, rows, q_shape, v_shape, i_shape = self._sizes(B, self._rows(q, "q"), width)
+        take = self._take
+        op = tp if order_table is None else take(order_table, "order_table", _I32, (B, width))
         kp, vp, ocp, oip, st = self._memory()
-        self._call("zeta_cache_attend", self._sizes(B, n, width),
-                   (take(q, "q", f32, (B, H, n, self.d_K)), take(gamma, "gamma", f32, (H,)),
-                    take(start, "start", i32, (B,)), take(count, "count", i32, (B,)), tp,
-                    kp, vp, op, ocp, oip,
-                    take(out, "out", self._vt, (B, H, n, self.d_V)),
-                    take(rowsum, "rowsum", f32, (B, H, n)),
-                    None if idx is None else take(idx, "idx", i32, (B, H, n, self.k))),
+        self._call(self._lib.zeta_cache_attend,
+                   (p, c, take(q, "q", _F32, q_shape), take(gamma, "gamma", _F32, self._heads),
+                    take(start, "start", _I32, per_seq), take(count, "count", _I32, per_seq),
+                    tp, kp, vp, op, ocp, oip, take(out, "out", self._vt, v_shape),
+                    take(rowsum, "rowsum", _F32, rows),
+                    None if idx is None else take(idx, "idx", _I32, i_shape)),
                    st, dev_status, stream)
