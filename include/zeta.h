@@ -24,8 +24,8 @@
  *     (B*H*N == 0) is valid and launches nothing.
  *   - Code width: codes are uint32 when d_K*bits <= 32, else uint64.
  *   - Limits: 1 <= d_K <= 8, 1 <= bits <= 24, d_K*bits <= 64, C >= 1, C | N,
- *     1 <= k <= C, 1 <= d_V <= 256, N < 2^31; zeta_sort_chunks also needs
- *     N / C <= 1024.
+ *     1 <= k <= C, 1 <= d_V <= 256, N*k < 2^31, B*H <= 65535; zeta_sort_chunks
+ *     also needs N / C <= 1024.
  */
 #ifndef ZETA_H
 #define ZETA_H
@@ -350,6 +350,8 @@ zeta_status_t zeta_attend_bwd(const zeta_problem_t *p, const float *q, const flo
  * to n <= C new tokens per sequence (n = 1: one token each).  A prompt read in
  * pieces and the tokens that follow it get the outputs that zeta_attend_fwd
  * computes for the whole sequence: the same codes, prefixes, windows and weights.
+ * The cache holds the order along one curve, that of zeta_encode: selections over
+ * several curves (zeta_encode_curves) have no cached form.
  *
  *   p     B sequences in this call, H, d_K, d_V, k, C, bits, v_dtype, flags as
  *         everywhere; N is the longest sequence the cache holds (C | N).
@@ -360,8 +362,8 @@ zeta_status_t zeta_attend_bwd(const zeta_problem_t *p, const float *q, const flo
  *         table_len * page >= N.
  *   start, count   int32 [B] (device): tokens sequence b held before this call
  *         and tokens it brings (0 <= count <= n, start + count <= N).  Rows
- *         count[b] .. n-1 are padding: never read, and left as they were where
- *         they are outputs.  A sequence outside these ranges is skipped whole and
+ *         count[b] .. n-1 are padding: nothing depends on what they hold, and
+ *         they are left as they were where they are outputs.  A sequence outside these ranges is skipped whole and
  *         ZETA_ERR_BOUNDS recorded.
  *   page_table     int32 [B, table_len]: token t of sequence b is row t % page of
  *         page page_table[b][t / page].  Only entries of tokens that exist are
@@ -382,8 +384,8 @@ zeta_status_t zeta_attend_bwd(const zeta_problem_t *p, const float *q, const flo
  * most one chunk per sequence, and the two planes hold the prefixes of both
  * chunks that its tokens lie in.
  *
- * Limits beside those above: C <= 8192, B*H*n < 2^31, pages * H * page < 2^31
- * (order_pages likewise).  No call needs a workspace; calls on different
+ * Limits beside those above: C <= 8192, pages * H * page < 2^31 (order_pages
+ * likewise).  No call needs a workspace; calls on different
  * sequences may overlap on different streams.  The calls have no backward.
  */
 typedef struct {
@@ -431,6 +433,10 @@ zeta_status_t zeta_cache_order(const zeta_problem_t *p, const zeta_cache_t *cc,
  * The token at position i = start[b] + t, in chunk c = i / C, attends to the k
  * keys around its code's rank in prefix c (none for c = 0) and to the keys of
  * its own chunk up to itself; weights, out and rowsum as in zeta_attend_fwd.
+ * Weights and sums are float32.  For bf16 values large calls run products on the
+ * tensor cores, which take a weight as two bf16 parts, within 2^-16 of it; out is
+ * rounded once.  The same token in calls of different sizes so has the same rowsum
+ * to float32 roundings and the same out to one step of its type.
  *   q         in : float [B, H, n, d_K]
  *   gamma     in : float [H]
  *   k_pages, v_pages, order_codes, order_idx  in : after append and order

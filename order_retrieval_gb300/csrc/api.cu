@@ -53,8 +53,8 @@ zeta_status_t check_cache(const zeta_problem_t *pp, const zeta_cache_t *cc, Prob
         cc->order_pages < 0 || cc->table_len < 0)
         return ZETA_ERR_INVALID_ARG;
     if ((int64_t)cc->table_len * cc->page < pr->N) return ZETA_ERR_INVALID_ARG;
+    // (B*H <= 65535 and n <= C <= 8192: the rows of a call fit 31 bits.)
     if (cc->page > 65536 || cc->n > pr->C || pr->C > 8192) return ZETA_ERR_UNSUPPORTED;
-    if (pr->S * cc->n > INT32_MAX) return ZETA_ERR_UNSUPPORTED;
     const int64_t per = (int64_t)pr->H * cc->page;
     if (cc->pages * per > INT32_MAX || cc->order_pages * per > INT32_MAX)
         return ZETA_ERR_UNSUPPORTED;

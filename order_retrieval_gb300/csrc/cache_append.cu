@@ -8,8 +8,8 @@
 // as a long piece does.  A block takes whole rows, so that the row a thread works
 // for needs divisions of 32 bits only.
 //
-// 9,900 tokens in 16 sequences, 8 heads, 12 bytes a key and 128 a value: 7.5 us for
-// 22 MB, 3.0 TB/s (8.0 us with the pieces of all rows as one list and a division of
+// 9,900 tokens in 16 sequences, 8 heads, 12 bytes a key and 128 a value: 7.7 us for
+// 22 MB, 2.9 TB/s (8.0 us with the pieces of all rows as one list and a division of
 // 64 bits).  What bounds it is finding the row: four pieces a thread, loads ahead of
 // stores, took 10 us, for that arithmetic then has fewer warps to hide in.
 #include "cache.cuh"

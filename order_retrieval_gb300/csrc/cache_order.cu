@@ -23,12 +23,15 @@
 // blocks share a slice when there are few slices; each sorts the run for itself,
 // which costs less than a second launch and a round trip of the run through memory.
 //
-// 27 of 32 sequences completing a chunk of 1024 under prefixes of 36 K entries on
-// average, 8 heads: 57 us for 128 MB, 2.2 TB/s; one sequence, 64 K entries, 8 heads:
-// 9.9 us, the chain of sort, search and one or two steps.  Bound by issue (58 % of the
-// slots, 101 instructions for an entry of each lane with the sorts) and behind it the
-// loads.  Stores entry by entry took 67 us, a bitonic sort and a merge of the entries
-// one by one 190 and 38 us.
+// 27 of 32 sequences completing a chunk of 1024 under prefixes of 7 K to 62 K entries, 36 K
+// on average, 8 heads: 57 us for 128 MB, 2.2 TB/s; one sequence, 64 K entries, 8 heads:
+// 10 us, the chain of sort, search and one or two steps.  Bound by how the work is dealt:
+// with 256 slices in the call each prefix is one block's, and the 216 that have work lie
+// two to an SM on some of the 152.  The longest sequence alone takes 38 us, the longest
+// thirteen of the 27 take the whole 56, 27 equal prefixes of 35 K 47, of 61 K 65.  Within a
+// block it is issue (58 % of the slots over the call, 101 instructions for an entry of
+// each lane with the sorts; 64 registers, up to 40 bytes of spills).  Stores entry by entry
+// took 67 us, a bitonic sort and a merge of the entries one by one 190 and 38 us.
 #include "cache.cuh"
 
 namespace zeta {

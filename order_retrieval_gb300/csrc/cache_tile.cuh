@@ -24,11 +24,15 @@
 //    whose result is not finite is taken again, key by key, without the others.
 //
 // 16 pieces of up to 1024 rows (9,704 together), 8 heads, 19 K tokens before each on
-// average, C 1024, k 64, d_V 64: 208 us, where the bytes take 66 at the HBM rate and the
-// products 3.  The windows are 64 scattered value rows a row: with their keys and the
-// own chunks 1.05 GB come out of L2 (290 MB of it from DRAM), 5.0 TB/s, near the 5.4
-// that gathers of such rows reach by themselves; 45 % of the issue slots are used, with
-// two blocks of 8 warps an SM.  One piece of 1024 rows: 37 us, a block's latency.
+// average, C 1024, k 64, d_V 64: 213 us, where the bytes take 66 at the HBM rate and the
+// products 5.  The windows are 64 scattered value rows a row: with their keys and the
+// own chunks 1.04 GB come out of L2 (289 MB of it from DRAM), 4.9 TB/s; 46 % of the issue
+// slots are used, with two blocks of 8 warps an SM (128 registers, 48 to 128 bytes of
+// spills up to 64 wide; 168 and none above).  What bounds it is waiting: for the gathers,
+// and then for the own chunk, which starts when every window of the block is done.  It is
+// no ceiling of the machine: the training forward spends 1.6 to 1.8 ns a row on the same
+// work, this 2.7.  One piece of 1024 rows: 40 us, a block's latency.  d_K of 1 and 2 run the
+// form for four coordinates, the missing ones zero.
 #pragma once
 
 #include "cache.cuh"

@@ -141,7 +141,8 @@ class ZetaCache:
     k_pages f32 [pages, H, page, d_K], v_pages [pages, H, page, d_V],
     order_codes (the problem's code type) and order_idx (int32)
     [2, order_pages, H, page]; ``empty`` allocates them.  N: the longest
-    sequence (a multiple of C); C, k, bits, weight as for ``zeta_attention``.
+    sequence (a multiple of C); C, k, bits, weight as for ``zeta_attention`` with one
+    curve (selections over several curves have no cached form).
 
     Tables are int32 [B, table_len]: token t of sequence b is row t % page of page
     table[b, t // page]; which pages a sequence gets is the caller's business.
@@ -155,7 +156,9 @@ class ZetaCache:
     The prefixes of completed chunks are kept in the order pools through
     order_table (default: table; pass another one when sequences share K/V pages).
     Everything is enqueued on the given or current stream and allocates nothing,
-    so a step can be captured into a CUDA graph.  Findings of the kernels (a
+    so a step can be captured into a CUDA graph.  Weights and sums are float32; for bf16
+    values large calls take each weight as two bf16 parts (within 2^-16 of it), so that a
+    token's outputs in calls of different sizes agree to one step of bf16.  Findings of the kernels (a
     length or page out of range) go to ``status``, one int32 word, unless
     dev_status is given.  There is no backward.  Pools and sizes are those the cache was
     made with: they cannot be assigned, and a pool whose memory changes in place is taken
