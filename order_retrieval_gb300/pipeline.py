@@ -165,7 +165,10 @@ class ZetaCache:
     as it then lies, or refused where it no longer fits.
     """
 
-    _lib = None                          # set last; from then on nothing else is
+    _lib = None                          # set last; from then on these stay as they are
+    _FIXED = frozenset(("k_pages", "v_pages", "order_codes", "order_idx", "status", "pages",
+                        "order_pages", "page", "H", "d_K", "d_V", "N", "C", "k", "bits", "flags",
+                        "v_dtype", "device"))
 
     def __init__(self, k_pages, v_pages, order_codes, order_idx, N: int, C: int, k: int,
                  bits: int = 10, weight: str = "cauchy"):
@@ -206,7 +209,7 @@ class ZetaCache:
 
     def __setattr__(self, name, value):
         # The structs of earlier calls and captured graphs hold the pools and sizes.
-        if self._lib is not None:
+        if name in self._FIXED and self._lib is not None:
             raise AttributeError(f"{name}: a ZetaCache keeps the pools and sizes it was made "
                                  "with; make another one")
         super().__setattr__(name, value)

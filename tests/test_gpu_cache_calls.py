@@ -81,6 +81,21 @@ def test_pools_and_sizes_cannot_be_assigned(name):
     assert getattr(c, name) is old
 
 
+def test_a_cache_may_carry_what_its_user_adds():
+    class Named(ZetaCache):
+        def __init__(self, *args, **kw):
+            super().__init__(*args, **kw)
+            self.name = "one"
+
+    c = Named.empty(4, 16, 2, 3, 64, 64, 32, 4)
+    c.name = "two"
+    c.step = 1
+    c.step = 2
+    assert (c.name, c.step) == ("two", 2)
+    with pytest.raises(AttributeError):
+        c.order_pages = 8
+
+
 @pytest.mark.parametrize("how", ["data", "set_"])
 def test_pools_that_move_are_followed(how):
     """New memory under the same tensors, as they hold it at the call: outputs and pools are
