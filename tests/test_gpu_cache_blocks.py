@@ -199,12 +199,12 @@ def test_captured_largest_blocks():
 @WEIGHTS
 @pytest.mark.parametrize("d_V", [64, 128])
 def test_blocks_of_a_few_rows(d_V, weight):
-    """Up to seven rows of many sequences, which share their own chunk from a chunk of 1024
-    on: idle sequences, single rows and rows on both sides of a chunk's end."""
-    w = _large(B=32, H=8, N=3072, C=1024, d_V=d_V)
+    """Up to seven rows of many sequences under chunks of 1000, enough to share them: idle
+    sequences, single rows and rows on both sides of a chunk's end."""
+    w = _large(B=32, H=8, N=3000, C=1000, d_V=d_V)
     sv = Serving(w, 64, weight)
-    sv.step([1024] * 32)
-    sv.step([1020, 1019, 1021, 700] * 8, n=1024)
+    sv.step([1000] * 32)
+    sv.step([996, 995, 997, 700] * 8, n=1000)
     sv.got = [dict() for _ in range(32)]
     sv.step([7, 7, 0, 5, 1, 6, 7, 2] * 4, n=7)
     sv.check_order()
