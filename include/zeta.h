@@ -458,6 +458,120 @@ zeta_status_t zeta_cache_attend(const zeta_problem_t *p, const zeta_cache_t *cc,
                                 cudaStream_t stream);
 
 /*
+ * Drafting: a tree of guessed tokens per sequence and step.
+ *
+ * Sequence b holds start[b] tokens and brings count[b] <= n drafted ones, the nodes of a
+ * tree: node t hangs below node parent[b][t] < t, or below the sequence's last token
+ * (parent -1); its depth is that of its parent plus one, 0 at the top, and its position
+ * start[b] + depth.  Keys and values of the nodes stay in the step's own tensors.  One
+ * step, on one stream:
+ *   zeta_cache_reserve      pages for the longest line that may be accepted;
+ *   zeta_cache_attend_tree  every node over the cache and its own line (each layer's
+ *                           cache; several nodes may be tried in one call);
+ *   (the program decides which node's line is right)
+ *   zeta_cache_accept       that line becomes the sequence's next tokens (each layer's
+ *                           cache);
+ *   zeta_cache_order        with count = accepted, as after zeta_cache_append.
+ * A line ends with the chunk that start lies in (C): attend_tree gives nodes behind that
+ * end no result and accept cuts the line there, so that a step's nodes share one sorted
+ * prefix.  A step can always accept a token: a chunk that is full begins the next.
+ *   parent   int32 [B, n] (device): entries count[b] .. n-1 are not looked at; an entry
+ *            outside [-1, t) costs the lines through it (ZETA_ERR_BOUNDS).
+ *   start, count  as for the cache calls, but 0 <= start <= N and, where count > 0,
+ *            start < N: only the line's tokens need room.
+ * Limit: n <= 1024.
+ */
+
+/*
+ * zeta_cache_attend_tree -- attention of the nodes over the cache.
+ * Passage: as for zeta_select_topk and zeta_attend_fwd.
+ * Node t of sequence b, with position i < (c + 1) C, c = start[b] / C, attends to the k
+ * keys around its code's rank in prefix c (none for c = 0), to the tokens cC .. start[b]-1
+ * and to the nodes of its line, itself included; weights, out and rowsum as in
+ * zeta_attend_fwd.  That is what zeta_cache_attend gives for the same tokens in a line;
+ * weights and rounding as there.
+ *   q, k      in : float [B, H, n, d_K]: the nodes' queries and keys
+ *   v         in : v_dtype [B, H, n, d_V]  (16-B aligned)
+ *   gamma     in : float [H]
+ *   k_pages, v_pages, order_codes, order_idx  in : the cache before this step
+ *   out       out: v_dtype [B, H, n, d_V]  (16-B aligned)
+ *   rowsum    out: float [B, H, n]
+ *   idx       out: int32 [B, H, n, k], the window's tokens (-1 in chunk 0), or null
+ *   dev_status  optional int32 device word; an order entry outside [0, cC) or a page
+ *             out of range drops its key and records ZETA_ERR_BOUNDS.
+ * Rows of nodes behind the chunk's end, of nodes whose line has a bad parent and from
+ * count[b] on are left as they were.
+ * Errors: ZETA_ERR_INVALID_ARG, ZETA_ERR_UNSUPPORTED.
+ */
+zeta_status_t zeta_cache_attend_tree(const zeta_problem_t *p, const zeta_cache_t *cc,
+                                     const float *q, const float *k, const void *v,
+                                     const float *gamma, const int32_t *start,
+                                     const int32_t *count, const int32_t *parent,
+                                     const int32_t *page_table, const float *k_pages,
+                                     const void *v_pages, const int32_t *order_table,
+                                     const void *order_codes, const int32_t *order_idx, void *out,
+                                     float *rowsum, int32_t *idx, int32_t *dev_status,
+                                     cudaStream_t stream);
+
+/*
+ * zeta_cache_accept -- a line of nodes into the pages.
+ * The pages have no counterpart: it is zeta_cache_append along a line.
+ * Keys and values of the line that ends in node leaf[b], as far as it lies before the
+ * chunk's end, become the tokens start[b] .. start[b] + accepted[b] - 1.
+ *   k, v      in : the tensors given to zeta_cache_attend_tree (v 16-B aligned)
+ *   leaf      in : int32 [B], -1: nothing is accepted; not looked at where count is 0
+ *   k_pages, v_pages  in/out (written at the accepted tokens' rows only)
+ *   accepted  out: int32 [B], tokens accepted: the count for zeta_cache_order
+ *   path      out: int32 [B, n], node of the j-th accepted token, -1 from accepted[b] on;
+ *             or null
+ *   dev_status  optional int32 device word (ZETA_ERR_BOUNDS: a leaf outside
+ *             [-1, count), a line with a bad parent or a sequence out of range accepts
+ *             nothing; a page out of range skips its token's row)
+ * Errors: ZETA_ERR_INVALID_ARG, ZETA_ERR_UNSUPPORTED.
+ */
+zeta_status_t zeta_cache_accept(const zeta_problem_t *p, const zeta_cache_t *cc, const float *k,
+                                const void *v, const int32_t *start, const int32_t *count,
+                                const int32_t *parent, const int32_t *leaf,
+                                const int32_t *page_table, float *k_pages, void *v_pages,
+                                int32_t *accepted, int32_t *path, int32_t *dev_status,
+                                cudaStream_t stream);
+
+/*
+ * zeta_cache_reserve -- page tables and row numbers from the requests' lengths.
+ * The pages have no counterpart.
+ * After the call sequence b holds ceil((start[b] + count[b]) / page) pages, entries
+ * [0, held[b]) of its table.  First every sequence that holds more gives its last pages
+ * back to the list (a request that has ended: start = count = 0), their entries become -1;
+ * then the others take theirs in the order of b, from the list's end.  From the first
+ * sequence on that the list is too short for, sequences that need pages get none and stay
+ * as they were: granted[b] = 0.  All others: granted[b] = count[b].  Given granted as
+ * their count, the other calls take what has pages.
+ *   p, cc     B, N, C as everywhere, n, page, pages, table_len of the cache (the heads and
+ *             the order pools play no part); n bounds count
+ *   start, count  int32 [B], 0 <= count <= n, 0 <= start, start + count <= N
+ *   page_table  in/out: int32 [B, table_len]
+ *   held        in/out: int32 [B], pages that sequence b holds
+ *   free_list   in/out: int32 [pages], places [0, *free_count) are the free pages
+ *   free_count  in/out: int32 [1]
+ *   granted     out: int32 [B]
+ *   slots       out: int32 [B, n], row page_table[b][i / page] * page + i % page of the new
+ *               token i = start[b] + t, for data that a program keeps in the same pages; -1
+ *               from granted[b] on; or null
+ *   dev_status  optional int32 device word (ZETA_ERR_BOUNDS: a length or held out of
+ *               range, the sequence is skipped, granted 0; a list longer than the pools
+ *               have pages, nothing changes; a page number out of range, it is passed on)
+ * The result depends on the order of the sequences alone, and a call that takes pages is
+ * undone by one that gives them back.  Pages that sequences share are not the list's: a
+ * table holds them beyond this call's doing.  granted may be the array given as count.
+ * Errors: ZETA_ERR_INVALID_ARG, ZETA_ERR_UNSUPPORTED.
+ */
+zeta_status_t zeta_cache_reserve(const zeta_problem_t *p, const zeta_cache_t *cc,
+                                 const int32_t *start, const int32_t *count, int32_t *page_table,
+                                 int32_t *held, int32_t *free_list, int32_t *free_count,
+                                 int32_t *granted, int32_t *slots, int32_t *dev_status,
+                                 cudaStream_t stream);
+
+/*
  * zeta_check_bounded_wait -- diagnostic of the device-side failure detection.
  * The pages have no counterpart: every wait of the TMA-fed and tensor-core
  * kernels (zeta_project_encode, the own-chunk block of zeta_attend_bwd) on an

@@ -119,6 +119,12 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
     L.zeta_cache_order.restype = S
     L.zeta_cache_attend.argtypes = [PP, PC] + [P] * 15
     L.zeta_cache_attend.restype = S
+    L.zeta_cache_attend_tree.argtypes = [PP, PC] + [P] * 18
+    L.zeta_cache_attend_tree.restype = S
+    L.zeta_cache_accept.argtypes = [PP, PC] + [P] * 13
+    L.zeta_cache_accept.restype = S
+    L.zeta_cache_reserve.argtypes = [PP, PC] + [P] * 10
+    L.zeta_cache_reserve.restype = S
     _lib = L
     return L
 
@@ -449,3 +455,76 @@ def zeta_cache_attend(p, c, q, gamma, start, count, page_table, k_pages, v_pages
                                    _ptr(v_pages), _ptr(order_table), _ptr(order_codes),
                                    _ptr(order_idx), _ptr(out), _ptr(rowsum), _ptr(idx),
                                    _ptr(dev_status), _stream(stream)))
+
+
+# ---------------------------------------------------------------- drafting ---
+
+def zeta_cache_attend_tree(p, c, q, k, v, gamma, start, count, parent, page_table, k_pages,
+                           v_pages, order_table, order_codes, order_idx, out, rowsum, idx=None,
+                           dev_status=None, stream=None):
+    """q, k [B,H,n,d_K], v [B,H,n,d_V] of the drafted nodes, parent int32 [B,n]; out
+    [B,H,n,d_V], rowsum [B,H,n], idx [B,H,n,k] or None."""
+    S, R = p.B * p.H * c.n, c.pages * p.H * c.page
+    O = 2 * c.order_pages * p.H * c.page
+    vt = v_torch_dtype(p)
+    _expect(q, "q", torch.float32, S * p.d_K)
+    _expect(k, "k", torch.float32, S * p.d_K)
+    _expect(v, "v", vt, S * p.d_V)
+    _expect(gamma, "gamma", torch.float32, p.H)
+    _expect(parent, "parent", torch.int32, p.B * c.n)
+    _expect(k_pages, "k_pages", torch.float32, R * p.d_K)
+    _expect(v_pages, "v_pages", vt, R * p.d_V)
+    _expect(order_codes, "order_codes", code_dtype(p), O)
+    _expect(order_idx, "order_idx", torch.int32, O)
+    _expect(out, "out", vt, S * p.d_V)
+    _expect(rowsum, "rowsum", torch.float32, S)
+    _expect(idx, "idx", torch.int32, S * p.k)
+    _expect_cache(p, c, start, count,
+                  [(page_table, "page_table"), (order_table, "order_table")], dev_status)
+    _check("zeta_cache_attend_tree",
+           lib().zeta_cache_attend_tree(ctypes.byref(p), ctypes.byref(c), _ptr(q), _ptr(k),
+                                        _ptr(v), _ptr(gamma), _ptr(start), _ptr(count),
+                                        _ptr(parent), _ptr(page_table), _ptr(k_pages),
+                                        _ptr(v_pages), _ptr(order_table), _ptr(order_codes),
+                                        _ptr(order_idx), _ptr(out), _ptr(rowsum), _ptr(idx),
+                                        _ptr(dev_status), _stream(stream)))
+
+
+def zeta_cache_accept(p, c, k, v, start, count, parent, leaf, page_table, k_pages, v_pages,
+                      accepted, path=None, dev_status=None, stream=None):
+    """The line of nodes that ends in leaf [B] into the pages; accepted int32 [B], path int32
+    [B,n] or None."""
+    S, R = p.B * p.H * c.n, c.pages * p.H * c.page
+    vt = v_torch_dtype(p)
+    _expect(k, "k", torch.float32, S * p.d_K)
+    _expect(v, "v", vt, S * p.d_V)
+    _expect(k_pages, "k_pages", torch.float32, R * p.d_K)
+    _expect(v_pages, "v_pages", vt, R * p.d_V)
+    _expect(parent, "parent", torch.int32, p.B * c.n)
+    _expect(leaf, "leaf", torch.int32, p.B)
+    _expect(accepted, "accepted", torch.int32, p.B)
+    _expect(path, "path", torch.int32, p.B * c.n)
+    _expect_cache(p, c, start, count, [(page_table, "page_table")], dev_status)
+    _check("zeta_cache_accept",
+           lib().zeta_cache_accept(ctypes.byref(p), ctypes.byref(c), _ptr(k), _ptr(v),
+                                   _ptr(start), _ptr(count), _ptr(parent), _ptr(leaf),
+                                   _ptr(page_table), _ptr(k_pages), _ptr(v_pages),
+                                   _ptr(accepted), _ptr(path), _ptr(dev_status),
+                                   _stream(stream)))
+
+
+def zeta_cache_reserve(p, c, start, count, page_table, held, free_list, free_count, granted,
+                       slots=None, dev_status=None, stream=None):
+    """held, granted int32 [B], free_list int32 [pages], free_count int32 [1], slots int32
+    [B,n] or None."""
+    _expect(held, "held", torch.int32, p.B)
+    _expect(free_list, "free_list", torch.int32, c.pages)
+    _expect(free_count, "free_count", torch.int32, 1)
+    _expect(granted, "granted", torch.int32, p.B)
+    _expect(slots, "slots", torch.int32, p.B * c.n)
+    _expect_cache(p, c, start, count, [(page_table, "page_table")], dev_status)
+    _check("zeta_cache_reserve",
+           lib().zeta_cache_reserve(ctypes.byref(p), ctypes.byref(c), _ptr(start), _ptr(count),
+                                    _ptr(page_table), _ptr(held), _ptr(free_list),
+                                    _ptr(free_count), _ptr(granted), _ptr(slots),
+                                    _ptr(dev_status), _stream(stream)))

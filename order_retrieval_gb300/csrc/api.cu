@@ -6,7 +6,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
-#include "cache.cuh"
+#include "cache_tree.cuh"
 
 zeta::CallRange::CallRange(const char *name) { nvtxRangePushA(name); }
 zeta::CallRange::~CallRange() { nvtxRangePop(); }
@@ -341,6 +341,80 @@ ZETA_API zeta_status_t zeta_cache_attend(const zeta_problem_t *p, const zeta_cac
     c.otab = order_table;
     return from_cuda(zeta::launch_cache_attend(pr, c, q, gamma, k_pages, v_pages, order_codes,
                                                order_idx, out, rowsum, idx, dev_status, stream));
+}
+
+ZETA_API zeta_status_t zeta_cache_reserve(const zeta_problem_t *p, const zeta_cache_t *cc,
+                                          const int32_t *start, const int32_t *count,
+                                          int32_t *page_table, int32_t *held, int32_t *free_list,
+                                          int32_t *free_count, int32_t *granted, int32_t *slots,
+                                          int32_t *dev_status, cudaStream_t stream) {
+    zeta::CallRange range_("zeta_cache_reserve");
+    Prob pr;
+    zeta::Cache c;
+    zeta_status_t s = check_cache(p, cc, &pr, &c);
+    if (s != ZETA_OK) return s;
+    if (empty(pr) || c.n == 0) return ZETA_OK;
+    if (c.pages < 1) return ZETA_ERR_INVALID_ARG;
+    if (!start || !count || !page_table || !held || !free_list || !free_count || !granted)
+        return ZETA_ERR_INVALID_ARG;
+    c.start = start;
+    c.count = count;
+    return from_cuda(zeta::launch_cache_reserve(pr, c, page_table, held, free_list, free_count,
+                                                granted, slots, dev_status, stream));
+}
+
+ZETA_API zeta_status_t zeta_cache_attend_tree(
+    const zeta_problem_t *p, const zeta_cache_t *cc, const float *q, const float *k, const void *v,
+    const float *gamma, const int32_t *start, const int32_t *count, const int32_t *parent,
+    const int32_t *page_table, const float *k_pages, const void *v_pages,
+    const int32_t *order_table, const void *order_codes, const int32_t *order_idx, void *out,
+    float *rowsum, int32_t *idx, int32_t *dev_status, cudaStream_t stream) {
+    zeta::CallRange range_("zeta_cache_attend_tree");
+    Prob pr;
+    zeta::Cache c;
+    zeta_status_t s = check_cache(p, cc, &pr, &c);
+    if (s != ZETA_OK) return s;
+    if (c.n > zeta::kMaxDraft) return ZETA_ERR_UNSUPPORTED;
+    if (empty(pr) || c.n == 0) return ZETA_OK;
+    if (c.pages < 1 || c.opages < 1) return ZETA_ERR_INVALID_ARG;
+    if (!q || !k || !v || !gamma || !start || !count || !parent || !page_table || !k_pages ||
+        !v_pages || !order_table || !order_codes || !order_idx || !out || !rowsum)
+        return ZETA_ERR_INVALID_ARG;
+    if (!aligned16(v) || !aligned16(v_pages) || !aligned16(out)) return ZETA_ERR_INVALID_ARG;
+    c.start = start;
+    c.count = count;
+    c.ptab = page_table;
+    c.otab = order_table;
+    const zeta::TreeArgs g{c,   parent, q,         k,      gamma, k_pages,    v,     v_pages,
+                           order_codes, order_idx, out,    rowsum, idx,   dev_status, pr.N, pr.H,
+                           pr.dK, pr.dV, pr.k,      pr.C,   pr.bits, pr.wk, pr.code64};
+    return from_cuda(zeta::launch_tree_rows(pr, g, stream));
+}
+
+ZETA_API zeta_status_t zeta_cache_accept(const zeta_problem_t *p, const zeta_cache_t *cc,
+                                         const float *k, const void *v, const int32_t *start,
+                                         const int32_t *count, const int32_t *parent,
+                                         const int32_t *leaf, const int32_t *page_table,
+                                         float *k_pages, void *v_pages, int32_t *accepted,
+                                         int32_t *path, int32_t *dev_status,
+                                         cudaStream_t stream) {
+    zeta::CallRange range_("zeta_cache_accept");
+    Prob pr;
+    zeta::Cache c;
+    zeta_status_t s = check_cache(p, cc, &pr, &c);
+    if (s != ZETA_OK) return s;
+    if (c.n > zeta::kMaxDraft) return ZETA_ERR_UNSUPPORTED;
+    if (empty(pr) || c.n == 0) return ZETA_OK;
+    if (c.pages < 1) return ZETA_ERR_INVALID_ARG;
+    if (!k || !v || !start || !count || !parent || !leaf || !page_table || !k_pages || !v_pages ||
+        !accepted)
+        return ZETA_ERR_INVALID_ARG;
+    if (!aligned16(v) || !aligned16(v_pages)) return ZETA_ERR_INVALID_ARG;
+    c.start = start;
+    c.count = count;
+    c.ptab = page_table;
+    return from_cuda(zeta::launch_cache_accept(pr, c, parent, leaf, k, v, k_pages, v_pages,
+                                               accepted, path, dev_status, stream));
 }
 
 ZETA_API zeta_status_t zeta_check_bounded_wait(uint32_t iterations, int32_t arrive,

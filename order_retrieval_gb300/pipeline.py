@@ -153,6 +153,14 @@ class ZetaCache:
         cache.order(start, count, table, n=n)     # when a sequence completes a chunk
         cache.attend(q, gamma, start, count, table, out, rowsum)
 
+    Drafted tokens, a tree of up to n nodes per sequence (parent int32 [B, n], -1 at the
+    top), whose keys and values stay in k and v until a line of them is accepted::
+
+        cache.reserve(start, longest, table, held, free, free_count, granted)
+        cache.attend_tree(q, k, v, gamma, start, count, parent, table, out, rowsum)
+        cache.accept(k, v, start, count, parent, leaf, table, accepted)
+        cache.order(start, accepted, table, n=n)
+
     The prefixes of completed chunks are kept in the order pools through
     order_table (default: table; pass another one when sequences share K/V pages).
     Everything is enqueued on the given or current stream and allocates nothing,
@@ -344,4 +352,66 @@ class ZetaCache:
                     tp, kp, vp, op, ocp, oip, take(out, "out", self._vt, v_shape),
                     take(rowsum, "rowsum", _F32, rows),
                     None if idx is None else take(idx, "idx", _I32, i_shape)),
+                   st, dev_status, stream)
+
+    def attend_tree(self, q, k, v, gamma, start, count, parent, page_table, out, rowsum,
+                    order_table=None, idx=None, dev_status=None, stream=None):
+        """Drafted nodes over the cache and their lines: q, k f32 [B,H,n,d_K], v [B,H,n,d_V],
+        parent int32 [B,n] (parent[b,t] < t, -1: below the sequence's last token) -> out
+        [B,H,n,d_V], rowsum f32 [B,H,n] and, where given, idx int32 [B,H,n,k].  Rows from
+        count[b] on and of nodes behind the end of the chunk that start[b] lies in stay as they
+        were.  n <= 1024."""
+        tp, B, width = self._table(page_table)
+        n = self._rows(q, "q")
+        p, c, per_seq, rows, q_shape, v_shape, i_shape = self._sizes(B, n, width)
+        take = self._take
+        op = tp if order_table is None else take(order_table, "order_table", _I32, (B, width))
+        kp, vp, ocp, oip, st = self._memory()
+        self._call(self._lib.zeta_cache_attend_tree,
+                   (p, c, take(q, "q", _F32, q_shape), take(k, "k", _F32, q_shape),
+                    take(v, "v", self._vt, v_shape), take(gamma, "gamma", _F32, self._heads),
+                    take(start, "start", _I32, per_seq), take(count, "count", _I32, per_seq),
+                    take(parent, "parent", _I32, (B, n)), tp, kp, vp, op, ocp, oip,
+                    take(out, "out", self._vt, v_shape), take(rowsum, "rowsum", _F32, rows),
+                    None if idx is None else take(idx, "idx", _I32, i_shape)),
+                   st, dev_status, stream)
+
+    def accept(self, k, v, start, count, parent, leaf, page_table, accepted, path=None,
+               dev_status=None, stream=None):
+        """The line of nodes that ends in leaf int32 [B] (-1: none) becomes the sequence's next
+        tokens, up to the end of the chunk that start[b] lies in; accepted int32 [B] gets how many,
+        path int32 [B,n], where given, their nodes (-1 behind them)."""
+        tp, B, width = self._table(page_table)
+        n = self._rows(k, "k")
+        p, c, per_seq, _, k_shape, v_shape, _ = self._sizes(B, n, width)
+        take = self._take
+        kp, vp, _, _, st = self._memory()
+        self._call(self._lib.zeta_cache_accept,
+                   (p, c, take(k, "k", _F32, k_shape), take(v, "v", self._vt, v_shape),
+                    take(start, "start", _I32, per_seq), take(count, "count", _I32, per_seq),
+                    take(parent, "parent", _I32, (B, n)), take(leaf, "leaf", _I32, per_seq), tp,
+                    kp, vp, take(accepted, "accepted", _I32, per_seq),
+                    None if path is None else take(path, "path", _I32, (B, n))),
+                   st, dev_status, stream)
+
+    def reserve(self, start, count, page_table, held, free, free_count, granted, slots=None,
+                dev_status=None, stream=None, n=None):
+        """Sequence b is given or gives back pages until it holds those of its start[b] + count[b]
+        tokens: page_table, held int32 [B] (pages it holds), free int32 [pages] (places
+        [0, free_count) are the free pages) and free_count int32 [1] change in place.  granted
+        int32 [B] gets count[b], or 0 where the list was too short; slots int32 [B,n], where
+        given, the row number of every new token.  n: the step's rows (default: those of slots,
+        or C)."""
+        tp, B, width = self._table(page_table)
+        if n is None:
+            n = self.C if slots is None else slots.shape[-1]
+        p, c, per_seq, *_ = self._sizes(B, n, width)
+        take = self._take
+        st = self._memory()[4]
+        self._call(self._lib.zeta_cache_reserve,
+                   (p, c, take(start, "start", _I32, per_seq), take(count, "count", _I32, per_seq),
+                    tp, take(held, "held", _I32, per_seq), take(free, "free", _I32, (self.pages,)),
+                    take(free_count, "free_count", _I32, (1,)),
+                    take(granted, "granted", _I32, per_seq),
+                    None if slots is None else take(slots, "slots", _I32, (B, n))),
                    st, dev_status, stream)
