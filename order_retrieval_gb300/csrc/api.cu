@@ -388,7 +388,7 @@ ZETA_API zeta_status_t zeta_cache_attend_tree(
     const zeta::TreeArgs g{c,   parent, q,         k,      gamma, k_pages,    v,     v_pages,
                            order_codes, order_idx, out,    rowsum, idx,   dev_status, pr.N, pr.H,
                            pr.dK, pr.dV, pr.k,      pr.C,   pr.bits, pr.wk, pr.code64};
-    return from_cuda(zeta::launch_tree_rows(pr, g, stream));
+    return from_cuda(zeta::launch_cache_attend_tree(pr, g, stream));
 }
 
 ZETA_API zeta_status_t zeta_cache_accept(const zeta_problem_t *p, const zeta_cache_t *cc,

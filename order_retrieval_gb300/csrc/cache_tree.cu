@@ -11,7 +11,7 @@
 // node's line is found by one thread in the parents in shared memory, its rank by 128
 // probes a step.  The keys (window, chunk, line) are one list, weighed a thread each
 // 1024 at a time; then a thread per value column (and share of the keys) sums.
-#include "cache_tree.cuh"
+#include "cache_tree_tile.cuh"
 
 namespace zeta {
 namespace {
@@ -179,7 +179,14 @@ tree_rows_kernel(const __grid_constant__ TreeArgs g) {
 
 }  // namespace
 
-cudaError_t launch_tree_rows(const Prob &p, const TreeArgs &g, cudaStream_t st) {
+cudaError_t launch_cache_attend_tree(const Prob &p, const TreeArgs &g, cudaStream_t st) {
+    const int piece = p.vdt == ZETA_BF16 ? 8 : 4;    // values of 16 bytes
+    if (p.dK <= 4 && p.dV <= 128 && p.dV % piece == 0) {
+        const int64_t groups = p.S * ((g.c.n + kTreeRows - 1) / kTreeRows);
+        int cs = 1;
+        while (cs < 4 && groups * cs * 2 <= 152 * 4) cs *= 2;
+        return p.vdt == ZETA_BF16 ? launch_tree_tile_bf16(p, g, cs, st) : launch_tree_tile_f32(p, g, cs, st);
+    }
     const dim3 grid((unsigned)g.c.n, (unsigned)p.H, (unsigned)p.B);
     if (p.vdt == ZETA_BF16) {
         if (p.code64) tree_rows_kernel<uint64_t, __nv_bfloat16><<<grid, kNT, 0, st>>>(g);

@@ -49,7 +49,7 @@ __device__ __forceinline__ int climb(const int *parent, int t, Visit visit) {
     return depth;
 }
 
-cudaError_t launch_tree_rows(const Prob &p, const TreeArgs &g, cudaStream_t st);
+cudaError_t launch_cache_attend_tree(const Prob &p, const TreeArgs &g, cudaStream_t st);
 cudaError_t launch_cache_accept(const Prob &p, const Cache &c, const int32_t *parent,
                                 const int32_t *leaf, const float *k, const void *v, float *k_pages,
                                 void *v_pages, int32_t *accepted, int32_t *path, int32_t *status,

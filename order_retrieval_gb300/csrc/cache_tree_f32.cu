@@ -1,0 +1,11 @@
+// cache_tree_f32.cu -- the tile kernel for drafted trees (cache_tree_tile.cuh), float32 values.
+#include "cache_tree_tile.cuh"
+
+namespace zeta {
+
+cudaError_t launch_tree_tile_f32(const Prob &p, const TreeArgs &g, int cs, cudaStream_t st) {
+    return p.dV <= 64 ? dispatch_tree_tile<float, 64>(p, g, cs, st)
+                      : dispatch_tree_tile<float, 128>(p, g, cs, st);
+}
+
+}  // namespace zeta
