@@ -184,7 +184,7 @@ cudaError_t launch_cache_attend_tree(const Prob &p, const TreeArgs &g, cudaStrea
     if (p.dK <= 4 && p.dV <= 128 && p.dV % piece == 0) {
         const int64_t groups = p.S * ((g.c.n + kTreeRows - 1) / kTreeRows);
         int cs = 1;
-        while (cs < 4 && groups * cs * 2 <= 152 * 4) cs *= 2;
+        while (cs < 8 && groups * cs * 2 <= 152 * 3) cs *= 2;
         return p.vdt == ZETA_BF16 ? launch_tree_tile_bf16(p, g, cs, st) : launch_tree_tile_f32(p, g, cs, st);
     }
     const dim3 grid((unsigned)g.c.n, (unsigned)p.H, (unsigned)p.B);

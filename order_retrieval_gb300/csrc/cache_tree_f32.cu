@@ -4,8 +4,8 @@
 namespace zeta {
 
 cudaError_t launch_tree_tile_f32(const Prob &p, const TreeArgs &g, int cs, cudaStream_t st) {
-    return p.dV <= 64 ? dispatch_tree_tile<float, 64>(p, g, cs, st)
-                      : dispatch_tree_tile<float, 128>(p, g, cs, st);
+    return p.dV <= 64 ? dispatch_tree_tile<float, 64, false>(p, g, cs, st)
+                      : dispatch_tree_tile<float, 128, false>(p, g, cs, st);
 }
 
 }  // namespace zeta

@@ -1,21 +1,26 @@
 // cache_tree_tile.cuh -- attention of trees of drafted tokens: bf16 values with d_V a
 // multiple of 8, float32 with a multiple of 4, up to 128 wide, d_K <= 4.
 //
-// Same definition as the row kernel (cache_tree.cu).  A block of four warps takes 16
-// nodes of one sequence and head, or a cluster of 2 or 4 blocks does where there are few:
-// every block of it has some of the nodes' windows and some of the keys that all 16 share,
-// and the sums are joined through distributed shared memory.
+// Same definition as the row kernel (cache_tree.cu).  A block of eight warps takes 16 nodes of
+// one sequence and head, or a cluster of up to 8 blocks does where there are few: every block
+// of it has some of the nodes' windows and some of the keys that all 16 share, and the sums
+// are joined through distributed shared memory.  A warp takes its windows one by one, then
+// its part of the shared keys; none waits for another between set-up and join.
 //  * Lines: a bit per node above, found by climbing in shared memory.  A run of nodes
 //    that hang below one another by number (a chain) is one step of the climb.
-//  * Window: a warp takes two nodes at a time.  The first code of every block of 2^fsh
-//    prefix entries lies in shared memory; a warp counts there and among the block's
-//    entries, looks up and weighs the entries a lane each and streams their value rows.
-//  * The sequence's tokens of the chunk and the nodes are one list of keys, staged by
-//    cp.async in tiles; a warp takes a quarter of each.  bf16: weights are built in mma A
-//    fragments, as a bf16 half and the bf16 of what that leaves (within 2^-16 together).
-//    float32: weights through shared memory, then a thread sums 4 nodes x 8 (16) columns.
-//  * A masked weight of zero times a value that is not finite is NaN: a node whose result
-//    is not finite is taken again, key by key, without the others.
+//  * Window: the first code of every block of 2^fsh prefix entries lies in shared memory; a
+//    warp counts there and among the block's entries, and asks with those for the entries
+//    that the window may hold.  It looks up and weighs the entries a lane each, then their
+//    value rows stream through registers.
+//  * Shared keys: the sequence's tokens of the chunk, then the nodes, 16 (float32: 8) a step
+//    and warp, straight from global memory, the next step's coordinates ahead.
+//  * bf16 products run on mma.sync without shared memory: of 16 keys lane (g, t) loads 32
+//    bytes (values 16t ..) of the rows of keys g and g + 8, a whole row to four lanes, so that
+//    a load touches 8 lines of L1; movmatrix turns the 8 x 8 blocks into A operands (values
+//    times keys).  B (keys times columns) has 8 nodes' weights, a window's in column 0 and 1.
+//    A weight enters as a bf16 half and the bf16 of what that leaves, within 2^-16 together.
+//  * A weight of zero times a value that is not finite is NaN: a node whose result is not
+//    finite is taken again, key by key, without the others.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -25,47 +30,81 @@
 
 namespace zeta {
 
-// cs: blocks a group of 16 nodes (1, 2 or 4).
+// cs: blocks to 16 nodes (1, 2, 4 or 8).
 cudaError_t launch_tree_tile_bf16(const Prob &p, const TreeArgs &g, int cs, cudaStream_t st);
 cudaError_t launch_tree_tile_f32(const Prob &p, const TreeArgs &g, int cs, cudaStream_t st);
 
 namespace {
 
+#ifndef ZETA_TREE_DEPTH
+#define ZETA_TREE_DEPTH 1
+#endif
+#ifndef ZETA_TREE_NB
+#define ZETA_TREE_NB 3
+#endif
+#ifndef ZETA_TREE_BLOCKS
+#define ZETA_TREE_BLOCKS 2
+#endif
 namespace cg = cooperative_groups;
 
-constexpr int kTreeWarps = 4, kTreeThreads = 32 * kTreeWarps, kTreeRows = 16;
+constexpr int kTreeWarps = 8, kTreeThreads = 32 * kTreeWarps;
+constexpr int kTreeRows = 16, kTreeGroups = kTreeRows / 8;   // nodes of a block; in groups of 8
 constexpr int kTreeFences = 256;
-constexpr int kNoRow = INT32_MIN;
+constexpr int kTreeTable = 1024;                     // pages whose numbers lie in shared memory
 
 template <typename V, int DVP>
 struct TreeSmem {
     static constexpr bool MMA = sizeof(V) == 2;
-    static constexpr int TK = MMA ? 64 : 32;         // keys a tile
-    union {
-        struct {
-            V v[3][TK * DVP];                        // bf16: 16-byte piece c of row r at c ^ (r & 7)
-            float k[3][4][TK];                       // coordinates apart
-        } own;
-        float part[kTreeWarps][kTreeRows][DVP + 4];  // the warps' sums
-    };
+    static constexpr int KS = MMA ? 16 : 8, KL = KS / 4, KP = KL / 2;    // shared keys a step, a lane; pairs
+    static constexpr int NV = DVP / 16;              // 16-byte pieces of them a lane holds (float32: of four keys)
+    float part[kTreeWarps][kTreeRows][DVP + 4];      // sums over shared keys, warp by warp
+    struct {                                         // of a warp's window
+        int row[64];
+        union {
+            int cand[128];                           // entries that it may hold
+            float w[64];                             // float32: weights
+            uint16_t half[2][64];                    // bf16: weights' halves and rests
+        };
+        float x[64 * 4];                             // coordinates
+    } gather[kTreeWarps];
     uint64_t fence[kTreeFences];
-    struct {                                         // a warp's two nodes
-        float w[kTreeWarps][2][64];
-        int row[kTreeWarps][2][64];
-    } gather;
-    float w[MMA ? 1 : kTreeWarps][8][20];            // float32: weights [key][node]
+    int ptab[kTreeTable];
+    float w[MMA ? 1 : kTreeWarps][8][20];            // float32, shared keys: weights [key][node]
     union {
         int parent[kMaxDraft];
         float win[kTreeRows][DVP + 4];               // window sums
     };
     uint32_t run[kMaxDraft / 32];                    // bit u: parent[u] == u - 1
     uint32_t above[kTreeRows][kMaxDraft / 32];       // nodes of a line
-    int rows[4][TK];                                 // pool rows of the tile's keys, ~node, kNoRow
     float q[kTreeRows][4];
     int depth[kTreeRows], wst[kTreeRows];
     float swin[kTreeRows], mwin[kTreeRows];
     float psum[kTreeWarps][kTreeRows], pmin[kTreeWarps][kTreeRows];
+    float factor[kTreeWarps + 1][kTreeRows], least[kTreeRows];   // softmax: of the parts and the window; the shift
+    float total[kTreeRows];
+    bool again[kTreeRows];                           // not finite
 };
+
+__device__ __forceinline__ uint4 ld16(const void *p) {
+    uint4 a;
+    asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w)
+                 : "l"(p));
+    return a;
+}
+// 32 bytes: one load where P is 32-byte aligned (WIDE), else two of 16 at p and q.
+template <bool WIDE>
+__device__ __forceinline__ void ld32(uint32_t (&x)[8], const char *p, const char *q) {
+    if constexpr (WIDE) {
+        asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
+                     : "l"(p));
+    } else {
+        const uint4 a = ld16(p), b = ld16(q);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+}
 
 // The line of node t as bits of `above` (words of `run` read from the top one down);
 // its depth, -1 where a parent is no earlier node.
@@ -85,22 +124,6 @@ __device__ __forceinline__ int climb_bits(const int *parent, const uint32_t *run
         t = p;
     }
     return depth;
-}
-
-// Values of a 16-byte piece as pairs, times f, onto acc.
-template <typename V>
-__device__ __forceinline__ void add_piece(float2 (&acc)[8 / sizeof(V)], const uint4 &x, float f) {
-    const float2 ff = dup2(f);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    if constexpr (sizeof(V) == 2) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            acc[c] = fma2(ff, make_float2(__uint_as_float(w[c] << 16), __uint_as_float(w[c] & 0xffff0000u)), acc[c]);
-    } else {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-            acc[c] = fma2(ff, make_float2(__uint_as_float(w[2 * c]), __uint_as_float(w[2 * c + 1])), acc[c]);
-    }
 }
 
 // One node key by key (a warp, lanes over the value columns).
@@ -164,627 +187,760 @@ __device__ __noinline__ void slow_node(const TreeArgs &g, int64_t rid, int b, in
         if (lane + 32 * e < g.dV) VT<V>::st(o + lane + 32 * e, __fdiv_rn(acc[e], s));
 }
 
-template <typename V, int DVP, int DK, int WK>
-__global__ void __launch_bounds__(kTreeThreads, 4)
+// A code of the order, 32 or 64 bits wide.
+__device__ __forceinline__ uint64_t ld_code(const char *codes, uint32_t row, int code64) {
+    const char *p = codes + ((uint64_t)row << (2 + code64));
+    return (uint64_t)ld4_if(p + 4, code64) << 32 | __ldg(reinterpret_cast<const uint32_t *>(p));
+}
+
+template <typename V, int DVP, int DK, int WK, bool WIDE>
+__global__ void __launch_bounds__(kTreeThreads, ZETA_TREE_BLOCKS)
 tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     using Sm = TreeSmem<V, DVP>;
-    constexpr int TK = Sm::TK, NT = kTreeThreads, NW = kTreeWarps;
+    constexpr int NT = kTreeThreads, NW = kTreeWarps;
     constexpr int PPR = DVP * (int)sizeof(V) / 16;           // 16-byte pieces of a padded row
-    constexpr int NP = 8 / (int)sizeof(V);                   // pairs of a piece
     extern __shared__ __align__(16) unsigned char raw[];
     Sm &sm = *reinterpret_cast<Sm *>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cr = cs == 1 ? 0 : (int)(blockIdx.x % (unsigned)cs);   // block in the cluster
     const int f0 = (int)(blockIdx.x / (unsigned)cs) * kTreeRows;     // first node
     const int s = blockIdx.y, b = s / g.H, h = s - b * g.H;
+    const int64_t node0 = (int64_t)s * g.c.n;                // the slice's node 0
+    const int32_t *ptab = g.c.ptab + (int64_t)b * g.c.tlen, *otab = g.c.otab + (int64_t)b * g.c.tlen;
+    // What does not depend on the lengths is asked for with them.
+    const int ahead = min(f0 + kTreeRows, g.c.n), pages_near = min(g.c.tlen, kTreeTable);
+    const int parent = tid < ahead ? __ldg(g.parent + (int64_t)b * g.c.n + tid) : 0;
+    const float q_in = tid < kTreeRows * 4 && f0 + (tid >> 2) < ahead && (tid & 3) < g.dK
+                           ? __ldg(g.q + (node0 + f0 + (tid >> 2)) * g.dK + (tid & 3)) : 0.f;
+    for (int e = tid; e < pages_near; e += NT) sm.ptab[e] = __ldg(ptab + e);
     const Seq seq = drafts_of(g.c, b, g.N, g.status);
     if (f0 >= seq.count) return;                             // the whole cluster returns
     const int nn = min(f0 + kTreeRows, seq.count), nq = nn - f0;
     const int chunk = seq.start / g.C, cC = chunk * g.C, L = seq.start - cC;
-    const int32_t *ptab = g.c.ptab + (int64_t)b * g.c.tlen, *otab = g.c.otab + (int64_t)b * g.c.tlen;
-    const int64_t node0 = (int64_t)s * g.c.n;                // the slice's node 0
-    const V *pool = static_cast<const V *>(g.v_pages);
-    const V *fresh = static_cast<const V *>(g.v) + node0 * g.dV;
     const float gm = __ldg(g.gamma + h);
     const float inv_g2 = __frcp_rn(gm * gm);
-    const int64_t plane = ((int64_t)g.c.opages * g.H << g.c.psh) * (chunk & 1);
-    const int ppr = g.dV * (int)sizeof(V) / 16;
-    auto order_row = [&](int id, int e) { return row_in(id, e, h, g.H, g.c.psh, g.c.pmask, g.c.opages); };
-    auto pool_row = [&](int id, int t) { return row_in(id, t, h, g.H, g.c.psh, g.c.pmask, g.c.pages); };
-    auto order_code = [&](int64_t at) -> uint64_t {
-        return g.code64 ? __ldg(static_cast<const unsigned long long *>(g.order_codes) + at)
-                        : (uint64_t)__ldg(static_cast<const uint32_t *>(g.order_codes) + at);
-    };
+    const int psh = g.c.psh, pmask = g.c.pmask;
+    const int ppr = g.dV * (int)sizeof(V) / 16, vrow = g.dV * (int)sizeof(V);
+    const int krow = (DK == 3 ? 3 : g.dK) * 4;               // bytes of a row
+    const int64_t plane = ((int64_t)g.c.opages * g.H << psh) * (chunk & 1);
+    const char *codes = static_cast<const char *>(g.order_codes) + (plane << (2 + g.code64));
+    const int32_t *entries = g.order_idx + plane;
+    // Row of position t in the pools where its page's number is id, which must be in range.
+    const int hp = g.H << psh, hb = h << psh;
+    auto row_at = [&](int id, int t) { return id * hp + hb + (t & pmask); };
+    // Page numbers: of the sequence's tokens from shared memory where they fit, of the
+    // order's entries from there too where both go by one table.
+    const bool near = ((seq.start + pmask) >> psh) <= pages_near;
+    const int32_t *pt = near ? sm.ptab : ptab, *ot = near && otab == ptab ? sm.ptab : otab;
 
     // ------------------------------------------------------------ set-up ---
-    // Shared keys x: the chunk's L tokens, then the nodes up to the block's last one; the
-    // block takes tiles cr, cr + cs, ...
-    const int keys = L + nn, tiles = (keys + TK - 1) / TK;
-    const int mine = cr < tiles ? (tiles - cr + cs - 1) / cs : 0;
-    auto ask_row = [&](int i) {                              // page of the thread's key of its tile i
-        const int x = (cr + i * cs) * TK + tid;
-        return tid < TK && x < L ? page_id(ptab, cC + x, g.c.psh) : -1;
-    };
-    bool lost_key = false;                                   // this thread met a key without a page
-    auto put_row = [&](int i, int id) {
-        const int x = (cr + i * cs) * TK + tid;
-        if (tid < TK && i < mine) {
-            int row = kNoRow;
-            if (x < L) {
-                row = pool_row(id, cC + x);
-                if (row < 0) {
-                    set_status(g.status, ZETA_ERR_BOUNDS);
-                    lost_key = true;
-                    row = kNoRow;
-                }
-            } else if (x < keys) {
-                row = ~(x - L);
-            }
-            sm.rows[i & 3][tid] = row;
-        }
-        __syncwarp();                                        // one branch again before the products
-    };
-    auto load_tile = [&](int i) {                            // into stage i % 3, asynchronously
-        if (i < mine) {
-            const int bf = i % 3;
-            const int *rows = sm.rows[i & 3];
-#pragma unroll
-            for (int u = 0; u < TK * PPR / NT; ++u) {
-                const int id = u * NT + tid;
-                const int row = id / PPR, ch = id % PPR;
-                if (ch < ppr) {
-                    const int pr = rows[row];
-                    const V *src = pr >= 0 ? pool + (int64_t)pr * g.dV : fresh + (int64_t)(pr == kNoRow ? 0 : ~pr) * g.dV;
-                    const int at = Sm::MMA ? ch ^ (row & 7) : ch;
-                    cp_async16(smem_u32(&sm.own.v[bf][row * DVP + at * (16 / (int)sizeof(V))]),
-                               src + ch * (16 / (int)sizeof(V)), pr == kNoRow ? 0 : 16);
-                }
-            }
-            for (int id = tid; id < TK * DK; id += NT) {
-                const int d = id / TK, row = id % TK;
-                const int pr = rows[row];
-                const bool ok = pr != kNoRow && d < g.dK;
-                const float *src = pr >= 0 ? g.k_pages + (int64_t)pr * g.dK : g.k + (node0 + ~pr) * g.dK;
-                cp_async4(smem_u32(&sm.own.k[bf][d][row]), ok ? src + d : g.k_pages, ok ? 4 : 0);
-            }
-        }
-        cp_async_commit();
-    };
-    {
-        const int i0 = ask_row(0), i1 = ask_row(1), i2 = ask_row(2);
-        for (int u = tid; u < nn; u += NT) sm.parent[u] = __ldg(g.parent + (int64_t)b * g.c.n + u);
-        if (tid < kTreeRows * 4) {
-            const int r = tid >> 2, d = tid & 3;
-            sm.q[r][d] = r < nq && d < g.dK ? __ldg(g.q + (node0 + f0 + r) * g.dK + d) : 0.f;
-        }
-        for (int e = tid; e < kTreeRows * (kMaxDraft / 32); e += NT) (&sm.above[0][0])[e] = 0u;
-        put_row(0, i0);
-        put_row(1, i1);
-        put_row(2, i2);
-    }
-    int kid = ask_row(3);
+    if (tid < nn) sm.parent[tid] = parent;
+    for (int u = NT + tid; u < nn; u += NT) sm.parent[u] = __ldg(g.parent + (int64_t)b * g.c.n + u);
+    if (tid < kTreeRows * 4) sm.q[tid >> 2][tid & 3] = q_in;
+    if (tid < kTreeRows) sm.again[tid] = false;
+    for (int e = tid; e < kTreeRows * (kMaxDraft / 32); e += NT) (&sm.above[0][0])[e] = 0u;
     __syncthreads();
-    load_tile(0);
-    load_tile(1);
-    int fsh = 5;
-    while ((cC >> fsh) >= kTreeFences) ++fsh;
-    const int nf = (cC + (1 << fsh) - 1) >> fsh;
-    if (chunk > 0) {
-        constexpr int NF = kTreeFences / NT;
-        int fr[NF];
-        uint64_t fz[NF];
-#pragma unroll
-        for (int u = 0; u < NF; ++u) fr[u] = page_id(otab, min(u * NT + tid, nf - 1) << fsh, g.c.psh);
-#pragma unroll
-        for (int u = 0; u < NF; ++u) {
-            fr[u] = order_row(fr[u], min(u * NT + tid, nf - 1) << fsh);
-            fz[u] = order_code(plane + max(fr[u], 0));
-        }
-#pragma unroll
-        for (int u = 0; u < NF; ++u) {
-            if (fr[u] < 0) set_status(g.status, ZETA_ERR_BOUNDS);
-            sm.fence[u * NT + tid] = u * NT + tid < nf && fr[u] >= 0 ? fz[u] : ~0ull;
-        }
+    const int fsh = max(5, 24 - __clz(cC | 1));              // one fence in 2^fsh entries: up to 256
+    const int nf = (cC + (1 << fsh) - 1) >> fsh, fe = tid << fsh;
+    uint64_t fz = ~0ull;
+    if (tid < nf) {
+        const int id = ot[fe >> psh];
+        if ((unsigned)id < (unsigned)g.c.opages) fz = ld_code(codes, row_at(id, fe), g.code64);
+        else set_status(g.status, ZETA_ERR_BOUNDS);
     }
-    for (int w = warp; w * 32 < nn; w += NW) {
-        const int u = w * 32 + lane;
-        const uint32_t bits = __ballot_sync(kFull, u < nn && u > 0 && sm.parent[u] == u - 1);
-        if (lane == 0) sm.run[w] = bits;
-    }
-    __syncthreads();
-    if (tid < kTreeRows) {
-        int depth = -1;
-        if (tid < nq) {
-            depth = climb_bits(sm.parent, sm.run, f0 + tid, sm.above[tid]);
-            if (depth < 0) set_status(g.status, ZETA_ERR_BOUNDS);
-            if (seq.start + depth >= cC + g.C) depth = -1;   // behind the chunk's end
+    if (warp == 0) {                                         // the lines
+        for (int w = 0; w * 32 < nn; ++w) {
+            const int u = w * 32 + lane;
+            const uint32_t bits = __ballot_sync(kFull, u < nn && u > 0 && sm.parent[u] == u - 1);
+            if (lane == 0) sm.run[w] = bits;
         }
-        sm.depth[tid] = depth;                               // -1: no result
+        __syncwarp();
+        if (lane < kTreeRows) {
+            int depth = -1;
+            if (lane < nq) {
+                depth = climb_bits(sm.parent, sm.run, f0 + lane, sm.above[lane]);
+                if (depth < 0) set_status(g.status, ZETA_ERR_BOUNDS);
+                if (seq.start + depth >= cC + g.C) depth = -1;   // behind the chunk's end
+            }
+            sm.depth[lane] = depth;                          // -1: no result
+        }
+        __syncwarp();
     }
-    __syncthreads();
 
-    // ----------------------------------------------------------- windows ---
-    const int CW = NW * cs, cw = cr * NW + warp;             // the cluster's warps, this one
-    for (int r0 = cw; r0 < nq; r0 += 2 * CW) {
-        int rr[2], st[2] = {0, 0};
-        bool live[2];
+    constexpr int H = Sm::MMA ? DVP / 64 : 1;                // 64-column halves (bf16)
+    const int g4 = lane >> 2, s4 = lane & 3;
+    // Of 16 keys' rows (x: g, g + 8), A operands m of the values 16 (g / 2) + g % 2 + 4c, + 2 for
+    // c = 0..3: mul(c, m).
+    auto operands = [](const uint32_t (*x)[8], auto mul) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            rr[u] = min(r0 + u * CW, kTreeRows - 1);
-            live[u] = r0 + u * CW < nq && sm.depth[rr[u]] >= 0;
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t m[4] = {movmatrix_trans(x[0][2 * c]), movmatrix_trans(x[0][2 * c + 1]),
+                                   movmatrix_trans(x[1][2 * c]), movmatrix_trans(x[1][2 * c + 1])};
+            mul(c, m);
         }
-        if (!live[0] && !live[1]) continue;
-        float sw[2] = {0.f, 0.f}, mr[2] = {INFINITY, INFINITY};
-        float2 o[2][NP];
+    };
+    const int column = 16 * (g4 >> 1) + (g4 & 1);            // the first of the lane's values
+    // Where in a row the lane's 32 bytes of 64 columns are (bf16; within the row).
+    auto spot = [&](int hh, int e) { return WIDE ? min(128 * hh + 32 * s4, vrow - 32) : min(8 * hh + 2 * s4 + e, ppr - 1) * 16; };
+
+    // Shared keys: whole steps of the chunk's tokens where they lie within a page, the other
+    // tokens, the nodes up to the block's last one.
+    constexpr int KS = Sm::KS, KL = Sm::KL, KP = Sm::KP, NV = Sm::NV;
+    const int CW = NW * cs, cw = warp * cs + cr;             // the cluster's warps, this one
+    const bool pairs = (reinterpret_cast<uintptr_t>(g.k_pages) & 7) == 0;    // two coordinates a load
+    const int n_main = DK == 3 && pairs && pmask >= KS - 1 && (cC & (KS - 1)) == 0 ? L / KS : 0;
+    const int n_node = (nn + KS - 1) / KS, n_rest = (L + KS - 1) / KS - n_main + n_node;
+    const char *vt = static_cast<const char *>(g.v_pages), *vf = static_cast<const char *>(g.v) + node0 * vrow;
+    const char *kt = reinterpret_cast<const char *>(g.k_pages), *kf = reinterpret_cast<const char *>(g.k) + node0 * krow;
+    const int first_key = Sm::MMA ? 2 * s4 : 2 * (lane >> 3);                // the lane's first key of a step
+    const int piece = min(lane & 15, ppr - 1) * 16;          // float32: its bytes of a value row
+    const int second = NV == 4 ? 0 : min((lane & 15) + 16, ppr - 1) * 16 - piece;
+    // The whole steps' values are asked into L2 ahead.
+    for (int i = cw; i < n_main; i += CW) {
+        const int first = cC + i * KS, id = pt[first >> psh];
+        if ((unsigned)id < (unsigned)g.c.pages && lane * 128 < KS * vrow)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(vt + (uint64_t)(uint32_t)row_at(id, first) * (uint32_t)vrow + lane * 128));
+    }
+
+    // ------------------------------------------------------------ window ---
+    // The cluster's warps take the nodes in turn.  While a window's keys and values are under
+    // way the next one's search begins.
+    const int kh = (g.kw + 1) / 2;
+    const bool few = g.kw <= 64;
+    auto next = [&](int r) {                                 // the warp's next node with a result, from r on
+        while (r < nq && sm.depth[r] < 0) r += CW;
+        return r;
+    };
+    // Rank: among the fences, then among a block's entries, 64 probes a step; the last step's are
+    // asked for here and looked at in found.  Where a window has up to 64 entries, those that
+    // it may hold are asked for with them.
+    uint64_t z = 0, zz[2] = {0, 0};
+    int ra = 0, re = 0, cand[4], lo = 0;                     // entries before ra are <= z, from re on > z
+    bool open[2] = {false, false};
+    auto probe = [&](int step) {
+        bool lost = false;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int v = 0; v < 2; ++v) {
+            const int at = ra + (v * 32 + lane + 1) * step - 1, to = min(at, cC - 1);
+            const int id = ot[to >> psh];
+            const bool in = (unsigned)id < (unsigned)g.c.opages;
+            open[v] = at < re && in;
+            lost |= at < re && !in;
+            zz[v] = ld_code(codes, in ? row_at(id, to) : 0, g.code64);
+        }
+        if (lost) set_status(g.status, ZETA_ERR_BOUNDS);
+    };
+    auto found = [&](int step) {
+        __syncwarp();
+        const int le = __popc(__ballot_sync(kFull, open[0] && zz[0] <= z)) + __popc(__ballot_sync(kFull, open[1] && zz[1] <= z));
+        ra = min(ra + le * step, re);
+        re = min(re, ra + step - 1);
+    };
+    auto search = [&](int r) {
+        if (chunk == 0) return;
+        float p[kMaxDK];
 #pragma unroll
-            for (int c = 0; c < NP; ++c) o[u][c] = make_float2(0.f, 0.f);
-        constexpr int LPR = PPR, RPI = 32 / LPR;             // lanes a value row, rows a load
-        const int grp = lane / LPR, sub = lane % LPR;
-        float q[2][DK];
+        for (int d = 0; d < kMaxDK; ++d) p[d] = d < DK ? sm.q[r][d < DK ? d : 0] : 0.f;
+        z = code_of(p, DK == 3 ? 3 : g.dK, g.bits);
+        const int f8 = 8 * __popc(__ballot_sync(kFull, lane * 8 + 7 < nf && sm.fence[lane * 8 + 7] <= z));
+        const int f = f8 + (lane & 7);
+        const int n = f8 + __popc(__ballot_sync(kFull, lane < 8 && f < nf && sm.fence[min(f, kTreeFences - 1)] <= z));
+        ra = n > 0 ? ((n - 1) << fsh) + 1 : 0;
+        re = n > 0 ? min(cC, n << fsh) : 0;
+        for (int len = 1 << fsh; len > 64;) {                // most entries still open
+            const int step = (len + 63) / 64;
+            probe(step);
+            found(step);
+            len = step - 1;
+        }
+        probe(1);
+        if (few) {
+            lo = min(max(ra - kh, 0), cC - g.kw);
+            const int hi = min(max(re - kh, 0), cC - g.kw) + g.kw;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int d = 0; d < DK; ++d) q[u][d] = sm.q[rr[u]][d];
-        if (chunk > 0) {
-            // Ranks: among the fences, then among a block's entries.
-            uint64_t z[2];
-            int a[2], e[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float p[kMaxDK];
-#pragma unroll
-                for (int d = 0; d < kMaxDK; ++d) p[d] = d < DK ? q[u][d < DK ? d : 0] : 0.f;
-                z[u] = code_of(p, g.dK, g.bits);
-                int le = 0;
-#pragma unroll
-                for (int f = 0; f < kTreeFences / 32; ++f) le += f * 32 + lane < nf && sm.fence[f * 32 + lane] <= z[u];
-                const int fr = (int)__reduce_add_sync(kFull, (unsigned)le);
-                a[u] = fr > 0 ? ((fr - 1) << fsh) + 1 : 0;   // entries before a are <= z
-                e[u] = fr > 0 ? min(cC, fr << fsh) : 0;      // entries from e on are > z
+            for (int v = 0; v < 4; ++v) {
+                const int at = lo + v * 32 + lane, id = ot[min(at, cC - 1) >> psh];
+                cand[v] = ldi_if(entries + row_at(id, at), at < hi && (unsigned)id < (unsigned)g.c.opages);
             }
-            for (int len = 1 << fsh; len > 0;) {             // most entries still open
-                constexpr int PR = 2;                        // probes a lane and node
-                const int step = (len + 32 * PR - 1) / (32 * PR);
-                int row[2][PR];
-                uint64_t zz[2][PR];
-                auto at = [&](int u, int v) { return min(a[u] + (v * 32 + lane + 1) * step - 1, cC - 1); };
+        }
+    };
+    auto take_window = [&](int r) {
+        constexpr int LPR = PPR, RPI = 32 / LPR;             // float32: lanes a value row, rows a load
+        constexpr int WS = Sm::MMA ? 16 : 4 * RPI;           // entries a step
+        auto &ga = sm.gather[warp];
+        float *win = sm.win[r];
+        const int64_t rid = node0 + f0 + r;
+        found(1);
+        const int st = min(max(ra - kh, 0), cC - g.kw), from = st - lo;
+        if (lane == 0) sm.wst[r] = st;
+        if (few) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+            for (int v = 0; v < 4; ++v) ga.cand[v * 32 + lane] = cand[v];
+            __syncwarp();
+        }
+        float q[DK], sw = 0.f, mr = INFINITY;
 #pragma unroll
-                    for (int v = 0; v < PR; ++v) row[u][v] = page_id(otab, at(u, v), g.c.psh);
+        for (int d = 0; d < DK; ++d) q[d] = sm.q[r][d];
+        int following = nq;
+        for (int t0 = 0; t0 < g.kw; t0 += 64) {              // up to 64 entries at a time, two a lane
+            int row[2];
+            bool is[2], lost = false;
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int v = 0; v < PR; ++v) {
-                        row[u][v] = order_row(row[u][v], at(u, v));
-                        zz[u][v] = order_code(plane + max(row[u][v], 0));
-                    }
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    int le = 0;
-#pragma unroll
-                    for (int v = 0; v < PR; ++v) {
-                        const bool open = a[u] + (v * 32 + lane + 1) * step - 1 < e[u];
-                        if (open && row[u][v] < 0) set_status(g.status, ZETA_ERR_BOUNDS);
-                        le += __popc(__ballot_sync(kFull, open && row[u][v] >= 0 && zz[u][v] <= z[u]));
-                    }
-                    a[u] = min(a[u] + le * step, e[u]);
-                    e[u] = min(e[u], a[u] + step - 1);
+            for (int v = 0; v < 2; ++v) {
+                const int slot = t0 + v * 32 + lane;
+                const bool there = slot < g.kw;
+                int j;
+                if (few) {
+                    j = there ? ga.cand[min(from + slot, 127)] : -1;
+                } else {
+                    const int at = st + slot, id = ot[min(at, cC - 1) >> psh];
+                    j = ldi_if(entries + row_at(id, at), there && (unsigned)id < (unsigned)g.c.opages);
                 }
-                len = step - 1;
+                const bool in = (unsigned)j < (unsigned)cC;
+                if (g.idx && there) g.idx[rid * g.kw + slot] = in ? j : -1;
+                const int id = pt[(in ? j : 0) >> psh];
+                is[v] = in && (unsigned)id < (unsigned)g.c.pages;
+                row[v] = row_at(id, j);
+                lost |= there && !is[v];
+            }
+            if (lost) set_status(g.status, ZETA_ERR_BOUNDS);
+            __syncwarp();                                    // the entries have been read
+            // In the place of an entry that is none, another of the window: its values enter the
+            // sum anyway, so that a zero weight adds no NaN of its own.
+            const unsigned h0 = __ballot_sync(kFull, is[0]), h1 = __ballot_sync(kFull, is[1]);
+            if ((h0 & h1) != kFull) {
+                const int some = __shfl_sync(kFull, h0 ? row[0] : row[1], __ffs(h0 ? h0 : h1 | 1u << 31) - 1);
+                if (!is[0]) row[0] = h0 | h1 ? some : 0;
+                if (!is[1]) row[1] = h0 | h1 ? some : 0;
+            }
+            ga.row[lane] = row[0];
+            ga.row[32 + lane] = row[1];
+            __syncwarp();                                    // the rows are there
+            // Coordinates one by one, so that a load touches a row's line once.
+            const int steps = (min(64, g.kw - t0) + WS - 1) / WS;
+            float x[2 * DK];
+#pragma unroll
+            for (int v = 0; v < 2 * DK; ++v) {
+                const int at = v * 32 + lane;
+                if (DK == 3 || at % DK < g.dK)
+                    x[v] = __ldg(reinterpret_cast<const float *>(kt + (uint64_t)(uint32_t)ga.row[at / DK] * (uint32_t)krow) + at % DK);
+                else
+                    x[v] = 0.f;
+            }
+            auto load = [&](uint32_t (&y)[2][8], int i, int hh) {
+                if (i >= steps) return;
+                const int *rows = ga.row + i * WS;
+                if constexpr (Sm::MMA) {
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        const char *p = vt + (uint64_t)(uint32_t)rows[8 * v + g4] * (uint32_t)vrow;
+                        ld32<WIDE>(y[v], p + spot(hh, 0), p + spot(hh, 1));
+                    }
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        *reinterpret_cast<uint4 *>(&y[v / 2][v % 2 * 4]) =
+                            ld16(vt + (uint64_t)(uint32_t)rows[v * RPI + lane / LPR] * (uint32_t)vrow + min(lane % LPR, ppr - 1) * 16);
+                }
+            };
+            constexpr int NB = ZETA_TREE_NB;                 // steps in flight
+            uint32_t buf[NB][2][8];
+#pragma unroll
+            for (int o = 0; o < NB; ++o) load(buf[o], o, 0);
+            if (t0 + 64 >= g.kw) {
+                following = next(r + CW);
+                if (following < nq) search(following);
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                st[u] = min(max(a[u] - (g.kw + 1) / 2, 0), cC - g.kw);
-                if (lane == 0 && live[u]) sm.wst[rr[u]] = st[u];
+            for (int v = 0; v < 2 * DK; ++v) ga.x[v * 32 + lane] = x[v];
+            __syncwarp();
+            float d2[2];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                d2[v] = 0.f;
+#pragma unroll
+                for (int d = 0; d < DK; ++d) {
+                    const float f = q[d] - ga.x[(v * 32 + lane) * DK + d];
+                    d2[v] = __fmaf_rn(f, f, d2[v]);
+                }
+                if (!is[v]) d2[v] = INFINITY;
             }
-            // Up to 64 entries of both nodes at a time.
-            for (int t0 = 0; t0 < g.kw; t0 += 64) {
-                auto slot = [&](int v) { return t0 + (v & 1) * 32 + lane; };
-                auto there = [&](int v) { return live[v >> 1] && slot(v) < g.kw; };
-                int j[4], row[4];
-                float x[4][DK];
+            float scale = 1.f;                               // of the sums so far
+            if constexpr (WK == kWSoftmax) {
+                float least = fminf(d2[0], d2[1]);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) j[v] = page_id(otab, min(st[v >> 1] + slot(v), cC - 1), g.c.psh);
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int orow = order_row(j[v], st[v >> 1] + slot(v));
-                    j[v] = ldi_if(g.order_idx + plane + orow, there(v) && orow >= 0);
+                for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(kFull, least, o));
+                if (least < mr) {
+                    scale = mr == INFINITY ? 0.f : __expf((least - mr) * inv_g2);
+                    sw *= scale;
+                    mr = least;
                 }
+            }
 #pragma unroll
-                for (int v = 0; v < 4; ++v) row[v] = page_id(ptab, (unsigned)j[v] < (unsigned)cC ? j[v] : 0, g.c.psh);
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    row[v] = (unsigned)j[v] < (unsigned)cC ? pool_row(row[v], j[v]) : -1;
-                    const float *kp = g.k_pages + (int64_t)max(row[v], 0) * g.dK;
-#pragma unroll
-                    for (int d = 0; d < DK; ++d) x[v][d] = d < g.dK ? __ldg(kp + d) : 0.f;
+            for (int v = 0; v < 2; ++v) {
+                const float w = is[v] ? weight_fast<WK>(d2[v], mr, inv_g2) : 0.f;
+                sw += w;
+                if constexpr (Sm::MMA) {
+                    const __nv_bfloat16 half = __float2bfloat16_rn(w);
+                    ga.half[0][v * 32 + lane] = __bfloat16_as_ushort(half);
+                    ga.half[1][v * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(w - __bfloat162float(half)));
+                } else {
+                    ga.w[v * 32 + lane] = w;
                 }
-                float d2[4];
-                bool lost = false;
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    d2[v] = 0.f;
-#pragma unroll
-                    for (int d = 0; d < DK; ++d) {
-                        const float f = q[v >> 1][d] - x[v][d];
-                        d2[v] = __fmaf_rn(f, f, d2[v]);
-                    }
-                    if (row[v] < 0) d2[v] = INFINITY;
-                    lost |= there(v) && row[v] < 0;
-                    if (g.idx && there(v))
-                        g.idx[(node0 + f0 + rr[v >> 1]) * g.kw + slot(v)] = (unsigned)j[v] < (unsigned)cC ? j[v] : -1;
-                }
-                if (lost) set_status(g.status, ZETA_ERR_BOUNDS);
-                if constexpr (WK == kWSoftmax) {
-                    __syncwarp();
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        float least = fminf(d2[2 * u], d2[2 * u + 1]);
-#pragma unroll
-                        for (int f = 16; f > 0; f >>= 1) least = fminf(least, __shfl_xor_sync(kFull, least, f));
-                        if (least < mr[u]) {
-                            const float f = mr[u] == INFINITY ? 0.f : __expf((least - mr[u]) * inv_g2);
-#pragma unroll
-                            for (int c = 0; c < NP; ++c) o[u][c] = mul2(o[u][c], dup2(f));
-                            sw[u] *= f;
-                            mr[u] = least;
+            }
+            __syncwarp();                                    // the weights are there
+            for (int hh = 0;; ++hh) {                        // 64 columns at a time (bf16)
+                float acc[16] = {0.f};                       // float32: a piece's sums
+                auto use = [&](const uint32_t (&y)[2][8], int i) {
+                    if constexpr (Sm::MMA) {
+                        // Halves of the weights in column 0 of B, rests in column 1.
+                        uint32_t b0 = 0u, b1 = 0u;
+                        if (g4 < 2) {
+                            b0 = *reinterpret_cast<const uint32_t *>(&ga.half[g4][i * WS + 2 * s4]);
+                            b1 = *reinterpret_cast<const uint32_t *>(&ga.half[g4][i * WS + 2 * s4 + 8]);
                         }
-                    }
-                }
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const float w = row[v] >= 0 ? weight_fast<WK>(d2[v], mr[v >> 1], inv_g2) : 0.f;
-                    sw[v >> 1] += w;
-                    sm.gather.w[warp][v >> 1][(v & 1) * 32 + lane] = w;
-                    sm.gather.row[warp][v >> 1][(v & 1) * 32 + lane] = row[v];
-                }
-                __syncwarp();
-                // Value rows in batches of 4 RPI entries of both nodes, two batches in flight.
-                constexpr int EB = 4 * RPI, NB = 64 / EB;
-                const int last = min(64, g.kw - t0);
-                uint4 bufs[2][2][4];
-                auto load = [&](uint4 (&buf)[2][4], int e0) {
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
+                        __syncwarp();
+                        operands(y, [&](int w, const uint32_t (&m)[4]) {
+                            mma16816(*reinterpret_cast<float(*)[4]>(&acc[4 * w]), m, b0, b1);
+                        });
+                    } else {
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
-                            const int pr = sm.gather.row[warp][u][e0 + grp + v * RPI];
-                            buf[u][v] = ld16_if(pool + (int64_t)max(pr, 0) * g.dV + sub * (16 / (int)sizeof(V)),
-                                                pr >= 0 && sub < ppr);
+                            const uint32_t *u = &y[v / 2][v % 2 * 4];
+                            const float2 w = dup2(ga.w[i * WS + v * RPI + lane / LPR]);
+                            const float2 a = fma2(w, make_float2(__uint_as_float(u[0]), __uint_as_float(u[1])), make_float2(acc[0], acc[1]));
+                            const float2 b = fma2(w, make_float2(__uint_as_float(u[2]), __uint_as_float(u[3])), make_float2(acc[2], acc[3]));
+                            acc[0] = a.x;
+                            acc[1] = a.y;
+                            acc[2] = b.x;
+                            acc[3] = b.y;
                         }
+                    }
                 };
-                auto add = [&](const uint4 (&buf)[2][4], int e0) {
+                for (int i = 0; i < steps; i += NB) {
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
+                    for (int o = 0; o < NB; ++o) {
+                        if (i + o < steps) use(buf[o], i + o);
+                        load(buf[o], i + o + NB, hh);
+                    }
+                }
+                const bool more = hh + 1 < H && ppr > 8;
+                if (more) {
 #pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            add_piece<V>(o[u], buf[u][v], sm.gather.w[warp][u][e0 + grp + v * RPI]);
+                    for (int o = 0; o < NB; ++o) load(buf[o], o, 1);
+                }
+                auto put = [&](int c, float a) {             // onto the sums so far
+                    float *to = win + hh * 64 + c;
+                    *to = t0 > 0 ? __fmaf_rn(scale, *to, a) : a;
                 };
-                load(bufs[0], 0);
-                if (EB < last) load(bufs[1], EB);
+                if constexpr (Sm::MMA) {
+                    if (s4 == 0) {
 #pragma unroll
-                for (int e0 = 0; e0 < NB; ++e0) {
-                    if (e0 * EB < last) add(bufs[e0 & 1], e0 * EB);
-                    if (e0 + 2 < NB && (e0 + 2) * EB < last) load(bufs[e0 & 1], (e0 + 2) * EB);
+                        for (int c = 0; c < 4; ++c) {
+                            put(column + 4 * c, acc[4 * c] + acc[4 * c + 1]);
+                            put(column + 4 * c + 2, acc[4 * c + 2] + acc[4 * c + 3]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int o = 16; o >= LPR; o >>= 1)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[c] += __shfl_xor_sync(kFull, acc[c], o);
+                    if (lane < LPR) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) put(lane * 4 + c, acc[c]);
+                    }
+                }
+                if (!more) break;
+            }
+            __syncwarp();                                    // rows and weights have been read
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sw += __shfl_xor_sync(kFull, sw, o);
+        if (lane == 0) {
+            sm.swin[r] = sw;
+            sm.mwin[r] = mr;
+        }
+        return following;
+    };
+    auto no_window = [&](int r) {
+        for (int c = lane; c < DVP; c += 32) sm.win[r][c] = 0.f;
+        if (g.idx)
+            for (int c = lane; c < g.kw; c += 32) g.idx[(node0 + f0 + r) * g.kw + c] = -1;
+        if (lane == 0) {
+            sm.swin[r] = 0.f;
+            sm.mwin[r] = INFINITY;
+        }
+        return next(r + CW);
+    };
+    int mine = nq;                                           // the node that is searched for
+
+    // ------------------------------------------------------- shared keys ---
+    // Dealt to the cluster's warps.  A lane has the weights of one node of a group and 4
+    // (float32: 2) keys: node lane / 4 and keys 2 s4, + 1, + 8, + 9; or node lane % 8 and keys
+    // 2 (lane / 8), + 1.
+    {
+        constexpr int NG = kTreeGroups, ACC = DVP / 4;
+        const bool two = nq > 8;                             // nodes in both groups
+        const int node = Sm::MMA ? g4 : lane & 7;
+        float acc[NG][ACC];                                  // MMA: [half][w][4]; else [4 nodes][DVP / 64][4]
+        float2 sum[NG];                                      // weights of first and second keys
+        float m[NG];                                         // softmax shifts
+        float q[NG][DK];
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+#pragma unroll
+            for (int e = 0; e < ACC; ++e) acc[n][e] = 0.f;
+            sum[n] = make_float2(0.f, 0.f);
+            m[n] = INFINITY;
+#pragma unroll
+            for (int d = 0; d < DK; ++d) q[n][d] = sm.q[8 * n + node][d];
+        }
+        // Weights of group n for KP pairs of keys given as 2 DK floats, one key after the other;
+        // takes: which keys the node takes, a bit each (looked at where masked).
+        auto weigh = [&](int n, const float2 (*k)[DK], float2 *w, unsigned takes, bool masked) {
+#pragma unroll
+            for (int e = 0; e < KP; ++e) {
+                float x[2 * DK];
+#pragma unroll
+                for (int d = 0; d < DK; ++d) {
+                    const float2 f = sub2(make_float2(q[n][2 * d % DK], q[n][(2 * d + 1) % DK]), k[e][d]);
+                    x[2 * d] = f.x;
+                    x[2 * d + 1] = f.y;
+                }
+                w[e] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int d = 0; d < DK; ++d) {
+                    w[e].x = __fmaf_rn(x[d], x[d], w[e].x);
+                    w[e].y = __fmaf_rn(x[DK + d], x[DK + d], w[e].y);
+                }
+                if (masked) {                                // infinitely far: no key of the node
+                    if (!(takes >> (2 * e) & 1u)) w[e].x = INFINITY;
+                    if (!(takes >> (2 * e) & 2u)) w[e].y = INFINITY;
+                }
+            }
+            if constexpr (WK == kWSoftmax) {                 // move the shift to the least d2
+                float least = fminf(w[0].x, w[0].y);
+                if (KP == 2) least = fminf(least, fminf(w[KP - 1].x, w[KP - 1].y));
+#pragma unroll
+                for (int o = Sm::MMA ? 1 : 8; o <= (Sm::MMA ? 2 : 16); o <<= 1) least = fminf(least, __shfl_xor_sync(kFull, least, o));
+                const float to = fminf(m[n], least);
+                if (__any_sync(kFull, to != m[n])) {
+                    const float f = to == m[n] ? 1.f : m[n] == INFINITY ? 0.f : __expf((to - m[n]) * inv_g2);
+                    if constexpr (Sm::MMA) {                 // the sums of nodes 2 s4 and + 1
+                        const float fa = __shfl_sync(kFull, f, 8 * s4), fb = __shfl_sync(kFull, f, 8 * s4 + 4);
+#pragma unroll
+                        for (int c = 0; c < ACC; ++c) acc[n][c] *= c & 1 ? fb : fa;
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float fr = __shfl_sync(kFull, f, (lane >> 4) * 4 + r);
+#pragma unroll
+                            for (int c = 0; c < DVP / 16; ++c) acc[n][r * (DVP / 16) + c] *= fr;
+                        }
+                    }
+                    sum[n] = mul2(sum[n], dup2(f));
+                    m[n] = to;
+                }
+            }
+            const float shift = m[n] == INFINITY ? 0.f : m[n];   // finite even where no key is taken yet
+#pragma unroll
+            for (int e = 0; e < KP; ++e) {
+                w[e] = weight_pair<WK>(w[e], shift, dup2(inv_g2));
+                if (masked) {
+                    if (!(takes >> (2 * e) & 1u)) w[e].x = 0.f;
+                    if (!(takes >> (2 * e) & 2u)) w[e].y = 0.f;
+                }
+                sum[n] = add2(sum[n], w[e]);
+            }
+        };
+        // The step's values times the weights of both groups' nodes.
+        auto multiply = [&](const float2 (*w)[Sm::KP], const uint32_t (*v)[8], auto &more) {
+            if constexpr (Sm::MMA) {
+                uint32_t b[NG][4];                           // halves and rests of two pairs
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        b[n][e] = pack_bf16(w[n][e].x, w[n][e].y);
+                        b[n][2 + e] = pack_rest(w[n][e], b[n][e]);
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int hh = 0; hh < H; ++hh)
+                    operands(v + 2 * hh, [&](int c, const uint32_t (&x)[4]) {
+#pragma unroll
+                        for (int n = 0; n < NG; ++n) {
+                            if (n == 1 && !two) break;
+                            float(&o)[4] = *reinterpret_cast<float(*)[4]>(&acc[n][16 * hh + 4 * c]);
+                            mma16816(o, x, b[n][0], b[n][1]);
+                            mma16816(o, x, b[n][2], b[n][3]);
+                        }
+                    });
+            } else {
+                float(&ws)[8][20] = sm.w[warp];
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    ws[first_key][8 * n + node] = w[n][0].x;
+                    ws[first_key + 1][8 * n + node] = w[n][0].y;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (e == 4) more(4);                     // the values of the other four keys
+#pragma unroll
+                    for (int n = 0; n < NG; ++n) {
+                        if (n == 1 && !two) break;
+                        const float4 w4 = *reinterpret_cast<const float4 *>(&ws[e][8 * n + (lane >> 4) * 4]);
+                        const float wr[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                        for (int c = 0; c < DVP / 64; ++c) {
+                            const int at = (e & 3) * (DVP / 64) + c;
+                            const uint32_t *y = &v[at / 2][at % 2 * 4];
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                float *o = &acc[n][r * (DVP / 16) + 4 * c];
+                                const float2 lo = fma2(dup2(wr[r]), make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), make_float2(o[0], o[1]));
+                                const float2 hi = fma2(dup2(wr[r]), make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])), make_float2(o[2], o[3]));
+                                o[0] = lo.x;
+                                o[1] = lo.y;
+                                o[2] = hi.x;
+                                o[3] = hi.y;
+                            }
+                        }
+                    }
                 }
                 __syncwarp();                                // the weights have been read
             }
-        } else if (g.idx) {
+        };
+        // Whole steps within a page.
+        for (int i = cw; i < n_main; i += CW) {
+            const int first = cC + i * KS, id = pt[first >> psh];
+            if ((unsigned)id >= (unsigned)g.c.pages) {
+                set_status(g.status, ZETA_ERR_BOUNDS);
+                continue;
+            }
+            const uint32_t r0 = (uint32_t)row_at(id, first);
+            const float2 *kp = reinterpret_cast<const float2 *>(kt + (uint64_t)r0 * 12u + 12 * first_key);
+            float2 kc[KP][DK];
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                if (live[u])
-                    for (int f = lane; f < g.kw; f += 32) g.idx[(node0 + f0 + rr[u]) * g.kw + f] = -1;
+            for (int e = 0; e < KP; ++e)
+#pragma unroll
+                for (int d = 0; d < DK; ++d) kc[e][d] = __ldg(kp + 12 * e + d);
+            const char *src = vt + (uint64_t)r0 * (uint32_t)vrow;
+            uint32_t v[NV / 2][8];
+            auto values = [&](int e0) {
+                if constexpr (Sm::MMA) {
+#pragma unroll
+                    for (int e = 0; e < 2 * H; ++e) {
+                        const char *p = src + (8 * (e & 1) + g4) * vrow;
+                        ld32<WIDE>(v[e], p + spot(e / 2, 0), p + spot(e / 2, 1));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < NV; ++e)
+                        *reinterpret_cast<uint4 *>(&v[e / 2][e % 2 * 4]) =
+                            ld16(src + (e0 + e / (NV / 4)) * vrow + piece + e % (NV / 4) * second);
+                }
+            };
+            values(0);
+            float2 w[NG][KP];
+#pragma unroll
+            for (int n = 0; n < NG; ++n)
+                if (n == 0 || two) weigh(n, kc, w[n], 0u, false);
+                else w[n][0] = w[n][KP - 1] = make_float2(0.f, 0.f);
+            multiply(w, v, values);
         }
+        // The lines and fences are there for the rest; the first window's search begins.
+        sm.fence[tid] = fz;
+        __syncthreads();
+        mine = next(cw);
+        if (mine < nq) search(mine);
+        // The others, key by key.
+        for (int i = cw; i < n_rest; i += CW) {
+            const bool fresh = i >= n_rest - n_node;
+            const int x0 = (fresh ? i - (n_rest - n_node) : n_main + i) * KS, end = fresh ? nn : L;
+            const char *kb = fresh ? kf : kt, *vb = fresh ? vf : vt;
+            // Row of key k of the step (any where there is none), and whether there is one.
+            auto row_of = [&](int k, bool &in) {
+                const int x = min(x0 + k, end - 1);
+                in = x0 + k < end;
+                if (fresh) return (uint32_t)x;
+                const int id = pt[(cC + x) >> psh];
+                const bool page = (unsigned)id < (unsigned)g.c.pages;
+                if (!page) set_status(g.status, ZETA_ERR_BOUNDS);
+                in = in && page;
+                return (uint32_t)(page ? row_at(id, cC + x) : 0);
+            };
+            uint32_t row[KL], vrows[2];
+            unsigned takes[NG] = {0};                        // which the node takes, a bit each
+            unsigned above[NG];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float ssum = sw[u];
+            for (int n = 0; n < NG; ++n) above[n] = fresh ? sm.above[8 * n + node][x0 >> 5] >> (x0 & 31) : ~0u;
 #pragma unroll
-            for (int f = 16; f > 0; f >>= 1) ssum += __shfl_xor_sync(kFull, ssum, f);
+            for (int e = 0; e < KL; ++e) {
+                const int key = first_key + (e & 1) + 4 * (e & 2);
+                bool in;
+                row[e] = row_of(key, in);
 #pragma unroll
-            for (int f = 16; f >= LPR; f >>= 1)
+                for (int n = 0; n < NG; ++n)
+                    if (in && (above[n] >> key & 1u)) takes[n] |= 1u << e;
+            }
+            bool in;
+            vrows[0] = Sm::MMA ? row_of(g4, in) : row[0];
+            vrows[1] = Sm::MMA ? row_of(g4 + 8, in) : row[1];
+            __syncwarp();
+            uint32_t v[NV / 2][8];
+            auto values = [&](int e0) {
+                if constexpr (Sm::MMA) {
 #pragma unroll
-                for (int c = 0; c < NP; ++c) {
-                    o[u][c].x += __shfl_xor_sync(kFull, o[u][c].x, f);
-                    o[u][c].y += __shfl_xor_sync(kFull, o[u][c].y, f);
+                    for (int e = 0; e < 2 * H; ++e) {
+                        const char *p = vb + (uint64_t)vrows[e & 1] * (uint32_t)vrow;
+                        ld32<WIDE>(v[e], p + spot(e / 2, 0), p + spot(e / 2, 1));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < NV; ++e) {
+                        const int k = e0 + e / (NV / 4);
+                        const uint32_t r = __shfl_sync(kFull, vrows[e / (NV / 4) & 1], k / 2 * 8);
+                        *reinterpret_cast<uint4 *>(&v[e / 2][e % 2 * 4]) =
+                            ld16(vb + (uint64_t)r * (uint32_t)vrow + piece + e % (NV / 4) * second);
+                    }
                 }
-            if (live[u]) {
-                if (lane < LPR) {
+            };
+            values(0);
+            float2 kc[KP][DK], w[NG][KP];
 #pragma unroll
-                    for (int c = 0; c < NP; ++c)
-                        *reinterpret_cast<float2 *>(&sm.win[rr[u]][sub * 2 * NP + 2 * c]) = o[u][c];
+            for (int e = 0; e < KP; ++e) {
+                float x[2 * DK];
+#pragma unroll
+                for (int d = 0; d < 2 * DK; ++d)
+                    x[d] = DK == 3 || d % DK < g.dK ? __ldg(reinterpret_cast<const float *>(kb + (uint64_t)row[2 * e + d / DK] * (uint32_t)krow) + d % DK) : 0.f;
+#pragma unroll
+                for (int d = 0; d < DK; ++d) kc[e][d] = make_float2(x[2 * d], x[2 * d + 1]);
+            }
+#pragma unroll
+            for (int n = 0; n < NG; ++n) weigh(n, kc, w[n], takes[n], true);
+            multiply(w, v, values);
+        }
+        float(&part)[kTreeRows][DVP + 4] = sm.part[warp];
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            float total = sum[n].x + sum[n].y;
+#pragma unroll
+            for (int o = Sm::MMA ? 1 : 8; o <= (Sm::MMA ? 2 : 16); o <<= 1) total += __shfl_xor_sync(kFull, total, o);
+            if (Sm::MMA ? s4 == 0 : lane < 8) {
+                sm.psum[warp][8 * n + node] = total;
+                sm.pmin[warp][8 * n + node] = m[n];
+            }
+            if (n == 1 && !two) break;
+            if constexpr (Sm::MMA) {
+#pragma unroll
+                for (int c = 0; c < 4 * H; ++c) {
+                    float *to = &part[8 * n + 2 * s4][c / 4 * 64 + column + c % 4 * 4];
+                    to[0] = acc[n][4 * c];
+                    to[2] = acc[n][4 * c + 2];
+                    to[DVP + 4] = acc[n][4 * c + 1];
+                    to[DVP + 6] = acc[n][4 * c + 3];
                 }
-                if (lane == 0) {
-                    sm.swin[rr[u]] = ssum;
-                    sm.mwin[rr[u]] = mr[u];
-                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int c = 0; c < DVP / 64; ++c) {
+                        const float *o = &acc[n][r * (DVP / 16) + 4 * c];
+                        *reinterpret_cast<float4 *>(&part[8 * n + (lane >> 4) * 4 + r][(lane & 15) * 4 + 64 * c]) = make_float4(o[0], o[1], o[2], o[3]);
+                    }
             }
         }
     }
 
-    // ------------------------------------------------------- shared keys ---
-    // bf16: lane (g4, s4) has nodes g4 (a) and g4 + 8 (b) and the key pairs 2 s4, +1 and +8,
-    // +9 of the warp's 16 keys.  float32: node lane % 16, keys 4 (lane / 16) .. + 3 of its 8.
-    const int g4 = lane >> 2, s4 = lane & 3;
-    const int na = Sm::MMA ? g4 : lane & 15, nb = g4 + 8;
-    constexpr int ACC = Sm::MMA ? DVP / 8 * 4 : DVP / 2;
-    float acc[ACC];                                          // MMA: [DVP / 8][4]; else [4 nodes][DVP / 8]
-#pragma unroll
-    for (int e = 0; e < ACC; ++e) acc[e] = 0.f;
-    float2 sa = make_float2(0.f, 0.f), sb = sa;              // sums of weights, first and second keys
-    float ma = INFINITY, mb = INFINITY;                      // softmax shifts
-    float2 qa[DK], qb[DK];                                   // each coordinate twice
-#pragma unroll
-    for (int d = 0; d < DK; ++d) {
-        qa[d] = dup2(sm.q[na][d]);
-        qb[d] = dup2(sm.q[nb & 15][d]);
-    }
-    const float2 ig2 = dup2(inv_g2);
-    const int nc = (g.dV + 15) >> 4;                         // 16-column pairs in use (bf16)
-    auto dist = [&](const float (&k)[4][TK], int kl, const float2 (&q)[DK]) {
-        float2 r = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int d = 0; d < DK; ++d) {
-            const float2 f = sub2(q[d], *reinterpret_cast<const float2 *>(&k[d][kl]));
-            r = fma2(f, f, r);
-        }
-        return r;
-    };
-    for (int i = 0; i < mine; ++i) {
-        cp_async_wait<1>();
-        // Tile i is here, i - 1 used up; a key without a page up to tile i + 2 is known to all.
-        const bool lost = __syncthreads_or(lost_key);
-        load_tile(i + 2);
-        put_row(i + 3, kid);
-        kid = ask_row(i + 4);
-        const int bf = i % 3, x0 = (cr + i * cs) * TK;
-        const float(&ks)[4][TK] = sm.own.k[bf];
-        const V *vs = sm.own.v[bf];
-        const int *rows = sm.rows[i & 3];
-        const bool masked = lost || x0 + TK > L;
-        // Whether node r takes the tile's key kl.
-        auto takes = [&](int r, int kl) {
-            const int x = rows[kl];
-            return x >= 0 || (x != kNoRow && (sm.above[r][~x >> 5] >> (~x & 31) & 1u));
-        };
-        auto mask = [&](int r, int kl, float2 x, float none) {
-            return make_float2(takes(r, kl) ? x.x : none, takes(r, kl + 1) ? x.y : none);
-        };
-        if constexpr (Sm::MMA) {
-            const int kb = warp * 16;
-            if (x0 + kb >= keys) continue;
-            float2 da[2], db[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int kl = kb + e * 8 + 2 * s4;
-                da[e] = dist(ks, kl, qa);
-                db[e] = dist(ks, kl, qb);
-            }
-            if constexpr (WK == kWSoftmax) {                 // move the shifts to the least d2
-                if (masked) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int kl = kb + e * 8 + 2 * s4;
-                        da[e] = mask(na, kl, da[e], INFINITY);
-                        db[e] = mask(nb, kl, db[e], INFINITY);
-                    }
-                }
-                float la = fminf(fminf(da[0].x, da[0].y), fminf(da[1].x, da[1].y));
-                float lb = fminf(fminf(db[0].x, db[0].y), fminf(db[1].x, db[1].y));
-#pragma unroll
-                for (int f = 1; f <= 2; f <<= 1) {
-                    la = fminf(la, __shfl_xor_sync(kFull, la, f));
-                    lb = fminf(lb, __shfl_xor_sync(kFull, lb, f));
-                }
-                const float xa = fminf(ma, la), xb = fminf(mb, lb);
-                const float fa = xa == ma ? 1.f : ma == INFINITY ? 0.f : __expf((xa - ma) * inv_g2);
-                const float fb = xb == mb ? 1.f : mb == INFINITY ? 0.f : __expf((xb - mb) * inv_g2);
-#pragma unroll
-                for (int nt = 0; nt < DVP / 8; ++nt) {
-                    acc[4 * nt] *= fa;
-                    acc[4 * nt + 1] *= fa;
-                    acc[4 * nt + 2] *= fb;
-                    acc[4 * nt + 3] *= fb;
-                }
-                sa = mul2(sa, dup2(fa));
-                sb = mul2(sb, dup2(fb));
-                ma = xa;
-                mb = xb;
-            }
-            // Finite even where no key is taken yet.
-            const float xa = ma == INFINITY ? 0.f : ma, xb = mb == INFINITY ? 0.f : mb;
-            uint32_t a[4], rest[4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int kl = kb + e * 8 + 2 * s4;
-                float2 wa = weight_pair<WK>(da[e], xa, ig2), wb = weight_pair<WK>(db[e], xb, ig2);
-                if (masked) {
-                    wa = mask(na, kl, wa, 0.f);
-                    wb = mask(nb, kl, wb, 0.f);
-                }
-                sa = add2(sa, wa);
-                sb = add2(sb, wb);
-                a[2 * e] = pack_bf16(wa.x, wa.y);
-                a[2 * e + 1] = pack_bf16(wb.x, wb.y);
-                rest[2 * e] = pack_rest(wa, a[2 * e]);
-                rest[2 * e + 1] = pack_rest(wb, a[2 * e + 1]);
-            }
-            __syncwarp();
-            const uint32_t vbase = smem_u32(vs);
-            const int m = lane >> 3, key = kb + (m & 1) * 8 + (lane & 7);
-#pragma unroll
-            for (int n2 = 0; n2 < DVP / 16; ++n2) {
-                if (n2 < nc) {
-                    uint32_t v[4];
-                    ldsm_x4_trans(v, vbase + (uint32_t)(key * DVP + (((n2 * 2 + (m >> 1)) ^ (key & 7)) * 8)) * 2u);
-                    float(&lo)[4] = *reinterpret_cast<float(*)[4]>(&acc[8 * n2]);
-                    float(&hi)[4] = *reinterpret_cast<float(*)[4]>(&acc[8 * n2 + 4]);
-                    mma16816(lo, a, v[0], v[1]);
-                    mma16816(hi, a, v[2], v[3]);
-                    mma16816(lo, rest, v[0], v[1]);
-                    mma16816(hi, rest, v[2], v[3]);
-                }
-            }
-        } else {
-            const int kb = warp * 8;
-            if (x0 + kb >= keys) continue;
-            const int kl = kb + 4 * (lane >> 4);
-            float2 d0 = dist(ks, kl, qa), d1 = dist(ks, kl + 2, qa);
-            const int rg = lane >> 3, cg4 = lane & 7;        // 4 nodes, columns 4 cg4 + 32 j
-            if constexpr (WK == kWSoftmax) {
-                if (masked) {
-                    d0 = mask(na, kl, d0, INFINITY);
-                    d1 = mask(na, kl + 2, d1, INFINITY);
-                }
-                float la = fminf(fminf(d0.x, d0.y), fminf(d1.x, d1.y));
-                la = fminf(la, __shfl_xor_sync(kFull, la, 16));
-                const float xa = fminf(ma, la);
-                const float fa = xa == ma ? 1.f : ma == INFINITY ? 0.f : __expf((xa - ma) * inv_g2);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float f = __shfl_sync(kFull, fa, rg * 4 + r);
-#pragma unroll
-                    for (int c = 0; c < DVP / 8; ++c) acc[r * (DVP / 8) + c] *= f;
-                }
-                sa = mul2(sa, dup2(fa));
-                ma = xa;
-            }
-            const float xa = ma == INFINITY ? 0.f : ma;
-            float2 w0 = weight_pair<WK>(d0, xa, ig2), w1 = weight_pair<WK>(d1, xa, ig2);
-            if (masked) {
-                w0 = mask(na, kl, w0, 0.f);
-                w1 = mask(na, kl + 2, w1, 0.f);
-            }
-            sa = add2(sa, add2(w0, w1));
-            float(&ws)[8][20] = sm.w[warp];
-            ws[kl - kb][na] = w0.x;
-            ws[kl - kb + 1][na] = w0.y;
-            ws[kl - kb + 2][na] = w1.x;
-            ws[kl - kb + 3][na] = w1.y;
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float4 w = *reinterpret_cast<const float4 *>(&ws[e][rg * 4]);
-                const float wr[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int c = 0; c < DVP / 32; ++c) {
-                    const float4 v = *reinterpret_cast<const float4 *>(vs + (kb + e) * DVP + cg4 * 4 + 32 * c);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float *o = &acc[r * (DVP / 8) + 4 * c];
-                        const float2 lo = fma2(dup2(wr[r]), make_float2(v.x, v.y), make_float2(o[0], o[1]));
-                        const float2 hi = fma2(dup2(wr[r]), make_float2(v.z, v.w), make_float2(o[2], o[3]));
-                        o[0] = lo.x;
-                        o[1] = lo.y;
-                        o[2] = hi.x;
-                        o[3] = hi.y;
-                    }
-                }
-            }
-            __syncwarp();                                    // the weights have been read
-        }
-    }
-    cp_async_wait<0>();
-    __syncthreads();                                         // the tiles' memory is free
+    while (mine < nq) mine = chunk > 0 ? take_window(mine) : no_window(mine);
 
     // ---------------------------------------------------------- epilogue ---
-    float suma = sa.x + sa.y, sumb = sb.x + sb.y;
-    if constexpr (Sm::MMA) {
-#pragma unroll
-        for (int f = 1; f <= 2; f <<= 1) {
-            suma += __shfl_xor_sync(kFull, suma, f);
-            sumb += __shfl_xor_sync(kFull, sumb, f);
-        }
-#pragma unroll
-        for (int nt = 0; nt < DVP / 8; ++nt) {
-            const int col = nt * 8 + 2 * s4;
-            *reinterpret_cast<float2 *>(&sm.part[warp][na][col]) = make_float2(acc[4 * nt], acc[4 * nt + 1]);
-            *reinterpret_cast<float2 *>(&sm.part[warp][nb][col]) = make_float2(acc[4 * nt + 2], acc[4 * nt + 3]);
-        }
-        if (s4 == 0) {
-            sm.psum[warp][na] = suma;
-            sm.psum[warp][nb] = sumb;
-            sm.pmin[warp][na] = ma;
-            sm.pmin[warp][nb] = mb;
-        }
-    } else {
-        suma += __shfl_xor_sync(kFull, suma, 16);
-        const int rg = lane >> 3, cg4 = lane & 7;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int c = 0; c < DVP / 32; ++c) {
-                const float *o = &acc[r * (DVP / 8) + 4 * c];
-                *reinterpret_cast<float4 *>(&sm.part[warp][rg * 4 + r][cg4 * 4 + 32 * c]) = make_float4(o[0], o[1], o[2], o[3]);
-            }
-        if (lane < 16) {
-            sm.psum[warp][na] = suma;
-            sm.pmin[warp][na] = ma;
-        }
-    }
+    // Node r is finished by block r % cs, which has its window: the warps' parts of its sums are
+    // joined in each block, the blocks' by that one.
     cg::cluster_group cl = cg::this_cluster();
-    if (cs > 1) cl.sync(); else __syncthreads();
-    const int parts = NW * cs;
-    V *out = static_cast<V *>(g.out);
-    for (int r = cw; r < nq; r += CW) {                      // the nodes whose windows this warp has
-        if (sm.depth[r] < 0) continue;
-        float ps = 0.f, pm = INFINITY;
-        if (lane < parts) {
-            const Sm *o = cs > 1 ? cl.map_shared_rank(&sm, lane / NW) : &sm;
-            ps = o->psum[lane % NW][r];
-            pm = o->pmin[lane % NW][r];
-        }
-        float f = 1.f, fw = 1.f;
+    __syncthreads();
+    // P parts onto one shift: factors of the parts, of the window (where it takes part), and the
+    // sum of weights.
+    auto join = [&](int P, int r, bool window, auto psum, auto pmin) {
+        float total = window ? sm.swin[r] : 0.f;
         if constexpr (WK == kWSoftmax) {
-            float m = pm;
-#pragma unroll
-            for (int e = 16; e > 0; e >>= 1) m = fminf(m, __shfl_xor_sync(kFull, m, e));
-            const float mw = sm.mwin[r];
-            m = fminf(m, mw);
-            f = pm == INFINITY ? 0.f : __expf((m - pm) * inv_g2);
-            fw = mw == INFINITY ? 0.f : __expf((m - mw) * inv_g2);
+            float least = window ? sm.mwin[r] : INFINITY;
+            for (int p = 0; p < P; ++p) least = fminf(least, pmin(p));
+            auto factor = [&](float m) { return m == INFINITY ? 0.f : __expf((least - m) * inv_g2); };
+            if (window) total *= sm.factor[P][r] = factor(sm.mwin[r]);
+            for (int p = 0; p < P; ++p) total = __fmaf_rn(sm.factor[p][r] = factor(pmin(p)), psum(p), total);
+            sm.least[r] = least;
+        } else {
+            for (int p = 0; p < P; ++p) total += psum(p);
         }
-        float total = f * ps;
+        sm.total[r] = total;
+    };
+    auto add = [&](float2 o, int p, int r, float2 x) { return WK == kWSoftmax ? fma2(dup2(sm.factor[p][r]), x, o) : add2(o, x); };
+    if (cs > 1) {
+        if (tid < nq)
+            join(NW, tid, false, [&](int p) { return sm.psum[p][tid]; }, [&](int p) { return sm.pmin[p][tid]; });
+        __syncthreads();
+        for (int i = tid; i < kTreeRows * (DVP / 2); i += NT) {
+            const int r = i / (DVP / 2), col = i % (DVP / 2) * 2;
+            if (r >= nq) break;
+            float2 o = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 16; e > 0; e >>= 1) total += __shfl_xor_sync(kFull, total, e);
-        total = __fmaf_rn(fw, sm.swin[r], total);
-        float o[DVP / 32];
-#pragma unroll
-        for (int e = 0; e < DVP / 32; ++e) o[e] = fw * sm.win[r][lane + 32 * e];
-        for (int p = 0; p < parts; ++p) {
-            const Sm *from = cs > 1 ? cl.map_shared_rank(&sm, p / NW) : &sm;
-            const float fp = __shfl_sync(kFull, f, p);
-#pragma unroll
-            for (int e = 0; e < DVP / 32; ++e) o[e] = __fmaf_rn(fp, from->part[p % NW][r][lane + 32 * e], o[e]);
+            for (int p = 0; p < NW; ++p) o = add(o, p, r, *reinterpret_cast<const float2 *>(&sm.part[p][r][col]));
+            *reinterpret_cast<float2 *>(&sm.part[0][r][col]) = o;
         }
-        const int64_t rid = node0 + f0 + r;
-        bool bad = false;
+        if (tid < nq) {
+            sm.psum[0][tid] = sm.total[tid];
+            sm.pmin[0][tid] = WK == kWSoftmax ? sm.least[tid] : 0.f;
+        }
+        cl.sync();
+    }
+    const int parts = cs > 1 ? cs : NW;
+    auto of = [&](int p) { return cs > 1 ? cl.map_shared_rank(&sm, p) : &sm; };
+    const bool finish = tid < nq && tid % cs == cr && sm.depth[min(tid, kTreeRows - 1)] >= 0;
+    if (finish) {
+        join(parts, tid, true, [&](int p) { return of(p)->psum[cs > 1 ? 0 : p][tid]; }, [&](int p) { return of(p)->pmin[cs > 1 ? 0 : p][tid]; });
+        g.rowsum[node0 + f0 + tid] = sm.total[tid];
+    }
+    __syncthreads();
+    // Two columns a thread.
+    bool bad = false;
+    V *out = static_cast<V *>(g.out) + (node0 + f0) * g.dV;
+    for (int i = tid; i < kTreeRows * (DVP / 2); i += NT) {
+        const int r = i / (DVP / 2) * cs + cr, col = i % (DVP / 2) * 2;
+        if (r >= nq) break;
+        if (sm.depth[r] < 0 || col >= g.dV) continue;
+        float2 o = *reinterpret_cast<const float2 *>(&sm.win[r][col]);
+        if (WK == kWSoftmax) o = mul2(o, dup2(sm.factor[parts][r]));
+        if (cs == 1) {
 #pragma unroll
-        for (int e = 0; e < DVP / 32; ++e) {
-            const int col = lane + 32 * e;
-            if (col < g.dV) {
-                const float x = __fdiv_rn(o[e], total);
-                bad |= !isfinite(x);
-                VT<V>::st(out + rid * g.dV + col, x);
-            }
+            for (int p = 0; p < NW; ++p) o = add(o, p, r, *reinterpret_cast<const float2 *>(&sm.part[p][r][col]));
+        } else {
+            for (int p = 0; p < cs; ++p) o = add(o, p, r, *reinterpret_cast<const float2 *>(&of(p)->part[0][r][col]));
         }
-        if (lane == 0) g.rowsum[rid] = total;
-        if (__any_sync(kFull, bad)) {
-            __syncwarp();                                    // the fast result is written first
-            slow_node<V, DVP, DK, WK>(g, rid, b, h, seq.start, cC > 0 ? sm.wst[r] : 0, sm.above[r], inv_g2);
-        }
+        o.x = __fdiv_rn(o.x, sm.total[r]);
+        o.y = __fdiv_rn(o.y, sm.total[r]);
+        if (!isfinite(o.x) || !isfinite(o.y)) sm.again[r] = bad = true;
+        if constexpr (Sm::MMA) *reinterpret_cast<__nv_bfloat162 *>(out + r * g.dV + col) = __floats2bfloat162_rn(o.x, o.y);
+        else *reinterpret_cast<float2 *>(out + r * g.dV + col) = o;
+    }
+    if (__syncthreads_or(bad)) {                             // the fast results are written first
+        for (int r = cw; r < nq; r += CW)
+            if (sm.depth[r] >= 0 && sm.again[r])
+                slow_node<V, DVP, DK, WK>(g, node0 + f0 + r, b, h, seq.start, cC > 0 ? sm.wst[r] : 0, sm.above[r], inv_g2);
     }
     if (cs > 1) cl.sync();                                   // read before any block ends
 }
 
-template <typename V, int DVP, int DK, int WK>
+template <typename V, int DVP, int DK, int WK, bool WIDE>
 cudaError_t run_tree_tile(const Prob &p, const TreeArgs &g, int cs, cudaStream_t st) {
     static PerDeviceOnce once;
     constexpr size_t smem = sizeof(TreeSmem<V, DVP>);
     cudaError_t e = once.run([] {
-        return cudaFuncSetAttribute(tree_tile_kernel<V, DVP, DK, WK>,
+        return cudaFuncSetAttribute(tree_tile_kernel<V, DVP, DK, WK, WIDE>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
     if (e != cudaSuccess) return e;
@@ -799,16 +955,16 @@ cudaError_t run_tree_tile(const Prob &p, const TreeArgs &g, int cs, cudaStream_t
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = cs > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, tree_tile_kernel<V, DVP, DK, WK>, g, cs);
+    e = cudaLaunchKernelEx(&cfg, tree_tile_kernel<V, DVP, DK, WK, WIDE>, g, cs);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <typename V, int DVP>
+template <typename V, int DVP, bool WIDE>
 cudaError_t dispatch_tree_tile(const Prob &p, const TreeArgs &g, int cs, cudaStream_t st) {
 #define ZETA_TREE(D)                                                                  \
-    (p.wk == kWSoftmax     ? run_tree_tile<V, DVP, D, kWSoftmax>(p, g, cs, st)        \
-     : p.wk == kWInvEuclid ? run_tree_tile<V, DVP, D, kWInvEuclid>(p, g, cs, st)      \
-                           : run_tree_tile<V, DVP, D, kWCauchy>(p, g, cs, st))
+    (p.wk == kWSoftmax     ? run_tree_tile<V, DVP, D, kWSoftmax, WIDE>(p, g, cs, st)        \
+     : p.wk == kWInvEuclid ? run_tree_tile<V, DVP, D, kWInvEuclid, WIDE>(p, g, cs, st)      \
+                           : run_tree_tile<V, DVP, D, kWCauchy, WIDE>(p, g, cs, st))
     return p.dK == 3 ? ZETA_TREE(3) : ZETA_TREE(4);
 #undef ZETA_TREE
 }
