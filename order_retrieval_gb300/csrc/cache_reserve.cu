@@ -9,11 +9,11 @@
 // The e-th page back is the e-th one out again: a shrink undoes a grow to the last
 // place of the list.
 //
-// One cluster of eight blocks, a range of sequences each: sums of r and m, exchanged
-// through distributed shared memory, give every block its offsets; the pages go back,
-// and a cluster barrier stands between that and the pages that are taken.  A thread
-// takes a sequence for the sums, a warp a sequence for its pages, the block all rows of
-// its sequences for the row numbers.  No workspace, one launch.
+// One cluster of eight blocks, a range of sequences each and of those some to a thread: one
+// sum over r and m, its totals exchanged through distributed shared memory, gives every
+// thread its offsets; the pages go back, and where there were any a cluster barrier stands
+// between that and the pages that are taken.  A warp moves a sequence's pages (eight a lane
+// under way), the block writes the row numbers of its sequences.  No workspace, one launch.
 #include <cooperative_groups.h>
 
 #include "cache_tree.cuh"
@@ -23,38 +23,52 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kBlocks = 8;
+constexpr int kBlocks = 8;
+constexpr int kFlight = 8;             // pages a lane moves at a time
 
 struct Lists {
     int32_t *table, *held, *free_list, *free_count, *granted, *slots, *status;
     int B, N;
 };
 
-// Exclusive sum over the block's threads; *total gets the sum.
-__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *sums, int64_t *total) {
+// Exclusive sums of x and y over the block's threads; the totals.
+struct Two {
+    int64_t x, y;
+};
+template <int kWarps>
+__device__ __forceinline__ Two block_scan(Two in, Two *sums, Two &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t in = x;
+    auto scan = [&](Two v) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(kFull, in, o);
-        if (lane >= o) in += y;
-    }
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(kFull, v.x, o), y = __shfl_up_sync(kFull, v.y, o);
+            if (lane >= o) {
+                v.x += x;
+                v.y += y;
+            }
+        }
+        return v;
+    };
+    const Two mine = scan(in);
     __syncthreads();                                 // the array is free
-    if (lane == 31) sums[warp] = in;
+    if (lane == 31) sums[warp] = mine;
     __syncthreads();
-    int64_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sums[w];
-        all += sums[w];
-    }
-    *total = all;
-    return before + in - x;
+    const Two warps = scan(lane < kWarps ? sums[lane] : Two{0, 0});
+    total = Two{__shfl_sync(kFull, warps.x, 31), __shfl_sync(kFull, warps.y, 31)};
+    const int64_t bx = __shfl_sync(kFull, warps.x, warp - 1 & 31), by = __shfl_sync(kFull, warps.y, warp - 1 & 31);
+    return Two{(warp ? bx : 0) + mine.x - in.x, (warp ? by : 0) + mine.y - in.y};
 }
 
+// A cluster barrier in two halves.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
+
+template <int kThreads>
 __global__ void __cluster_dims__(kBlocks, 1, 1) __launch_bounds__(kThreads)
 cache_reserve_kernel(Cache c, Lists l) {
-    __shared__ int64_t sums[kWarps], mine[2], offs[kThreads];
+    constexpr int kWarps = kThreads / 32;
+    __shared__ Two sums[kWarps], mine;
+    __shared__ int64_t offs[kThreads];
     __shared__ int lo_sh[kThreads], hi_sh[kThreads], start_sh[kThreads], got_sh[kThreads];
     cg::cluster_group cl = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -78,70 +92,85 @@ cache_reserve_kernel(Cache c, Lists l) {
         return true;
     };
 
-    // Sums of the block's range, and what the blocks before it and all have.
-    int64_t back = 0, more = 0;
-    for (int b = b0 + tid; b < b1; b += kThreads) {
+    // The thread's sequences b(tid, 0), b(tid, 1), ..: what they need, what all before them do.
+    const int each = (b1 - b0 + kThreads - 1) / kThreads;
+    auto seq_of = [&](int s, int i) { return b0 + s * each + i; };
+    Two need{0, 0}, all;                             // back and more
+    for (int i = 0; i < each && seq_of(tid, i) < b1; ++i) {
         int start, count, held, want;
-        sizes(b, start, count, held, want);
-        back += max(held - want, 0);
-        more += max(want - held, 0);
+        sizes(seq_of(tid, i), start, count, held, want);
+        need.x += max(held - want, 0);
+        need.y += max(want - held, 0);
     }
-    int64_t all_back, all_more;
-    block_scan(back, sums, &all_back);
-    block_scan(more, sums, &all_more);
-    if (tid == 0) {
-        mine[0] = all_back;
-        mine[1] = all_more;
-    }
+    Two at = block_scan<kWarps>(need, sums, all);
+    if (tid == 0) mine = all;
     cl.sync();
-    int64_t at_back = 0, at_more = 0, R = 0;
+    int64_t R = 0;
+#pragma unroll
     for (int p = 0; p < kBlocks; ++p) {
-        const int64_t *o = cl.map_shared_rank(mine, p);
+        const Two *o = cl.map_shared_rank(&mine, p);
         if (p < rank) {
-            at_back += o[0];
-            at_more += o[1];
+            at.x += o->x;
+            at.y += o->y;
         }
-        R += o[0];
+        R += o->x;
     }
+    cluster_arrive();                                // the sums have been read
     // A list that is not one: nothing moves.
     const bool sound = F0 >= 0 && F0 + R <= c.pages;
     if (!sound && tid == 0) set_status(l.status, ZETA_ERR_BOUNDS);
     const int64_t F = F0 + R;
-    if (sound && rank == 0 && tid == 0) *l.free_count = (int)F;   // every block has read it
 
-    for (int s0 = b0; s0 < b1 && sound; s0 += kThreads) {
-        const int b = s0 + tid;
-        int start = 0, count = 0, held = 0, want = 0;
-        if (b < b1) sizes(b, start, count, held, want);
-        int64_t total;
-        offs[tid] = at_back + block_scan(max(held - want, 0), sums, &total);
-        at_back += total;
-        lo_sh[tid] = want;
-        hi_sh[tid] = held;
-        if (b < b1 && held > want) l.held[b] = want;
-        __syncthreads();
-        for (int s = warp; s < min(kThreads, b1 - s0); s += kWarps) {
-            int32_t *tab = l.table + (int64_t)(s0 + s) * c.tlen;
-            const int lo = lo_sh[s], hi = hi_sh[s];
-            for (int e = lo + lane; e < hi; e += 32) {
-                const int id = tab[e];
-                if ((unsigned)id >= (unsigned)c.pages) set_status(l.status, ZETA_ERR_BOUNDS);
-                l.free_list[F - 1 - (offs[s] + e - lo)] = id;
-                tab[e] = -1;
-            }
+    // Pages [lo, hi) of a table, kFlight a lane at a time: get(e), then put(e, id).
+    auto move = [&](int lo, int hi, auto get, auto put) {
+        for (int e0 = lo + lane; e0 < hi; e0 += 32 * kFlight) {
+            int id[kFlight];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u)
+                if (e0 + 32 * u < hi) id[u] = get(e0 + 32 * u);
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u)
+                if (e0 + 32 * u < hi) {
+                    if ((unsigned)id[u] >= (unsigned)c.pages) set_status(l.status, ZETA_ERR_BOUNDS);
+                    put(e0 + 32 * u, id[u]);
+                }
         }
-        __syncthreads();
+    };
+    if (sound && R > 0) {
+        if (rank == 0 && tid == 0) *l.free_count = (int)F;     // every block has read it
+        for (int i = 0; i < each && all.x > 0; ++i) {
+            const int b = seq_of(tid, i);
+            int start = 0, count = 0, held = 0, want = 0;
+            if (b < b1) sizes(b, start, count, held, want);
+            offs[tid] = at.x;
+            at.x += max(held - want, 0);
+            lo_sh[tid] = want;
+            hi_sh[tid] = held;
+            if (b < b1 && held > want) l.held[b] = want;
+            __syncthreads();
+            for (int s = warp; s < kThreads && seq_of(s, i) < b1; s += kWarps) {
+                int32_t *tab = l.table + (int64_t)seq_of(s, i) * c.tlen;
+                const int lo = lo_sh[s];
+                const int64_t to = F - 1 - offs[s] + lo;
+                move(lo, hi_sh[s], [&](int e) { return tab[e]; },
+                     [&](int e, int id) {
+                         l.free_list[to - e] = id;
+                         tab[e] = -1;
+                     });
+            }
+            __syncthreads();
+        }
+        cluster_wait();
+        cl.sync();                                   // the list is whole
     }
-    cl.sync();                                       // the list is whole; the sums have been read
 
-    for (int s0 = b0; s0 < b1; s0 += kThreads) {
-        const int b = s0 + tid, ns = min(kThreads, b1 - s0);
+    for (int i = 0; i < each; ++i) {
+        const int b = seq_of(tid, i), ns = min(kThreads, (b1 - b0 - i + each - 1) / each);
         int start = 0, count = 0, held = 0, want = 0;
         const bool fits = b < b1 && sizes(b, start, count, held, want);
         const int m = max(want - held, 0);
-        int64_t total;
-        const int64_t off = at_more + block_scan(m, sums, &total);
-        at_more += total;
+        const int64_t off = at.y;
+        at.y += m;
         const bool ok = fits && sound && (m == 0 || off + m <= F);
         offs[tid] = off;
         lo_sh[tid] = held;
@@ -156,30 +185,50 @@ cache_reserve_kernel(Cache c, Lists l) {
         }
         __syncthreads();
         for (int s = warp; s < ns; s += kWarps) {
-            int32_t *tab = l.table + (int64_t)(s0 + s) * c.tlen;
-            const int lo = lo_sh[s], hi = hi_sh[s];
-            for (int e = lo + lane; e < hi; e += 32) {
-                const int id = l.free_list[F - 1 - (offs[s] + e - lo)];
-                if ((unsigned)id >= (unsigned)c.pages) set_status(l.status, ZETA_ERR_BOUNDS);
-                tab[e] = id;
-            }
+            int32_t *tab = l.table + (int64_t)seq_of(s, i) * c.tlen;
+            const int lo = lo_sh[s];
+            const int64_t from = F - 1 - offs[s] + lo;
+            move(lo, hi_sh[s], [&](int e) { return l.free_list[from - e]; },
+                 [&](int e, int id) { tab[e] = id; });
         }
         __syncthreads();
         if (l.slots) {
-            for (int64_t x = tid; x < (int64_t)ns * c.n; x += kThreads) {
-                const int s = (int)(x / c.n), t = (int)(x - (int64_t)s * c.n);
-                int slot = -1;
-                if (t < got_sh[s]) {
-                    const int i = start_sh[s] + t;
-                    const int id = l.table[(int64_t)(s0 + s) * c.tlen + (i >> c.psh)];
-                    if ((unsigned)id < (unsigned)c.pages) slot = (id << c.psh) | (i & c.pmask);
-                    else set_status(l.status, ZETA_ERR_BOUNDS);
+            // Four rows of a sequence a thread.
+            const unsigned n = (unsigned)c.n, quads = (n + 3) / 4, cells = (unsigned)ns * quads;
+            const bool whole = n % 4 == 0 && (reinterpret_cast<uintptr_t>(l.slots) & 15) == 0;
+            for (unsigned x = tid; x < cells; x += kThreads) {
+                const int s = (int)(x / quads), t0 = (int)(x - (unsigned)s * quads) * 4, got = got_sh[s];
+                const int j0 = start_sh[s] + t0;
+                const int32_t *tab = l.table + (int64_t)seq_of(s, i) * c.tlen;
+                int slot[4], at = -1, id = -1;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    slot[u] = -1;
+                    if (t0 + u >= got) continue;
+                    const int j = j0 + u;
+                    if (j >> c.psh != at) {
+                        at = j >> c.psh;
+                        id = tab[at];
+                        if ((unsigned)id >= (unsigned)c.pages) {
+                            set_status(l.status, ZETA_ERR_BOUNDS);
+                            id = -1;
+                        }
+                    }
+                    if (id >= 0) slot[u] = (id << c.psh) | (j & c.pmask);
                 }
-                l.slots[(int64_t)s0 * c.n + x] = slot;
+                int32_t *to = l.slots + (int64_t)seq_of(s, i) * c.n + t0;
+                if (whole) {
+                    *reinterpret_cast<int4 *>(to) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (t0 + u < c.n) to[u] = slot[u];
+                }
             }
         }
         __syncthreads();
     }
+    if (!(sound && R > 0)) cluster_wait();           // no block ends before its sums have been read
 }
 
 }  // namespace
@@ -188,7 +237,10 @@ cudaError_t launch_cache_reserve(const Prob &p, const Cache &c, int32_t *table, 
                                  int32_t *free_list, int32_t *free_count, int32_t *granted,
                                  int32_t *slots, int32_t *status, cudaStream_t st) {
     const Lists l{table, held, free_list, free_count, granted, slots, status, p.B, p.N};
-    cache_reserve_kernel<<<kBlocks, kThreads, 0, st>>>(c, l);
+    // Blocks of 1024 threads take a call of many rows: 512 sequences of one row 5.8 us a call in
+    // blocks of 512, 6.6 of 1024; 256 of 1024 rows, 90 K pages moved, 16.2 and 14.2.
+    if ((int64_t)p.B * c.n < 16384) cache_reserve_kernel<512><<<kBlocks, 512, 0, st>>>(c, l);
+    else cache_reserve_kernel<1024><<<kBlocks, 1024, 0, st>>>(c, l);
     return cudaGetLastError();
 }
 

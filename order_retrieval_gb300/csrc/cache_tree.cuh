@@ -49,6 +49,32 @@ __device__ __forceinline__ int climb(const int *parent, int t, Visit visit) {
     return depth;
 }
 
+// The same with the line as bits of `above`; run: bit t set where parent[t] == t - 1, t > 0,
+// so that nodes that hang below one another by number (a chain) are one step of up to 32.
+__device__ __forceinline__ int climb_bits(const int *parent, const uint32_t *run, int t,
+                                          uint32_t *above) {
+    int depth = -1;
+    while (t >= 0) {
+        const int w = t >> 5;
+        const uint32_t upto = 0xffffffffu >> (31 - (t & 31));
+        const uint32_t ends = ~run[w] & upto;        // nodes whose parent is not the one before
+        const int s = ends ? 31 - __clz(ends) : 0;
+        const uint32_t part = upto & (0xffffffffu << s);
+        above[w] |= part;
+        depth += __popc(part);
+        const int top = w * 32 + s, p = ends ? parent[top] : top - 1;
+        if (p < -1 || p >= top) return -1;
+        t = p;
+    }
+    return depth;
+}
+
+// The bits of `run` for nodes 32 w .. 32 w + 31 (a warp).
+__device__ __forceinline__ uint32_t run_bits(const int *parent, int w, int nodes) {
+    const int u = w * 32 + (threadIdx.x & 31);
+    return __ballot_sync(kFull, u < nodes && u > 0 && parent[u] == u - 1);
+}
+
 cudaError_t launch_cache_attend_tree(const Prob &p, const TreeArgs &g, cudaStream_t st);
 cudaError_t launch_cache_accept(const Prob &p, const Cache &c, const int32_t *parent,
                                 const int32_t *leaf, const float *k, const void *v, float *k_pages,

@@ -36,6 +36,12 @@ cudaError_t launch_tree_tile_f32(const Prob &p, const TreeArgs &g, int cs, cudaS
 
 namespace {
 
+#ifndef ZETA_TREE_NG
+#define ZETA_TREE_NG 2
+#endif
+#ifndef ZETA_TREE_NG2
+#define ZETA_TREE_NG2 1
+#endif
 #ifndef ZETA_TREE_DEPTH
 #define ZETA_TREE_DEPTH 1
 #endif
@@ -48,16 +54,17 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kTreeWarps = 8, kTreeThreads = 32 * kTreeWarps;
-constexpr int kTreeRows = 16, kTreeGroups = kTreeRows / 8;   // nodes of a block; in groups of 8
+constexpr int kTreeRows = 16;                        // nodes of a block, at most
 constexpr int kTreeFences = 256;
 constexpr int kTreeTable = 1024;                     // pages whose numbers lie in shared memory
 
 template <typename V, int DVP>
 struct TreeSmem {
     static constexpr bool MMA = sizeof(V) == 2;
+    static constexpr int NG = DVP == 64 ? ZETA_TREE_NG : ZETA_TREE_NG2, ROWS = 8 * NG;   // nodes of a block, in groups of 8
     static constexpr int KS = MMA ? 16 : 8, KL = KS / 4, KP = KL / 2;    // shared keys a step, a lane; pairs
     static constexpr int NV = DVP / 16;              // 16-byte pieces of them a lane holds (float32: of four keys)
-    float part[kTreeWarps][kTreeRows][DVP + 4];      // sums over shared keys, warp by warp
+    float part[kTreeWarps][ROWS][DVP + 4];      // sums over shared keys, warp by warp
     struct {                                         // of a warp's window
         int row[64];
         union {
@@ -72,17 +79,17 @@ struct TreeSmem {
     float w[MMA ? 1 : kTreeWarps][8][20];            // float32, shared keys: weights [key][node]
     union {
         int parent[kMaxDraft];
-        float win[kTreeRows][DVP + 4];               // window sums
+        float win[ROWS][DVP + 4];               // window sums
     };
     uint32_t run[kMaxDraft / 32];                    // bit u: parent[u] == u - 1
-    uint32_t above[kTreeRows][kMaxDraft / 32];       // nodes of a line
-    float q[kTreeRows][4];
-    int depth[kTreeRows], wst[kTreeRows];
-    float swin[kTreeRows], mwin[kTreeRows];
-    float psum[kTreeWarps][kTreeRows], pmin[kTreeWarps][kTreeRows];
-    float factor[kTreeWarps + 1][kTreeRows], least[kTreeRows];   // softmax: of the parts and the window; the shift
-    float total[kTreeRows];
-    bool again[kTreeRows];                           // not finite
+    uint32_t above[ROWS][kMaxDraft / 32];       // nodes of a line
+    float q[ROWS][4];
+    int depth[ROWS], wst[ROWS];
+    float swin[ROWS], mwin[ROWS];
+    float psum[kTreeWarps][ROWS], pmin[kTreeWarps][ROWS];
+    float factor[kTreeWarps + 1][ROWS], least[ROWS];   // softmax: of the parts and the window; the shift
+    float total[ROWS];
+    bool again[ROWS];                           // not finite
 };
 
 __device__ __forceinline__ uint4 ld16(const void *p) {
@@ -104,26 +111,6 @@ __device__ __forceinline__ void ld32(uint32_t (&x)[8], const char *p, const char
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
         x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     }
-}
-
-// The line of node t as bits of `above` (words of `run` read from the top one down);
-// its depth, -1 where a parent is no earlier node.
-__device__ __forceinline__ int climb_bits(const int *parent, const uint32_t *run, int t,
-                                          uint32_t *above) {
-    int depth = -1;
-    while (t >= 0) {
-        const int w = t >> 5;
-        const uint32_t upto = 0xffffffffu >> (31 - (t & 31));
-        const uint32_t ends = ~run[w] & upto;        // nodes whose parent is not the one before
-        const int s = ends ? 31 - __clz(ends) : 0;
-        const uint32_t part = upto & (0xffffffffu << s);
-        above[w] |= part;
-        depth += __popc(part);
-        const int top = w * 32 + s, p = ends ? parent[top] : top - 1;
-        if (p < -1 || p >= top) return -1;
-        t = p;
-    }
-    return depth;
 }
 
 // One node key by key (a warp, lanes over the value columns).
@@ -197,25 +184,25 @@ template <typename V, int DVP, int DK, int WK, bool WIDE>
 __global__ void __launch_bounds__(kTreeThreads, ZETA_TREE_BLOCKS)
 tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     using Sm = TreeSmem<V, DVP>;
-    constexpr int NT = kTreeThreads, NW = kTreeWarps;
+    constexpr int NT = kTreeThreads, NW = kTreeWarps, ROWS = Sm::ROWS;
     constexpr int PPR = DVP * (int)sizeof(V) / 16;           // 16-byte pieces of a padded row
     extern __shared__ __align__(16) unsigned char raw[];
     Sm &sm = *reinterpret_cast<Sm *>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cr = cs == 1 ? 0 : (int)(blockIdx.x % (unsigned)cs);   // block in the cluster
-    const int f0 = (int)(blockIdx.x / (unsigned)cs) * kTreeRows;     // first node
+    const int f0 = (int)(blockIdx.x / (unsigned)cs) * ROWS;     // first node
     const int s = blockIdx.y, b = s / g.H, h = s - b * g.H;
     const int64_t node0 = (int64_t)s * g.c.n;                // the slice's node 0
     const int32_t *ptab = g.c.ptab + (int64_t)b * g.c.tlen, *otab = g.c.otab + (int64_t)b * g.c.tlen;
     // What does not depend on the lengths is asked for with them.
-    const int ahead = min(f0 + kTreeRows, g.c.n), pages_near = min(g.c.tlen, kTreeTable);
+    const int ahead = min(f0 + ROWS, g.c.n), pages_near = min(g.c.tlen, kTreeTable);
     const int parent = tid < ahead ? __ldg(g.parent + (int64_t)b * g.c.n + tid) : 0;
-    const float q_in = tid < kTreeRows * 4 && f0 + (tid >> 2) < ahead && (tid & 3) < g.dK
+    const float q_in = tid < ROWS * 4 && f0 + (tid >> 2) < ahead && (tid & 3) < g.dK
                            ? __ldg(g.q + (node0 + f0 + (tid >> 2)) * g.dK + (tid & 3)) : 0.f;
     for (int e = tid; e < pages_near; e += NT) sm.ptab[e] = __ldg(ptab + e);
     const Seq seq = drafts_of(g.c, b, g.N, g.status);
     if (f0 >= seq.count) return;                             // the whole cluster returns
-    const int nn = min(f0 + kTreeRows, seq.count), nq = nn - f0;
+    const int nn = min(f0 + ROWS, seq.count), nq = nn - f0;
     const int chunk = seq.start / g.C, cC = chunk * g.C, L = seq.start - cC;
     const float gm = __ldg(g.gamma + h);
     const float inv_g2 = __frcp_rn(gm * gm);
@@ -236,9 +223,9 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     // ------------------------------------------------------------ set-up ---
     if (tid < nn) sm.parent[tid] = parent;
     for (int u = NT + tid; u < nn; u += NT) sm.parent[u] = __ldg(g.parent + (int64_t)b * g.c.n + u);
-    if (tid < kTreeRows * 4) sm.q[tid >> 2][tid & 3] = q_in;
-    if (tid < kTreeRows) sm.again[tid] = false;
-    for (int e = tid; e < kTreeRows * (kMaxDraft / 32); e += NT) (&sm.above[0][0])[e] = 0u;
+    if (tid < ROWS * 4) sm.q[tid >> 2][tid & 3] = q_in;
+    if (tid < ROWS) sm.again[tid] = false;
+    for (int e = tid; e < ROWS * (kMaxDraft / 32); e += NT) (&sm.above[0][0])[e] = 0u;
     __syncthreads();
     const int fsh = max(5, 24 - __clz(cC | 1));              // one fence in 2^fsh entries: up to 256
     const int nf = (cC + (1 << fsh) - 1) >> fsh, fe = tid << fsh;
@@ -250,12 +237,11 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     }
     if (warp == 0) {                                         // the lines
         for (int w = 0; w * 32 < nn; ++w) {
-            const int u = w * 32 + lane;
-            const uint32_t bits = __ballot_sync(kFull, u < nn && u > 0 && sm.parent[u] == u - 1);
+            const uint32_t bits = run_bits(sm.parent, w, nn);
             if (lane == 0) sm.run[w] = bits;
         }
         __syncwarp();
-        if (lane < kTreeRows) {
+        if (lane < ROWS) {
             int depth = -1;
             if (lane < nq) {
                 depth = climb_bits(sm.parent, sm.run, f0 + lane, sm.above[lane]);
@@ -580,7 +566,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     // (float32: 2) keys: node lane / 4 and keys 2 s4, + 1, + 8, + 9; or node lane % 8 and keys
     // 2 (lane / 8), + 1.
     {
-        constexpr int NG = kTreeGroups, ACC = DVP / 4;
+        constexpr int NG = Sm::NG, ACC = DVP / 4;
         const bool two = nq > 8;                             // nodes in both groups
         const int node = Sm::MMA ? g4 : lane & 7;
         float acc[NG][ACC];                                  // MMA: [half][w][4]; else [4 nodes][DVP / 64][4]
@@ -672,7 +658,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
                     operands(v + 2 * hh, [&](int c, const uint32_t (&x)[4]) {
 #pragma unroll
                         for (int n = 0; n < NG; ++n) {
-                            if (n == 1 && !two) break;
+                            if (n > 0 && !two) break;
                             float(&o)[4] = *reinterpret_cast<float(*)[4]>(&acc[n][16 * hh + 4 * c]);
                             mma16816(o, x, b[n][0], b[n][1]);
                             mma16816(o, x, b[n][2], b[n][3]);
@@ -691,7 +677,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
                     if (e == 4) more(4);                     // the values of the other four keys
 #pragma unroll
                     for (int n = 0; n < NG; ++n) {
-                        if (n == 1 && !two) break;
+                        if (n > 0 && !two) break;
                         const float4 w4 = *reinterpret_cast<const float4 *>(&ws[e][8 * n + (lane >> 4) * 4]);
                         const float wr[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
@@ -714,43 +700,58 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
                 __syncwarp();                                // the weights have been read
             }
         };
-        // Whole steps within a page.
-        for (int i = cw; i < n_main; i += CW) {
-            const int first = cC + i * KS, id = pt[first >> psh];
-            if ((unsigned)id >= (unsigned)g.c.pages) {
-                set_status(g.status, ZETA_ERR_BOUNDS);
-                continue;
+        // Whole steps within a page, some at a time.
+        struct Step {
+            float2 kc[Sm::KP][DK];
+            uint32_t v[Sm::NV / 2][8];
+            const char *src;
+            bool page;
+        };
+        auto values = [&](Step &t, int e0) {
+            if constexpr (Sm::MMA) {
+#pragma unroll
+                for (int e = 0; e < 2 * H; ++e) {
+                    const char *p = t.src + (8 * (e & 1) + g4) * vrow;
+                    ld32<WIDE>(t.v[e], p + spot(e / 2, 0), p + spot(e / 2, 1));
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < NV; ++e)
+                    *reinterpret_cast<uint4 *>(&t.v[e / 2][e % 2 * 4]) =
+                        ld16(t.src + (e0 + e / (NV / 4)) * vrow + piece + e % (NV / 4) * second);
+            }
+        };
+        auto fetch = [&](Step &t, int i) {
+            const int first = cC + i * KS, id = i < n_main ? pt[first >> psh] : -1;
+            t.page = (unsigned)id < (unsigned)g.c.pages;
+            if (!t.page) {
+                if (i < n_main) set_status(g.status, ZETA_ERR_BOUNDS);
+                return;
             }
             const uint32_t r0 = (uint32_t)row_at(id, first);
             const float2 *kp = reinterpret_cast<const float2 *>(kt + (uint64_t)r0 * 12u + 12 * first_key);
-            float2 kc[KP][DK];
 #pragma unroll
             for (int e = 0; e < KP; ++e)
 #pragma unroll
-                for (int d = 0; d < DK; ++d) kc[e][d] = __ldg(kp + 12 * e + d);
-            const char *src = vt + (uint64_t)r0 * (uint32_t)vrow;
-            uint32_t v[NV / 2][8];
-            auto values = [&](int e0) {
-                if constexpr (Sm::MMA) {
+                for (int d = 0; d < DK; ++d) t.kc[e][d] = __ldg(kp + 12 * e + d);
+            t.src = vt + (uint64_t)r0 * (uint32_t)vrow;
+            values(t, 0);
+        };
+        for (int i = cw; i < n_main; i += ZETA_TREE_DEPTH * CW) {
+            Step t[ZETA_TREE_DEPTH];
 #pragma unroll
-                    for (int e = 0; e < 2 * H; ++e) {
-                        const char *p = src + (8 * (e & 1) + g4) * vrow;
-                        ld32<WIDE>(v[e], p + spot(e / 2, 0), p + spot(e / 2, 1));
-                    }
-                } else {
+            for (int o = 0; o < ZETA_TREE_DEPTH; ++o) fetch(t[o], i + o * CW);
 #pragma unroll
-                    for (int e = 0; e < NV; ++e)
-                        *reinterpret_cast<uint4 *>(&v[e / 2][e % 2 * 4]) =
-                            ld16(src + (e0 + e / (NV / 4)) * vrow + piece + e % (NV / 4) * second);
-                }
-            };
-            values(0);
-            float2 w[NG][KP];
+            for (int o = 0; o < ZETA_TREE_DEPTH; ++o) {
+                if (!t[o].page) continue;
+                float2 w[NG][KP];
 #pragma unroll
-            for (int n = 0; n < NG; ++n)
-                if (n == 0 || two) weigh(n, kc, w[n], 0u, false);
-                else w[n][0] = w[n][KP - 1] = make_float2(0.f, 0.f);
-            multiply(w, v, values);
+                for (int n = 0; n < NG; ++n)
+                    if (n == 0 || two) weigh(n, t[o].kc, w[n], 0u, false);
+                    else w[n][0] = w[n][KP - 1] = make_float2(0.f, 0.f);
+                auto more = [&](int e0) { values(t[o], e0); };
+                multiply(w, t[o].v, more);
+            }
         }
         // The lines and fences are there for the rest; the first window's search begins.
         sm.fence[tid] = fz;
@@ -824,7 +825,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
             for (int n = 0; n < NG; ++n) weigh(n, kc, w[n], takes[n], true);
             multiply(w, v, values);
         }
-        float(&part)[kTreeRows][DVP + 4] = sm.part[warp];
+        float(&part)[ROWS][DVP + 4] = sm.part[warp];
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
             float total = sum[n].x + sum[n].y;
@@ -834,7 +835,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
                 sm.psum[warp][8 * n + node] = total;
                 sm.pmin[warp][8 * n + node] = m[n];
             }
-            if (n == 1 && !two) break;
+            if (n > 0 && !two) break;
             if constexpr (Sm::MMA) {
 #pragma unroll
                 for (int c = 0; c < 4 * H; ++c) {
@@ -884,7 +885,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
         if (tid < nq)
             join(NW, tid, false, [&](int p) { return sm.psum[p][tid]; }, [&](int p) { return sm.pmin[p][tid]; });
         __syncthreads();
-        for (int i = tid; i < kTreeRows * (DVP / 2); i += NT) {
+        for (int i = tid; i < ROWS * (DVP / 2); i += NT) {
             const int r = i / (DVP / 2), col = i % (DVP / 2) * 2;
             if (r >= nq) break;
             float2 o = make_float2(0.f, 0.f);
@@ -900,7 +901,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     }
     const int parts = cs > 1 ? cs : NW;
     auto of = [&](int p) { return cs > 1 ? cl.map_shared_rank(&sm, p) : &sm; };
-    const bool finish = tid < nq && tid % cs == cr && sm.depth[min(tid, kTreeRows - 1)] >= 0;
+    const bool finish = tid < nq && tid % cs == cr && sm.depth[min(tid, ROWS - 1)] >= 0;
     if (finish) {
         join(parts, tid, true, [&](int p) { return of(p)->psum[cs > 1 ? 0 : p][tid]; }, [&](int p) { return of(p)->pmin[cs > 1 ? 0 : p][tid]; });
         g.rowsum[node0 + f0 + tid] = sm.total[tid];
@@ -909,7 +910,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     // Two columns a thread.
     bool bad = false;
     V *out = static_cast<V *>(g.out) + (node0 + f0) * g.dV;
-    for (int i = tid; i < kTreeRows * (DVP / 2); i += NT) {
+    for (int i = tid; i < ROWS * (DVP / 2); i += NT) {
         const int r = i / (DVP / 2) * cs + cr, col = i % (DVP / 2) * 2;
         if (r >= nq) break;
         if (sm.depth[r] < 0 || col >= g.dV) continue;
@@ -939,13 +940,14 @@ template <typename V, int DVP, int DK, int WK, bool WIDE>
 cudaError_t run_tree_tile(const Prob &p, const TreeArgs &g, int cs, cudaStream_t st) {
     static PerDeviceOnce once;
     constexpr size_t smem = sizeof(TreeSmem<V, DVP>);
+    constexpr int Rows = TreeSmem<V, DVP>::ROWS;
     cudaError_t e = once.run([] {
         return cudaFuncSetAttribute(tree_tile_kernel<V, DVP, DK, WK, WIDE>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((g.c.n + kTreeRows - 1) / kTreeRows * cs), (unsigned)p.S);
+    cfg.gridDim = dim3((unsigned)((g.c.n + Rows - 1) / Rows * cs), (unsigned)p.S);
     cfg.blockDim = dim3(kTreeThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
