@@ -7,10 +7,14 @@
 // Behind the chunk's end there is no result: the prefix there would hold the line's own
 // keys, another one for each branch.
 //
-// Row kernel, for every type and size: a block of 128 threads per node and head.  The
-// node's line is found by one thread in the parents in shared memory, its rank by 128
-// probes a step.  The keys (window, chunk, line) are one list, weighed a thread each
-// 1024 at a time; then a thread per value column (and share of the keys) sums.
+// Row kernel, for the types and sizes that the tile kernel (cache_tree_tile.cuh) does not
+// take: a block of 128 threads per node and head.  The node's line is found by one thread in
+// the parents in shared memory, its rank by 128 probes a step.  The keys (window, chunk,
+// line) are one list, weighed a thread each 1024 at a time; then a thread per value column
+// (and share of the keys) sums.  The chunk is read once per node, by which it is bound: 64
+// sequences of 32 nodes, 8 heads, C 1024 took 1.25 ms, the tile kernel 57 us.
+#include <algorithm>
+
 #include "cache_tree_tile.cuh"
 
 namespace zeta {
@@ -177,15 +181,36 @@ tree_rows_kernel(const __grid_constant__ TreeArgs g) {
     if (tid == 0) g.rowsum[rid] = s;
 }
 
+// How the tile kernel's blocks are laid out, measured in us with 8 heads, d_V 64, windows of
+// 64, 8 K tokens a sequence:
+//  * Groups of 8 nodes to a block, and 4 warps to a group: one where a tree has no more, or
+//    values are wider than 64 (whose sums fill the registers).  Trees of 4 nodes, 64 sequences:
+//    one group (four blocks an SM) 25, two (two an SM) 30; of 12 nodes 41 : 39, of 32 62 : 58.  In
+//    calls that do not fill the SMs two groups' warps help: 4 sequences of 8 nodes, C 256, 9.7 : 9.1.
+//  * Blocks to the same nodes (a cluster), as many as run at once, where a warp has several
+//    windows or many of the chunk's keys: 4 sequences of 16 nodes, 1 / 2 / 4 / 8 blocks: 16 / 12 /
+//    10.5 / 9.9; C 4096 31 / 20 / 15 / 13; of 8 nodes, C 256, where neither holds, 9.0 / 9.7 / 9.8 /
+//    9.9.  More than run at once: 16 sequences of 16 nodes 19 / 15 / 24 / 43.
+struct Layout {
+    int ng, cs;
+};
+Layout tile_layout(const Prob &p, int n) {
+    Layout l{p.dV <= 64 && (n > 8 || p.S <= 64) ? 2 : 1, 1};
+    const int rows = 8 * l.ng, warps = 4 * l.ng;
+    const int64_t groups = p.S * ((n + rows - 1) / rows);
+    while (l.cs < 8 && groups * l.cs * 2 <= 152 * (4 / l.ng) &&
+           (std::min(n, rows) > warps * l.cs || p.C > 256 * l.cs))
+        l.cs *= 2;
+    return l;
+}
+
 }  // namespace
 
 cudaError_t launch_cache_attend_tree(const Prob &p, const TreeArgs &g, cudaStream_t st) {
     const int piece = p.vdt == ZETA_BF16 ? 8 : 4;    // values of 16 bytes
     if (p.dK <= 4 && p.dV <= 128 && p.dV % piece == 0) {
-        const int64_t groups = p.S * ((g.c.n + kTreeRows - 1) / kTreeRows);
-        int cs = 1;
-        while (cs < 8 && groups * cs * 2 <= 152 * 3) cs *= 2;
-        return p.vdt == ZETA_BF16 ? launch_tree_tile_bf16(p, g, cs, st) : launch_tree_tile_f32(p, g, cs, st);
+        const Layout l = tile_layout(p, g.c.n);
+        return p.vdt == ZETA_BF16 ? launch_tree_tile_bf16(p, g, l.ng, l.cs, st) : launch_tree_tile_f32(p, g, l.ng, l.cs, st);
     }
     const dim3 grid((unsigned)g.c.n, (unsigned)p.H, (unsigned)p.B);
     if (p.vdt == ZETA_BF16) {

@@ -1,11 +1,12 @@
 // cache_tree_tile.cuh -- attention of trees of drafted tokens: bf16 values with d_V a
 // multiple of 8, float32 with a multiple of 4, up to 128 wide, d_K <= 4.
 //
-// Same definition as the row kernel (cache_tree.cu).  A block of eight warps takes 16 nodes of
-// one sequence and head, or a cluster of up to 8 blocks does where there are few: every block
-// of it has some of the nodes' windows and some of the keys that all 16 share, and the sums
-// are joined through distributed shared memory.  A warp takes its windows one by one, then
-// its part of the shared keys; none waits for another between set-up and join.
+// Same definition as the row kernel (cache_tree.cu).  A block takes 8 or 16 nodes of one
+// sequence and head, or a cluster of up to 8 blocks does where there are few: every block of
+// it has some of the nodes' windows and some of the keys that all of them share, and the sums
+// are joined through distributed shared memory.  A warp takes its part of the shared keys,
+// then its windows one by one; between set-up and join none waits for another but once, for
+// the lines.
 //  * Lines: a bit per node above, found by climbing in shared memory.  A run of nodes
 //    that hang below one another by number (a chain) is one step of the climb.
 //  * Window: the first code of every block of 2^fsh prefix entries lies in shared memory; a
@@ -30,41 +31,26 @@
 
 namespace zeta {
 
-// cs: blocks to 16 nodes (1, 2, 4 or 8).
-cudaError_t launch_tree_tile_bf16(const Prob &p, const TreeArgs &g, int cs, cudaStream_t st);
-cudaError_t launch_tree_tile_f32(const Prob &p, const TreeArgs &g, int cs, cudaStream_t st);
+// ng: groups of 8 nodes to a block (1, or 2 up to 64 wide); cs: blocks to them (1, 2, 4 or 8).
+cudaError_t launch_tree_tile_bf16(const Prob &p, const TreeArgs &g, int ng, int cs, cudaStream_t st);
+cudaError_t launch_tree_tile_f32(const Prob &p, const TreeArgs &g, int ng, int cs, cudaStream_t st);
 
 namespace {
 
-#ifndef ZETA_TREE_NG
-#define ZETA_TREE_NG 2
-#endif
-#ifndef ZETA_TREE_NG2
-#define ZETA_TREE_NG2 1
-#endif
-#ifndef ZETA_TREE_DEPTH
-#define ZETA_TREE_DEPTH 1
-#endif
-#ifndef ZETA_TREE_NB
-#define ZETA_TREE_NB 3
-#endif
-#ifndef ZETA_TREE_BLOCKS
-#define ZETA_TREE_BLOCKS 2
-#endif
 namespace cg = cooperative_groups;
 
-constexpr int kTreeWarps = 8, kTreeThreads = 32 * kTreeWarps;
-constexpr int kTreeRows = 16;                        // nodes of a block, at most
 constexpr int kTreeFences = 256;
 constexpr int kTreeTable = 1024;                     // pages whose numbers lie in shared memory
 
-template <typename V, int DVP>
+template <typename V, int DVP, int NG>
 struct TreeSmem {
     static constexpr bool MMA = sizeof(V) == 2;
-    static constexpr int NG = DVP == 64 ? ZETA_TREE_NG : ZETA_TREE_NG2, ROWS = 8 * NG;   // nodes of a block, in groups of 8
+    // NG groups of 8 nodes a block; warps, blocks an SM (128 registers a thread), a window's steps
+    // under way.
+    static constexpr int ROWS = 8 * NG, NW = 4 * NG, PER_SM = 4 / NG, NB = NG + 1;
     static constexpr int KS = MMA ? 16 : 8, KL = KS / 4, KP = KL / 2;    // shared keys a step, a lane; pairs
     static constexpr int NV = DVP / 16;              // 16-byte pieces of them a lane holds (float32: of four keys)
-    float part[kTreeWarps][ROWS][DVP + 4];      // sums over shared keys, warp by warp
+    float part[NW][ROWS][DVP + 4];      // sums over shared keys, warp by warp
     struct {                                         // of a warp's window
         int row[64];
         union {
@@ -73,10 +59,10 @@ struct TreeSmem {
             uint16_t half[2][64];                    // bf16: weights' halves and rests
         };
         float x[64 * 4];                             // coordinates
-    } gather[kTreeWarps];
+    } gather[NW];
     uint64_t fence[kTreeFences];
     int ptab[kTreeTable];
-    float w[MMA ? 1 : kTreeWarps][8][20];            // float32, shared keys: weights [key][node]
+    float w[MMA ? 1 : NW][8][20];            // float32, shared keys: weights [key][node]
     union {
         int parent[kMaxDraft];
         float win[ROWS][DVP + 4];               // window sums
@@ -86,8 +72,8 @@ struct TreeSmem {
     float q[ROWS][4];
     int depth[ROWS], wst[ROWS];
     float swin[ROWS], mwin[ROWS];
-    float psum[kTreeWarps][ROWS], pmin[kTreeWarps][ROWS];
-    float factor[kTreeWarps + 1][ROWS], least[ROWS];   // softmax: of the parts and the window; the shift
+    float psum[NW][ROWS], pmin[NW][ROWS];
+    float factor[NW + 1][ROWS], least[ROWS];   // softmax: of the parts and the window; the shift
     float total[ROWS];
     bool again[ROWS];                           // not finite
 };
@@ -180,11 +166,11 @@ __device__ __forceinline__ uint64_t ld_code(const char *codes, uint32_t row, int
     return (uint64_t)ld4_if(p + 4, code64) << 32 | __ldg(reinterpret_cast<const uint32_t *>(p));
 }
 
-template <typename V, int DVP, int DK, int WK, bool WIDE>
-__global__ void __launch_bounds__(kTreeThreads, ZETA_TREE_BLOCKS)
+template <typename V, int DVP, int NG, int DK, int WK, bool WIDE>
+__global__ void __launch_bounds__(TreeSmem<V, DVP, NG>::NW * 32, TreeSmem<V, DVP, NG>::PER_SM)
 tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
-    using Sm = TreeSmem<V, DVP>;
-    constexpr int NT = kTreeThreads, NW = kTreeWarps, ROWS = Sm::ROWS;
+    using Sm = TreeSmem<V, DVP, NG>;
+    constexpr int NW = Sm::NW, NT = 32 * NW, ROWS = Sm::ROWS;
     constexpr int PPR = DVP * (int)sizeof(V) / 16;           // 16-byte pieces of a padded row
     extern __shared__ __align__(16) unsigned char raw[];
     Sm &sm = *reinterpret_cast<Sm *>(raw);
@@ -228,12 +214,18 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     for (int e = tid; e < ROWS * (kMaxDraft / 32); e += NT) (&sm.above[0][0])[e] = 0u;
     __syncthreads();
     const int fsh = max(5, 24 - __clz(cC | 1));              // one fence in 2^fsh entries: up to 256
-    const int nf = (cC + (1 << fsh) - 1) >> fsh, fe = tid << fsh;
-    uint64_t fz = ~0ull;
-    if (tid < nf) {
-        const int id = ot[fe >> psh];
-        if ((unsigned)id < (unsigned)g.c.opages) fz = ld_code(codes, row_at(id, fe), g.code64);
-        else set_status(g.status, ZETA_ERR_BOUNDS);
+    const int nf = (cC + (1 << fsh) - 1) >> fsh;
+    constexpr int NF = kTreeFences / NT;                     // a thread's
+    uint64_t fz[NF];
+#pragma unroll
+    for (int u = 0; u < NF; ++u) {
+        const int f = u * NT + tid;
+        fz[u] = ~0ull;
+        if (f < nf) {
+            const int e = f << fsh, id = ot[e >> psh];
+            if ((unsigned)id < (unsigned)g.c.opages) fz[u] = ld_code(codes, row_at(id, e), g.code64);
+            else set_status(g.status, ZETA_ERR_BOUNDS);
+        }
     }
     if (warp == 0) {                                         // the lines
         for (int w = 0; w * 32 < nn; ++w) {
@@ -281,7 +273,12 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     const int first_key = Sm::MMA ? 2 * s4 : 2 * (lane >> 3);                // the lane's first key of a step
     const int piece = min(lane & 15, ppr - 1) * 16;          // float32: its bytes of a value row
     const int second = NV == 4 ? 0 : min((lane & 15) + 16, ppr - 1) * 16 - piece;
-    // The whole steps' values are asked into L2 ahead.
+    // The whole steps' values, and the nodes' rows, are asked into L2 ahead.
+    if (cw < nn / KS + 1 && lane < KS) {
+        const int64_t r = min(cw * KS + lane, nn - 1);
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(vf + r * vrow));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(kf + r * krow));
+    }
     for (int i = cw; i < n_main; i += CW) {
         const int first = cC + i * KS, id = pt[first >> psh];
         if ((unsigned)id < (unsigned)g.c.pages && lane * 128 < KS * vrow)
@@ -429,7 +426,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
                             ld16(vt + (uint64_t)(uint32_t)rows[v * RPI + lane / LPR] * (uint32_t)vrow + min(lane % LPR, ppr - 1) * 16);
                 }
             };
-            constexpr int NB = ZETA_TREE_NB;                 // steps in flight
+            constexpr int NB = Sm::NB;                       // steps under way
             uint32_t buf[NB][2][8];
 #pragma unroll
             for (int o = 0; o < NB; ++o) load(buf[o], o, 0);
@@ -566,7 +563,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     // (float32: 2) keys: node lane / 4 and keys 2 s4, + 1, + 8, + 9; or node lane % 8 and keys
     // 2 (lane / 8), + 1.
     {
-        constexpr int NG = Sm::NG, ACC = DVP / 4;
+        constexpr int ACC = DVP / 4;
         const bool two = nq > 8;                             // nodes in both groups
         const int node = Sm::MMA ? g4 : lane & 7;
         float acc[NG][ACC];                                  // MMA: [half][w][4]; else [4 nodes][DVP / 64][4]
@@ -700,61 +697,47 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
                 __syncwarp();                                // the weights have been read
             }
         };
-        // Whole steps within a page, some at a time.
-        struct Step {
-            float2 kc[Sm::KP][DK];
-            uint32_t v[Sm::NV / 2][8];
-            const char *src;
-            bool page;
-        };
-        auto values = [&](Step &t, int e0) {
-            if constexpr (Sm::MMA) {
-#pragma unroll
-                for (int e = 0; e < 2 * H; ++e) {
-                    const char *p = t.src + (8 * (e & 1) + g4) * vrow;
-                    ld32<WIDE>(t.v[e], p + spot(e / 2, 0), p + spot(e / 2, 1));
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < NV; ++e)
-                    *reinterpret_cast<uint4 *>(&t.v[e / 2][e % 2 * 4]) =
-                        ld16(t.src + (e0 + e / (NV / 4)) * vrow + piece + e % (NV / 4) * second);
-            }
-        };
-        auto fetch = [&](Step &t, int i) {
-            const int first = cC + i * KS, id = i < n_main ? pt[first >> psh] : -1;
-            t.page = (unsigned)id < (unsigned)g.c.pages;
-            if (!t.page) {
-                if (i < n_main) set_status(g.status, ZETA_ERR_BOUNDS);
-                return;
+        // Whole steps within a page.
+        for (int i = cw; i < n_main; i += CW) {
+            const int first = cC + i * KS, id = pt[first >> psh];
+            if ((unsigned)id >= (unsigned)g.c.pages) {
+                set_status(g.status, ZETA_ERR_BOUNDS);
+                continue;
             }
             const uint32_t r0 = (uint32_t)row_at(id, first);
             const float2 *kp = reinterpret_cast<const float2 *>(kt + (uint64_t)r0 * 12u + 12 * first_key);
+            float2 kc[KP][DK];
 #pragma unroll
             for (int e = 0; e < KP; ++e)
 #pragma unroll
-                for (int d = 0; d < DK; ++d) t.kc[e][d] = __ldg(kp + 12 * e + d);
-            t.src = vt + (uint64_t)r0 * (uint32_t)vrow;
-            values(t, 0);
-        };
-        for (int i = cw; i < n_main; i += ZETA_TREE_DEPTH * CW) {
-            Step t[ZETA_TREE_DEPTH];
+                for (int d = 0; d < DK; ++d) kc[e][d] = __ldg(kp + 12 * e + d);
+            const char *src = vt + (uint64_t)r0 * (uint32_t)vrow;
+            uint32_t v[NV / 2][8];
+            auto values = [&](int e0) {
+                if constexpr (Sm::MMA) {
 #pragma unroll
-            for (int o = 0; o < ZETA_TREE_DEPTH; ++o) fetch(t[o], i + o * CW);
+                    for (int e = 0; e < 2 * H; ++e) {
+                        const char *p = src + (8 * (e & 1) + g4) * vrow;
+                        ld32<WIDE>(v[e], p + spot(e / 2, 0), p + spot(e / 2, 1));
+                    }
+                } else {
 #pragma unroll
-            for (int o = 0; o < ZETA_TREE_DEPTH; ++o) {
-                if (!t[o].page) continue;
-                float2 w[NG][KP];
+                    for (int e = 0; e < NV; ++e)
+                        *reinterpret_cast<uint4 *>(&v[e / 2][e % 2 * 4]) =
+                            ld16(src + (e0 + e / (NV / 4)) * vrow + piece + e % (NV / 4) * second);
+                }
+            };
+            values(0);
+            float2 w[NG][KP];
 #pragma unroll
-                for (int n = 0; n < NG; ++n)
-                    if (n == 0 || two) weigh(n, t[o].kc, w[n], 0u, false);
-                    else w[n][0] = w[n][KP - 1] = make_float2(0.f, 0.f);
-                auto more = [&](int e0) { values(t[o], e0); };
-                multiply(w, t[o].v, more);
-            }
+            for (int n = 0; n < NG; ++n)
+                if (n == 0 || two) weigh(n, kc, w[n], 0u, false);
+                else w[n][0] = w[n][KP - 1] = make_float2(0.f, 0.f);
+            multiply(w, v, values);
         }
         // The lines and fences are there for the rest; the first window's search begins.
-        sm.fence[tid] = fz;
+#pragma unroll
+        for (int u = 0; u < NF; ++u) sm.fence[u * NT + tid] = fz[u];
         __syncthreads();
         mine = next(cw);
         if (mine < nq) search(mine);
@@ -936,19 +919,19 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     if (cs > 1) cl.sync();                                   // read before any block ends
 }
 
-template <typename V, int DVP, int DK, int WK, bool WIDE>
+template <typename V, int DVP, int NG, int DK, int WK, bool WIDE>
 cudaError_t run_tree_tile(const Prob &p, const TreeArgs &g, int cs, cudaStream_t st) {
     static PerDeviceOnce once;
-    constexpr size_t smem = sizeof(TreeSmem<V, DVP>);
-    constexpr int Rows = TreeSmem<V, DVP>::ROWS;
+    constexpr size_t smem = sizeof(TreeSmem<V, DVP, NG>);
+    constexpr int Rows = TreeSmem<V, DVP, NG>::ROWS;
     cudaError_t e = once.run([] {
-        return cudaFuncSetAttribute(tree_tile_kernel<V, DVP, DK, WK, WIDE>,
+        return cudaFuncSetAttribute(tree_tile_kernel<V, DVP, NG, DK, WK, WIDE>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((g.c.n + Rows - 1) / Rows * cs), (unsigned)p.S);
-    cfg.blockDim = dim3(kTreeThreads);
+    cfg.blockDim = dim3(TreeSmem<V, DVP, NG>::NW * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at{};
@@ -957,16 +940,16 @@ cudaError_t run_tree_tile(const Prob &p, const TreeArgs &g, int cs, cudaStream_t
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = cs > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, tree_tile_kernel<V, DVP, DK, WK, WIDE>, g, cs);
+    e = cudaLaunchKernelEx(&cfg, tree_tile_kernel<V, DVP, NG, DK, WK, WIDE>, g, cs);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <typename V, int DVP, bool WIDE>
+template <typename V, int DVP, int NG, bool WIDE>
 cudaError_t dispatch_tree_tile(const Prob &p, const TreeArgs &g, int cs, cudaStream_t st) {
 #define ZETA_TREE(D)                                                                  \
-    (p.wk == kWSoftmax     ? run_tree_tile<V, DVP, D, kWSoftmax, WIDE>(p, g, cs, st)        \
-     : p.wk == kWInvEuclid ? run_tree_tile<V, DVP, D, kWInvEuclid, WIDE>(p, g, cs, st)      \
-                           : run_tree_tile<V, DVP, D, kWCauchy, WIDE>(p, g, cs, st))
+    (p.wk == kWSoftmax     ? run_tree_tile<V, DVP, NG, D, kWSoftmax, WIDE>(p, g, cs, st)        \
+     : p.wk == kWInvEuclid ? run_tree_tile<V, DVP, NG, D, kWInvEuclid, WIDE>(p, g, cs, st)      \
+                           : run_tree_tile<V, DVP, NG, D, kWCauchy, WIDE>(p, g, cs, st))
     return p.dK == 3 ? ZETA_TREE(3) : ZETA_TREE(4);
 #undef ZETA_TREE
 }
