@@ -227,7 +227,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
             else set_status(g.status, ZETA_ERR_BOUNDS);
         }
     }
-    if (warp == 0) {                                         // the lines
+    if (warp == NW - 1) {                                    // the lines, by the warp with the fewest steps
         for (int w = 0; w * 32 < nn; ++w) {
             const uint32_t bits = run_bits(sm.parent, w, nn);
             if (lane == 0) sm.run[w] = bits;
@@ -274,7 +274,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     const int piece = min(lane & 15, ppr - 1) * 16;          // float32: its bytes of a value row
     const int second = NV == 4 ? 0 : min((lane & 15) + 16, ppr - 1) * 16 - piece;
     // The whole steps' values, and the nodes' rows, are asked into L2 ahead.
-    if (cw < nn / KS + 1 && lane < KS) {
+    if (cw <= nn / KS && lane < KS) {
         const int64_t r = min(cw * KS + lane, nn - 1);
         asm volatile("prefetch.global.L2 [%0];" ::"l"(vf + r * vrow));
         asm volatile("prefetch.global.L2 [%0];" ::"l"(kf + r * krow));
@@ -741,8 +741,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
         __syncthreads();
         mine = next(cw);
         if (mine < nq) search(mine);
-        // The others, key by key.
-        for (int i = cw; i < n_rest; i += CW) {
+        // The others, key by key; the deal goes on where the whole steps' ended.
+        for (int i = (cw + CW - n_main % CW) % CW; i < n_rest; i += CW) {
             const bool fresh = i >= n_rest - n_node;
             const int x0 = (fresh ? i - (n_rest - n_node) : n_main + i) * KS, end = fresh ? nn : L;
             const char *kb = fresh ? kf : kt, *vb = fresh ? vf : vt;
