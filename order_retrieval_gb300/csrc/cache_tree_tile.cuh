@@ -60,7 +60,7 @@ struct TreeSmem {
         };
         float x[64 * 4];                             // coordinates
     } gather[NW];
-    uint64_t fence[kTreeFences];
+    uint64_t fence[kTreeFences], z[ROWS];            // codes of the fences, of the nodes
     int ptab[kTreeTable];
     float w[MMA ? 1 : NW][8][20];            // float32, shared keys: weights [key][node]
     union {
@@ -206,6 +206,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     const bool near = ((seq.start + pmask) >> psh) <= pages_near;
     const int32_t *pt = near ? sm.ptab : ptab, *ot = near && otab == ptab ? sm.ptab : otab;
 
+    bool lost = false;                                       // this thread met what is out of range
+
     // ------------------------------------------------------------ set-up ---
     if (tid < nn) sm.parent[tid] = parent;
     for (int u = NT + tid; u < nn; u += NT) sm.parent[u] = __ldg(g.parent + (int64_t)b * g.c.n + u);
@@ -224,10 +226,10 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
         if (f < nf) {
             const int e = f << fsh, id = ot[e >> psh];
             if ((unsigned)id < (unsigned)g.c.opages) fz[u] = ld_code(codes, row_at(id, e), g.code64);
-            else set_status(g.status, ZETA_ERR_BOUNDS);
+            else lost = true;
         }
     }
-    if (warp == NW - 1) {                                    // the lines, by the warp with the fewest steps
+    if (warp == NW - 1) {                                    // the lines and codes, by the warp with the fewest steps
         for (int w = 0; w * 32 < nn; ++w) {
             const uint32_t bits = run_bits(sm.parent, w, nn);
             if (lane == 0) sm.run[w] = bits;
@@ -237,10 +239,14 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
             int depth = -1;
             if (lane < nq) {
                 depth = climb_bits(sm.parent, sm.run, f0 + lane, sm.above[lane]);
-                if (depth < 0) set_status(g.status, ZETA_ERR_BOUNDS);
+                lost |= depth < 0;
                 if (seq.start + depth >= cC + g.C) depth = -1;   // behind the chunk's end
             }
             sm.depth[lane] = depth;                          // -1: no result
+            float p[kMaxDK];
+#pragma unroll
+            for (int d = 0; d < kMaxDK; ++d) p[d] = d < DK ? sm.q[lane][d < DK ? d : 0] : 0.f;
+            sm.z[lane] = code_of(p, DK == 3 ? 3 : g.dK, g.bits);
         }
         __syncwarp();
     }
@@ -301,7 +307,6 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     int ra = 0, re = 0, cand[4], lo = 0;                     // entries before ra are <= z, from re on > z
     bool open[2] = {false, false};
     auto probe = [&](int step) {
-        bool lost = false;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
             const int at = ra + (v * 32 + lane + 1) * step - 1, to = min(at, cC - 1);
@@ -311,7 +316,6 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
             lost |= at < re && !in;
             zz[v] = ld_code(codes, in ? row_at(id, to) : 0, g.code64);
         }
-        if (lost) set_status(g.status, ZETA_ERR_BOUNDS);
     };
     auto found = [&](int step) {
         __syncwarp();
@@ -321,10 +325,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     };
     auto search = [&](int r) {
         if (chunk == 0) return;
-        float p[kMaxDK];
-#pragma unroll
-        for (int d = 0; d < kMaxDK; ++d) p[d] = d < DK ? sm.q[r][d < DK ? d : 0] : 0.f;
-        z = code_of(p, DK == 3 ? 3 : g.dK, g.bits);
+        z = sm.z[r];
         const int f8 = 8 * __popc(__ballot_sync(kFull, lane * 8 + 7 < nf && sm.fence[lane * 8 + 7] <= z));
         const int f = f8 + (lane & 7);
         const int n = f8 + __popc(__ballot_sync(kFull, lane < 8 && f < nf && sm.fence[min(f, kTreeFences - 1)] <= z));
@@ -367,7 +368,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
         int following = nq;
         for (int t0 = 0; t0 < g.kw; t0 += 64) {              // up to 64 entries at a time, two a lane
             int row[2];
-            bool is[2], lost = false;
+            bool is[2];
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 const int slot = t0 + v * 32 + lane;
@@ -386,7 +387,6 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
                 row[v] = row_at(id, j);
                 lost |= there && !is[v];
             }
-            if (lost) set_status(g.status, ZETA_ERR_BOUNDS);
             __syncwarp();                                    // the entries have been read
             // In the place of an entry that is none, another of the window: its values enter the
             // sum anyway, so that a zero weight adds no NaN of its own.
@@ -399,16 +399,16 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
             ga.row[lane] = row[0];
             ga.row[32 + lane] = row[1];
             __syncwarp();                                    // the rows are there
-            // Coordinates one by one, so that a load touches a row's line once.
+            // Coordinates one a lane, CR rows a load, so that a load touches a row's line once.
+            constexpr int CR = 32 / DK, CL = (64 + CR - 1) / CR;
             const int steps = (min(64, g.kw - t0) + WS - 1) / WS;
-            float x[2 * DK];
+            const int c_row = lane / DK, c_at = lane % DK, entries_here = min(64, g.kw - t0);
+            float x[CL];
 #pragma unroll
-            for (int v = 0; v < 2 * DK; ++v) {
-                const int at = v * 32 + lane;
-                if (DK == 3 || at % DK < g.dK)
-                    x[v] = __ldg(reinterpret_cast<const float *>(kt + (uint64_t)(uint32_t)ga.row[at / DK] * (uint32_t)krow) + at % DK);
-                else
-                    x[v] = 0.f;
+            for (int v = 0; v < CL; ++v) {
+                x[v] = 0.f;
+                if (v * CR < entries_here && c_row < CR && v * CR + c_row < 64 && (DK == 3 || c_at < g.dK))
+                    x[v] = __ldg(reinterpret_cast<const float *>(kt + (uint64_t)(uint32_t)ga.row[v * CR + c_row] * (uint32_t)krow) + c_at);
             }
             auto load = [&](uint32_t (&y)[2][8], int i, int hh) {
                 if (i >= steps) return;
@@ -435,7 +435,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
                 if (following < nq) search(following);
             }
 #pragma unroll
-            for (int v = 0; v < 2 * DK; ++v) ga.x[v * 32 + lane] = x[v];
+            for (int v = 0; v < CL; ++v)
+                if (v * CR < entries_here && c_row < CR && v * CR + c_row < 64) ga.x[v * CR * DK + lane] = x[v];
             __syncwarp();
             float d2[2];
 #pragma unroll
@@ -700,8 +701,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
         // Whole steps within a page.
         for (int i = cw; i < n_main; i += CW) {
             const int first = cC + i * KS, id = pt[first >> psh];
-            if ((unsigned)id >= (unsigned)g.c.pages) {
-                set_status(g.status, ZETA_ERR_BOUNDS);
+            if (__any_sync(kFull, (unsigned)id >= (unsigned)g.c.pages)) {
+                lost = true;
                 continue;
             }
             const uint32_t r0 = (uint32_t)row_at(id, first);
@@ -753,7 +754,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
                 if (fresh) return (uint32_t)x;
                 const int id = pt[(cC + x) >> psh];
                 const bool page = (unsigned)id < (unsigned)g.c.pages;
-                if (!page) set_status(g.status, ZETA_ERR_BOUNDS);
+                lost |= !page;
                 in = in && page;
                 return (uint32_t)(page ? row_at(id, cC + x) : 0);
             };
@@ -841,6 +842,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     }
 
     while (mine < nq) mine = chunk > 0 ? take_window(mine) : no_window(mine);
+    if (lost) set_status(g.status, ZETA_ERR_BOUNDS);
 
     // ---------------------------------------------------------- epilogue ---
     // Node r is finished by block r % cs, which has its window: the warps' parts of its sums are
