@@ -50,7 +50,7 @@ struct TreeSmem {
     static constexpr int ROWS = 8 * NG, NW = 4 * NG, PER_SM = 4 / NG, NB = NG + 1;
     static constexpr int KS = MMA ? 16 : 8, KL = KS / 4, KP = KL / 2;    // shared keys a step, a lane; pairs
     static constexpr int NV = DVP / 16;              // 16-byte pieces of them a lane holds (float32: of four keys)
-    float part[NW][ROWS][DVP + 4];      // sums over shared keys, warp by warp
+    float part[NW][ROWS][DVP + 4];                   // sums over shared keys, warp by warp
     struct {                                         // of a warp's window
         int row[64];
         union {
@@ -73,7 +73,8 @@ struct TreeSmem {
     int depth[ROWS], wst[ROWS];
     float swin[ROWS], mwin[ROWS];
     float psum[NW][ROWS], pmin[NW][ROWS];
-    float factor[NW + 1][ROWS], least[ROWS];   // softmax: of the parts and the window; the shift
+    float factor[(NW > 8 ? NW : 8) + 1][ROWS], least[ROWS];   // softmax: of the parts (warps, or up to 8
+                                                     // blocks) and the window; the shift
     float total[ROWS];
     bool again[ROWS];                           // not finite
 };

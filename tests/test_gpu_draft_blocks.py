@@ -46,6 +46,19 @@ def test_block_layouts(B, H, n, kw, weight):
     d.check(picks | {(0, 0), (0, n - 1)}, heads=(0, H - 1))
 
 
+@pytest.mark.parametrize("weight", ["cauchy", "softmax", "inv_euclid"])
+@pytest.mark.parametrize("kw", [dict(), dict(d_V=128), dict(d_V=72), dict(v_dtype="f32", d_V=128),
+                                dict(v_dtype="f32", d_V=20)], ids=_name)
+@pytest.mark.parametrize("B,H,n", [(1, 1, 5), (2, 1, 16), (3, 5, 30), (9, 7, 8)])
+def test_long_chunks_over_many_blocks(B, H, n, kw, weight):
+    """Chunks long enough that up to eight blocks share a tree's keys, some of them none."""
+    w = _work(B=B, H=H, C=4096, N=8192, **kw)
+    starts = [8000, 4096 + 3, 4095][:B] + [5000] * (B - 3)
+    d = Drafting(w, 64, starts, [n] * B, n, weight)
+    d.attend()
+    d.check({(b, t) for b in range(min(B, 4)) for t in range(0, n, 3)}, heads=(0, H - 1))
+
+
 def _moved(t, elements):
     """The same tensor some elements behind an aligned address."""
     buf = torch.empty(t.numel() + elements, dtype=t.dtype, device=t.device)
