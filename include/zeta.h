@@ -527,6 +527,8 @@ zeta_status_t zeta_cache_attend_tree(const zeta_problem_t *p, const zeta_cache_t
  *   dev_status  optional int32 device word (ZETA_ERR_BOUNDS: a leaf outside
  *             [-1, count), a line with a bad parent or a sequence out of range accepts
  *             nothing; a page out of range skips its token's row)
+ * Two sequences whose accepted tokens map to the same row leave one of them there, as in
+ * zeta_cache_append.
  * Errors: ZETA_ERR_INVALID_ARG, ZETA_ERR_UNSUPPORTED.
  */
 zeta_status_t zeta_cache_accept(const zeta_problem_t *p, const zeta_cache_t *cc, const float *k,
@@ -561,8 +563,10 @@ zeta_status_t zeta_cache_accept(const zeta_problem_t *p, const zeta_cache_t *cc,
  *               range, the sequence is skipped, granted 0; a list longer than the pools
  *               have pages, nothing changes; a page number out of range, it is passed on)
  * The result depends on the order of the sequences alone, and a call that takes pages is
- * undone by one that gives them back.  Pages that sequences share are not the list's: a
- * table holds them beyond this call's doing.  granted may be the array given as count.
+ * undone by one that gives them back.  Calls on one list follow one another on a stream.
+ * A page is in one table or in the list: a table whose entries below held were filled in
+ * otherwise (shared prompts) gives them back as if they were its own.  granted may be the
+ * array given as count.
  * Errors: ZETA_ERR_INVALID_ARG, ZETA_ERR_UNSUPPORTED.
  */
 zeta_status_t zeta_cache_reserve(const zeta_problem_t *p, const zeta_cache_t *cc,

@@ -22,6 +22,19 @@
 //    A weight enters as a bf16 half and the bf16 of what that leaves, within 2^-16 together.
 //  * A weight of zero times a value that is not finite is NaN: a node whose result is not
 //    finite is taken again, key by key, without the others.
+//
+// 59 sequences with trees of 25 nodes on average, 8 heads, 10 K tokens before each and 508 of
+// them in its chunk of 1024, windows of 48, d_V 64: 52 us for 120 MB, 2.3 TB/s (34 % of the
+// measured HBM rate; DRAM reads 156 MB: every search reads the fences' and its block's sectors).
+// What bounds it is the warps' own way: 20.7 M instructions (half of them in windows: about 800
+// for a search, its lookups, weights and sums; 147 for 16 shared keys and 16 nodes) at 32 % of the
+// issue slots, with 16 warps an SM that wait for DRAM in turn and for results of their own
+// instructions; a fifth of the time SMs run empty at the end.  With everything in L2 it takes
+// 43 us.  Tried on the way: value rows by cp.async through rings in shared memory, half the
+// warps on windows and half on shared keys 86; operands put together by byte permutes, a load
+// touching 32 rows' lines instead of 8, 59; windows of two nodes at once 66; three blocks an SM with
+// 80 registers 64 to 72 (spills); 8 nodes and 4 warps a block 60; two steps of shared keys at
+// once 59; the next step's values by prefetch or not, no difference.
 #pragma once
 
 #include <cooperative_groups.h>
