@@ -494,7 +494,7 @@ zeta_status_t zeta_cache_attend(const zeta_problem_t *p, const zeta_cache_t *cc,
  *   v         in : v_dtype [B, H, n, d_V]  (16-B aligned)
  *   gamma     in : float [H]
  *   k_pages, v_pages, order_codes, order_idx  in : the cache before this step
- *   out       out: v_dtype [B, H, n, d_V]  (16-B aligned)
+ *   out       out: v_dtype [B, H, n, d_V]  (16-B aligned; not the memory of v)
  *   rowsum    out: float [B, H, n]
  *   idx       out: int32 [B, H, n, k], the window's tokens (-1 in chunk 0), or null
  *   dev_status  optional int32 device word; an order entry outside [0, cC) or a page
@@ -521,7 +521,8 @@ zeta_status_t zeta_cache_attend_tree(const zeta_problem_t *p, const zeta_cache_t
  *   k, v      in : the tensors given to zeta_cache_attend_tree (v 16-B aligned)
  *   leaf      in : int32 [B], -1: nothing is accepted; not looked at where count is 0
  *   k_pages, v_pages  in/out (written at the accepted tokens' rows only)
- *   accepted  out: int32 [B], tokens accepted: the count for zeta_cache_order
+ *   accepted  out: int32 [B], tokens accepted: the count for zeta_cache_order (not the
+ *             memory of start, count or leaf, nor path that of parent)
  *   path      out: int32 [B, n], node of the j-th accepted token, -1 from accepted[b] on;
  *             or null
  *   dev_status  optional int32 device word (ZETA_ERR_BOUNDS: a leaf outside
@@ -566,7 +567,7 @@ zeta_status_t zeta_cache_accept(const zeta_problem_t *p, const zeta_cache_t *cc,
  * undone by one that gives them back.  Calls on one list follow one another on a stream.
  * A page is in one table or in the list: a table whose entries below held were filled in
  * otherwise (shared prompts) gives them back as if they were its own.  granted may be the
- * array given as count.
+ * array given as count, but not start or held.
  * Errors: ZETA_ERR_INVALID_ARG, ZETA_ERR_UNSUPPORTED.
  */
 zeta_status_t zeta_cache_reserve(const zeta_problem_t *p, const zeta_cache_t *cc,

@@ -357,6 +357,8 @@ ZETA_API zeta_status_t zeta_cache_reserve(const zeta_problem_t *p, const zeta_ca
     if (c.pages < 1) return ZETA_ERR_INVALID_ARG;
     if (!start || !count || !page_table || !held || !free_list || !free_count || !granted)
         return ZETA_ERR_INVALID_ARG;
+    if (granted == start || granted == held || held == start || held == count)
+        return ZETA_ERR_INVALID_ARG;                 // written while other blocks read them
     c.start = start;
     c.count = count;
     return from_cuda(zeta::launch_cache_reserve(pr, c, page_table, held, free_list, free_count,
@@ -381,6 +383,7 @@ ZETA_API zeta_status_t zeta_cache_attend_tree(
         !v_pages || !order_table || !order_codes || !order_idx || !out || !rowsum)
         return ZETA_ERR_INVALID_ARG;
     if (!aligned16(v) || !aligned16(v_pages) || !aligned16(out)) return ZETA_ERR_INVALID_ARG;
+    if (out == v) return ZETA_ERR_INVALID_ARG;       // written while other nodes read it
     c.start = start;
     c.count = count;
     c.ptab = page_table;
@@ -409,6 +412,8 @@ ZETA_API zeta_status_t zeta_cache_accept(const zeta_problem_t *p, const zeta_cac
     if (!k || !v || !start || !count || !parent || !leaf || !page_table || !k_pages || !v_pages ||
         !accepted)
         return ZETA_ERR_INVALID_ARG;
+    if (accepted == start || accepted == count || accepted == leaf || path == parent)
+        return ZETA_ERR_INVALID_ARG;                 // written while other heads read them
     if (!aligned16(v) || !aligned16(v_pages)) return ZETA_ERR_INVALID_ARG;
     c.start = start;
     c.count = count;

@@ -74,6 +74,20 @@ def test_null_and_unaligned_pointers(L):
             assert getattr(L, f)(P, Q, *a, None, None) == 1, (f, pos)
 
 
+@pytest.mark.parametrize("f,out,inputs", [("zeta_cache_attend_tree", 13, (2,)),
+                                           ("zeta_cache_accept", 9, (2, 3, 5)),
+                                           ("zeta_cache_accept", 10, (4,)),
+                                           ("zeta_cache_reserve", 6, (0, 3)),
+                                           ("zeta_cache_reserve", 3, (0, 1))])
+def test_outputs_in_the_place_of_inputs(L, f, out, inputs):
+    """What other blocks still read must not be written: refused before a launch."""
+    P, Q = ctypes.byref(_prob()), ctypes.byref(_cache())
+    for pos in inputs:
+        a = [ctypes.c_void_p(0x10000 * (i + 1)) for i in range(CALLS[f][0])]
+        a[out] = a[pos]
+        assert getattr(L, f)(P, Q, *a, None, None) == 1, (f, out, pos)
+
+
 def test_empty_calls_are_no_ops(L):
     for p, c in ((_prob(B=0), _cache()), (_prob(H=0), _cache()), (_prob(), _cache(n=0))):
         P, Q = ctypes.byref(p), ctypes.byref(c)

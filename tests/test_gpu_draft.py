@@ -265,15 +265,16 @@ def test_bad_order_entries_are_dropped():
     assert hit > 0
 
 
-def test_pools_past_32_bit_offsets():
+@pytest.mark.parametrize("v_dtype,d_V", [("bf16", 256), ("bf16", 128), ("f32", 64)])
+def test_pools_past_32_bit_offsets(v_dtype, d_V):
     """Pages whose bytes lie past 2^32 of the pools."""
-    w = _work(B=1, H=8, N=1024, C=256, d_V=256, k=20)
+    w = _work(B=1, H=8, N=1024, C=256, d_V=d_V, k=20, v_dtype=v_dtype)
     d = Drafting(w, 64, [700], [11], 11)
     want = d.attend()
-    pages = 40000                                    # x 8 x 64 x 256 values: 10.5 GB
+    pages = 40000                                    # x 8 x 64 rows of at least 256 bytes: 5.2 GB
     ids = torch.arange(16, device="cuda") * 7 + pages - 140
     big = [torch.empty(pages, 8, 64, 3, device="cuda"),
-           torch.empty(pages, 8, 64, 256, dtype=torch.bfloat16, device="cuda")]
+           torch.empty(pages, 8, 64, d_V, dtype=d.vdt, device="cuda")]
     order = [torch.empty(2, pages, 8, 64, dtype=x.dtype, device="cuda")
              for x in (d.cache.order_codes, d.cache.order_idx)]
     old = d.table[0, :16].long()
