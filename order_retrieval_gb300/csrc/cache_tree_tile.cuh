@@ -14,7 +14,7 @@
 //    that the window may hold.  It looks up and weighs the entries a lane each, then their
 //    value rows stream through registers.
 //  * Shared keys: the sequence's tokens of the chunk, then the nodes, 16 (float32: 8) a step
-//    and warp, straight from global memory, the next step's coordinates ahead.
+//    and warp, straight from global memory.
 //  * bf16 products run on mma.sync without shared memory: of 16 keys lane (g, t) loads 32
 //    bytes (values 16t ..) of the rows of keys g and g + 8, a whole row to four lanes, so that
 //    a load touches 8 lines of L1; movmatrix turns the 8 x 8 blocks into A operands (values
@@ -29,12 +29,13 @@
 // What bounds it is the warps' own way: 20.7 M instructions (half of them in windows: about 800
 // for a search, its lookups, weights and sums; 147 for 16 shared keys and 16 nodes) at 32 % of the
 // issue slots, with 16 warps an SM that wait for DRAM in turn and for results of their own
-// instructions; a fifth of the time SMs run empty at the end.  With everything in L2 it takes
-// 43 us.  Tried on the way: value rows by cp.async through rings in shared memory, half the
+// instructions; a fifth of the time SMs run empty at the end.  (At 57 us for this, texts of
+// up to 2 K tokens, all in L2, took 43.)  Tried on the way: value rows by cp.async through rings in shared memory, half the
 // warps on windows and half on shared keys 86; operands put together by byte permutes, a load
 // touching 32 rows' lines instead of 8, 59; windows of two nodes at once 66; three blocks an SM with
 // 80 registers 64 to 72 (spills); 8 nodes and 4 warps a block 60; two steps of shared keys at
-// once 59; the next step's values by prefetch or not, no difference.
+// once 59; their values asked into L2 ahead, no difference; all slices' first nodes before their
+// others 54 (what they share leaves L2).
 #pragma once
 
 #include <cooperative_groups.h>
@@ -293,17 +294,6 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
     const int first_key = Sm::MMA ? 2 * s4 : 2 * (lane >> 3);                // the lane's first key of a step
     const int piece = min(lane & 15, ppr - 1) * 16;          // float32: its bytes of a value row
     const int second = NV == 4 ? 0 : min((lane & 15) + 16, ppr - 1) * 16 - piece;
-    // The whole steps' values, and the nodes' rows, are asked into L2 ahead.
-    if (cw <= nn / KS && lane < KS) {
-        const int64_t r = min(cw * KS + lane, nn - 1);
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(vf + r * vrow));
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(kf + r * krow));
-    }
-    for (int i = cw; i < n_main; i += CW) {
-        const int first = cC + i * KS, id = pt[first >> psh];
-        if ((unsigned)id < (unsigned)g.c.pages && lane * 128 < KS * vrow)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(vt + (uint64_t)(uint32_t)row_at(id, first) * (uint32_t)vrow + lane * 128));
-    }
 
     // ------------------------------------------------------------ window ---
     // The cluster's warps take the nodes in turn.  While a window's keys and values are under
