@@ -60,7 +60,8 @@ template <typename V, int DVP, int NG>
 struct TreeSmem {
     static constexpr bool MMA = sizeof(V) == 2;
     // NG groups of 8 nodes a block; warps, blocks an SM (128 registers a thread), a window's steps
-    // under way.
+    // under way (64 sequences, 16 nodes a block: 2, 3, 4 of them 54, 52, 56 us; lines of 200, 128
+    // wide, 8 nodes: 2, 3 of them 48.6, 51.7).
     static constexpr int ROWS = 8 * NG, NW = 4 * NG, PER_SM = 4 / NG, NB = NG + 1;
     static constexpr int KS = MMA ? 16 : 8, KL = KS / 4, KP = KL / 2;    // shared keys a step, a lane; pairs
     static constexpr int NV = DVP / 16;              // 16-byte pieces of them a lane holds (float32: of four keys)
