@@ -488,8 +488,9 @@ zeta_status_t zeta_cache_attend(const zeta_problem_t *p, const zeta_cache_t *cc,
  * Node t of sequence b, with position i < (c + 1) C, c = start[b] / C, attends to the k
  * keys around its code's rank in prefix c (none for c = 0), to the tokens cC .. start[b]-1
  * and to the nodes of its line, itself included; weights, out and rowsum as in
- * zeta_attend_fwd.  That is what zeta_cache_attend gives for the same tokens in a line;
- * weights and rounding as there.
+ * zeta_attend_fwd.  That is what zeta_cache_attend gives for the same tokens in a line.
+ * Weights and sums are float32 in calls of every size (a weight on the tensor cores: three
+ * bf16 parts that hold its 24 bits); out is rounded once.
  *   q, k      in : float [B, H, n, d_K]: the nodes' queries and keys
  *   v         in : v_dtype [B, H, n, d_V]  (16-B aligned)
  *   gamma     in : float [H]

@@ -18,13 +18,16 @@
 //  * bf16 products run on mma.sync without shared memory: of 16 keys lane (g, t) loads 32
 //    bytes (values 16t ..) of the rows of keys g and g + 8, a whole row to four lanes, so that
 //    a load touches 8 lines of L1; movmatrix turns the 8 x 8 blocks into A operands (values
-//    times keys).  B (keys times columns) has 8 nodes' weights, a window's in column 0 and 1.
-//    A weight enters as a bf16 half and the bf16 of what that leaves, within 2^-16 together.
+//    times keys).  B (keys times columns) has 8 nodes' weights, a window's in columns 0 to 2.
+//    A weight enters as three bf16 parts, each the nearest to what those before it leave: 3 x 8
+//    bits hold all 24 of it, so that sums are those of float32 weights.  (Two parts, within 2^-16,
+//    let one output in a thousand round to the other neighbour; the third costs 2.9 of the 55 us
+//    below.)
 //  * A weight of zero times a value that is not finite is NaN: a node whose result is not
 //    finite is taken again, key by key, without the others.
 //
 // 59 sequences with trees of 25 nodes on average, 8 heads, 10 K tokens before each and 508 of
-// them in its chunk of 1024, windows of 48, d_V 64: 52 us for 120 MB, 2.3 TB/s (34 % of the
+// them in its chunk of 1024, windows of 48, d_V 64: 55 us for 120 MB, 2.2 TB/s (32 % of the
 // measured HBM rate; DRAM reads 156 MB: every search reads the fences' and its block's sectors).
 // What bounds it is the warps' own way: 20.7 M instructions (half of them in windows: about 800
 // for a search, its lookups, weights and sums; 147 for 16 shared keys and 16 nodes) at 32 % of the
@@ -71,7 +74,7 @@ struct TreeSmem {
         union {
             int cand[128];                           // entries that it may hold
             float w[64];                             // float32: weights
-            uint16_t half[2][64];                    // bf16: weights' halves and rests
+            uint16_t bits[3][64];                    // bf16: weights' parts
         };
         float x[64 * 4];                             // coordinates
     } gather[NW];
@@ -113,6 +116,13 @@ __device__ __forceinline__ void ld32(uint32_t (&x)[8], const char *p, const char
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
         x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     }
+}
+
+// The bf16 next to each of two numbers, packed; what that leaves of them stays (exact).
+__device__ __forceinline__ uint32_t take_part(float2 &left) {
+    const uint32_t part = pack_bf16(left.x, left.y);
+    left = sub2(left, make_float2(__uint_as_float(part << 16), __uint_as_float(part & 0xffff0000u)));
+    return part;
 }
 
 // One node key by key (a warp, lanes over the value columns).
@@ -470,9 +480,13 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
                 const float w = is[v] ? weight_fast<WK>(d2[v], mr, inv_g2) : 0.f;
                 sw += w;
                 if constexpr (Sm::MMA) {
-                    const __nv_bfloat16 half = __float2bfloat16_rn(w);
-                    ga.half[0][v * 32 + lane] = __bfloat16_as_ushort(half);
-                    ga.half[1][v * 32 + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(w - __bfloat162float(half)));
+                    float left = w;
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) {
+                        const __nv_bfloat16 part = __float2bfloat16_rn(left);
+                        ga.bits[p][v * 32 + lane] = __bfloat16_as_ushort(part);
+                        left -= __bfloat162float(part);
+                    }
                 } else {
                     ga.w[v * 32 + lane] = w;
                 }
@@ -482,11 +496,11 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
                 float acc[16] = {0.f};                       // float32: a piece's sums
                 auto use = [&](const uint32_t (&y)[2][8], int i) {
                     if constexpr (Sm::MMA) {
-                        // Halves of the weights in column 0 of B, rests in column 1.
+                        // The weights' parts in columns 0, 1 and 2 of B.
                         uint32_t b0 = 0u, b1 = 0u;
-                        if (g4 < 2) {
-                            b0 = *reinterpret_cast<const uint32_t *>(&ga.half[g4][i * WS + 2 * s4]);
-                            b1 = *reinterpret_cast<const uint32_t *>(&ga.half[g4][i * WS + 2 * s4 + 8]);
+                        if (g4 < 3) {
+                            b0 = *reinterpret_cast<const uint32_t *>(&ga.bits[g4][i * WS + 2 * s4]);
+                            b1 = *reinterpret_cast<const uint32_t *>(&ga.bits[g4][i * WS + 2 * s4 + 8]);
                         }
                         __syncwarp();
                         operands(y, [&](int w, const uint32_t (&m)[4]) {
@@ -523,11 +537,12 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
                     *to = t0 > 0 ? __fmaf_rn(scale, *to, a) : a;
                 };
                 if constexpr (Sm::MMA) {
-                    if (s4 == 0) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            put(column + 4 * c, acc[4 * c] + acc[4 * c + 1]);
-                            put(column + 4 * c + 2, acc[4 * c + 2] + acc[4 * c + 3]);
+                    for (int c = 0; c < 4; ++c) {            // column 2 is the next lane's
+                        const float a = __shfl_down_sync(kFull, acc[4 * c], 1), b = __shfl_down_sync(kFull, acc[4 * c + 2], 1);
+                        if (s4 == 0) {
+                            put(column + 4 * c, acc[4 * c] + (acc[4 * c + 1] + a));
+                            put(column + 4 * c + 2, acc[4 * c + 2] + (acc[4 * c + 3] + b));
                         }
                     }
                 } else {
@@ -646,15 +661,15 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
         // The step's values times the weights of both groups' nodes.
         auto multiply = [&](const float2 (*w)[Sm::KP], const uint32_t (*v)[8], auto &more) {
             if constexpr (Sm::MMA) {
-                uint32_t b[NG][4];                           // halves and rests of two pairs
+                uint32_t b[NG][6];                           // three parts of two pairs
 #pragma unroll
-                for (int n = 0; n < NG; ++n) {
+                for (int n = 0; n < NG; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        b[n][e] = pack_bf16(w[n][e].x, w[n][e].y);
-                        b[n][2 + e] = pack_rest(w[n][e], b[n][e]);
+                        float2 left = w[n][e];
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) b[n][2 * p + e] = take_part(left);
                     }
-                }
                 __syncwarp();
 #pragma unroll
                 for (int hh = 0; hh < H; ++hh)
@@ -663,8 +678,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs g, int cs) {
                         for (int n = 0; n < NG; ++n) {
                             if (n > 0 && !two) break;
                             float(&o)[4] = *reinterpret_cast<float(*)[4]>(&acc[n][16 * hh + 4 * c]);
-                            mma16816(o, x, b[n][0], b[n][1]);
-                            mma16816(o, x, b[n][2], b[n][3]);
+#pragma unroll
+                            for (int p = 0; p < 3; ++p) mma16816(o, x, b[n][2 * p], b[n][2 * p + 1]);
                         }
                     });
             } else {

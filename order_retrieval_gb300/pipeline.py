@@ -165,12 +165,12 @@ class ZetaCache:
     order_table (default: table; pass another one when sequences share K/V pages).
     Everything is enqueued on the given or current stream and allocates nothing,
     so a step can be captured into a CUDA graph.  Weights and sums are float32; for bf16
-    values large calls take each weight as two bf16 parts (within 2^-16 of it), so that a
-    token's outputs in calls of different sizes agree to one step of bf16.  Findings of the kernels (a
-    length or page out of range) go to ``status``, one int32 word, unless
-    dev_status is given.  There is no backward.  Pools and sizes are those the cache was
-    made with: they cannot be assigned, and a pool whose memory changes in place is taken
-    as it then lies, or refused where it no longer fits.
+    values large calls of attend take the weights of a row's own chunk as two bf16 parts (within
+    2^-16), so that a token's outputs in calls of different sizes agree to one step of bf16;
+    attend_tree keeps all of a weight's bits.  Findings of the kernels (a length or page out of
+    range) go to ``status``, one int32 word, unless dev_status is given.  There is no backward.
+    Pools and sizes are those the cache was made with: they cannot be assigned, and a pool whose
+    memory changes in place is taken as it then lies, or refused where it no longer fits.
     """
 
     _lib = None                          # set last; from then on these stay as they are
