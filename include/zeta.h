@@ -465,16 +465,18 @@ zeta_status_t zeta_cache_attend(const zeta_problem_t *p, const zeta_cache_t *cc,
  * (parent -1); its depth is that of its parent plus one, 0 at the top, and its position
  * start[b] + depth.  Keys and values of the nodes stay in the step's own tensors.  One
  * step, on one stream:
- *   zeta_cache_reserve      pages for the longest line that may be accepted;
+ *   zeta_cache_reserve      with count = min(tokens of the longest line that may be
+ *                           accepted, C - start % C): its pages;
  *   zeta_cache_attend_tree  every node over the cache and its own line (each layer's
  *                           cache; several nodes may be tried in one call);
  *   (the program decides which node's line is right)
- *   zeta_cache_accept       that line becomes the sequence's next tokens (each layer's
- *                           cache);
+ *   zeta_cache_accept_granted  that line becomes the sequence's next tokens (each layer's
+ *                           cache), none where reserve had no pages for them;
  *   zeta_cache_order        with count = accepted, as after zeta_cache_append.
  * A line ends with the chunk that start lies in (C): attend_tree gives nodes behind that
  * end no result and accept cuts the line there, so that a step's nodes share one sorted
- * prefix.  A step can always accept a token: a chunk that is full begins the next.
+ * prefix.  A step that has a page can always accept a token: a chunk that is full begins
+ * the next.
  *   parent   int32 [B, n] (device): entries count[b] .. n-1 are not looked at; an entry
  *            outside [-1, t) costs the lines through it (ZETA_ERR_BOUNDS).
  *   start, count  as for the cache calls, but 0 <= start <= N and, where count > 0,
@@ -523,7 +525,9 @@ zeta_status_t zeta_cache_attend_tree(const zeta_problem_t *p, const zeta_cache_t
  *   leaf      in : int32 [B], -1: nothing is accepted; not looked at where count is 0
  *   k_pages, v_pages  in/out (written at the accepted tokens' rows only)
  *   accepted  out: int32 [B], tokens accepted: the count for zeta_cache_order (not the
- *             memory of start, count or leaf, nor path that of parent)
+ *             memory of start, count or leaf, nor path that of parent).  Every token of the
+ *             line counts, one without a page too: where pages may be missing call
+ *             zeta_cache_accept_granted
  *   path      out: int32 [B, n], node of the j-th accepted token, -1 from accepted[b] on;
  *             or null
  *   dev_status  optional int32 device word (ZETA_ERR_BOUNDS: a leaf outside
@@ -541,6 +545,22 @@ zeta_status_t zeta_cache_accept(const zeta_problem_t *p, const zeta_cache_t *cc,
                                 cudaStream_t stream);
 
 /*
+ * zeta_cache_accept_granted -- zeta_cache_accept of no more tokens than were granted.
+ * The pages have no counterpart: as for zeta_cache_accept.
+ * The line ends after granted[b] tokens where it has more, so that with zeta_cache_reserve's
+ * granted every token accepted has a page.
+ *   granted   in : int32 [B] (negative as 0); all else as for zeta_cache_accept
+ * Errors: ZETA_ERR_INVALID_ARG, ZETA_ERR_UNSUPPORTED.
+ */
+zeta_status_t zeta_cache_accept_granted(const zeta_problem_t *p, const zeta_cache_t *cc,
+                                        const float *k, const void *v, const int32_t *start,
+                                        const int32_t *count, const int32_t *parent,
+                                        const int32_t *leaf, const int32_t *granted,
+                                        const int32_t *page_table, float *k_pages, void *v_pages,
+                                        int32_t *accepted, int32_t *path, int32_t *dev_status,
+                                        cudaStream_t stream);
+
+/*
  * zeta_cache_reserve -- page tables and row numbers from the requests' lengths.
  * The pages have no counterpart.
  * After the call sequence b holds ceil((start[b] + count[b]) / page) pages, entries
@@ -549,10 +569,12 @@ zeta_status_t zeta_cache_accept(const zeta_problem_t *p, const zeta_cache_t *cc,
  * then the others take theirs in the order of b, from the list's end.  From the first
  * sequence on that the list is too short for, sequences that need pages get none and stay
  * as they were: granted[b] = 0.  All others: granted[b] = count[b].  Given granted as
- * their count, the other calls take what has pages.
+ * their count, zeta_cache_append, _order and _attend take what has pages; of a draft, whose
+ * count is one of nodes, zeta_cache_accept_granted does.
  *   p, cc     B, N, C as everywhere, n, page, pages, table_len of the cache (the heads and
  *             the order pools play no part); n bounds count
- *   start, count  int32 [B], 0 <= count <= n, 0 <= start, start + count <= N
+ *   start, count  int32 [B], 0 <= count <= n, 0 <= start, start + count <= N (of a draft the
+ *               tokens of its longest line up to the chunk's end: there is always room for them)
  *   page_table  in/out: int32 [B, table_len]
  *   held        in/out: int32 [B], pages that sequence b holds
  *   free_list   in/out: int32 [pages], places [0, *free_count) are the free pages

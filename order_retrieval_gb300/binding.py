@@ -123,6 +123,8 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
     L.zeta_cache_attend_tree.restype = S
     L.zeta_cache_accept.argtypes = [PP, PC] + [P] * 13
     L.zeta_cache_accept.restype = S
+    L.zeta_cache_accept_granted.argtypes = [PP, PC] + [P] * 14
+    L.zeta_cache_accept_granted.restype = S
     L.zeta_cache_reserve.argtypes = [PP, PC] + [P] * 10
     L.zeta_cache_reserve.restype = S
     _lib = L
@@ -490,10 +492,7 @@ def zeta_cache_attend_tree(p, c, q, k, v, gamma, start, count, parent, page_tabl
                                         _ptr(dev_status), _stream(stream)))
 
 
-def zeta_cache_accept(p, c, k, v, start, count, parent, leaf, page_table, k_pages, v_pages,
-                      accepted, path=None, dev_status=None, stream=None):
-    """The line of nodes that ends in leaf [B] into the pages; accepted int32 [B], path int32
-    [B,n] or None."""
+def _expect_accept(p, c, k, v, parent, leaf, k_pages, v_pages, accepted, path):
     S, R = p.B * p.H * c.n, c.pages * p.H * c.page
     vt = v_torch_dtype(p)
     _expect(k, "k", torch.float32, S * p.d_K)
@@ -504,6 +503,13 @@ def zeta_cache_accept(p, c, k, v, start, count, parent, leaf, page_table, k_page
     _expect(leaf, "leaf", torch.int32, p.B)
     _expect(accepted, "accepted", torch.int32, p.B)
     _expect(path, "path", torch.int32, p.B * c.n)
+
+
+def zeta_cache_accept(p, c, k, v, start, count, parent, leaf, page_table, k_pages, v_pages,
+                      accepted, path=None, dev_status=None, stream=None):
+    """The line of nodes that ends in leaf [B] into the pages; accepted int32 [B], path int32
+    [B,n] or None."""
+    _expect_accept(p, c, k, v, parent, leaf, k_pages, v_pages, accepted, path)
     _expect_cache(p, c, start, count, [(page_table, "page_table")], dev_status)
     _check("zeta_cache_accept",
            lib().zeta_cache_accept(ctypes.byref(p), ctypes.byref(c), _ptr(k), _ptr(v),
@@ -511,6 +517,20 @@ def zeta_cache_accept(p, c, k, v, start, count, parent, leaf, page_table, k_page
                                    _ptr(page_table), _ptr(k_pages), _ptr(v_pages),
                                    _ptr(accepted), _ptr(path), _ptr(dev_status),
                                    _stream(stream)))
+
+
+def zeta_cache_accept_granted(p, c, k, v, start, count, parent, leaf, granted, page_table, k_pages,
+                              v_pages, accepted, path=None, dev_status=None, stream=None):
+    """zeta_cache_accept of at most granted [B] tokens a line."""
+    _expect_accept(p, c, k, v, parent, leaf, k_pages, v_pages, accepted, path)
+    _expect(granted, "granted", torch.int32, p.B)
+    _expect_cache(p, c, start, count, [(page_table, "page_table")], dev_status)
+    _check("zeta_cache_accept_granted",
+           lib().zeta_cache_accept_granted(ctypes.byref(p), ctypes.byref(c), _ptr(k), _ptr(v),
+                                           _ptr(start), _ptr(count), _ptr(parent), _ptr(leaf),
+                                           _ptr(granted), _ptr(page_table), _ptr(k_pages),
+                                           _ptr(v_pages), _ptr(accepted), _ptr(path),
+                                           _ptr(dev_status), _stream(stream)))
 
 
 def zeta_cache_reserve(p, c, start, count, page_table, held, free_list, free_count, granted,

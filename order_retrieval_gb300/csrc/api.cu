@@ -394,14 +394,13 @@ ZETA_API zeta_status_t zeta_cache_attend_tree(
     return from_cuda(zeta::launch_cache_attend_tree(pr, g, stream));
 }
 
-ZETA_API zeta_status_t zeta_cache_accept(const zeta_problem_t *p, const zeta_cache_t *cc,
-                                         const float *k, const void *v, const int32_t *start,
-                                         const int32_t *count, const int32_t *parent,
-                                         const int32_t *leaf, const int32_t *page_table,
-                                         float *k_pages, void *v_pages, int32_t *accepted,
-                                         int32_t *path, int32_t *dev_status,
-                                         cudaStream_t stream) {
-    zeta::CallRange range_("zeta_cache_accept");
+namespace {
+
+zeta_status_t accept(const zeta_problem_t *p, const zeta_cache_t *cc, const float *k,
+                     const void *v, const int32_t *start, const int32_t *count,
+                     const int32_t *parent, const int32_t *leaf, const int32_t *granted,
+                     bool limited, const int32_t *page_table, float *k_pages, void *v_pages, int32_t *accepted,
+                     int32_t *path, int32_t *dev_status, cudaStream_t stream) {
     Prob pr;
     zeta::Cache c;
     zeta_status_t s = check_cache(p, cc, &pr, &c);
@@ -410,16 +409,41 @@ ZETA_API zeta_status_t zeta_cache_accept(const zeta_problem_t *p, const zeta_cac
     if (empty(pr) || c.n == 0) return ZETA_OK;
     if (c.pages < 1) return ZETA_ERR_INVALID_ARG;
     if (!k || !v || !start || !count || !parent || !leaf || !page_table || !k_pages || !v_pages ||
-        !accepted)
+        !accepted || (limited && !granted))
         return ZETA_ERR_INVALID_ARG;
-    if (accepted == start || accepted == count || accepted == leaf || path == parent)
+    if (accepted == start || accepted == count || accepted == leaf || path == parent ||
+        (granted && (accepted == granted || path == granted)))
         return ZETA_ERR_INVALID_ARG;                 // written while other heads read them
     if (!aligned16(v) || !aligned16(v_pages)) return ZETA_ERR_INVALID_ARG;
     c.start = start;
     c.count = count;
     c.ptab = page_table;
-    return from_cuda(zeta::launch_cache_accept(pr, c, parent, leaf, k, v, k_pages, v_pages,
-                                               accepted, path, dev_status, stream));
+    return from_cuda(zeta::launch_cache_accept(pr, c, parent, leaf, granted, k, v, k_pages,
+                                               v_pages, accepted, path, dev_status, stream));
+}
+
+}  // namespace
+
+ZETA_API zeta_status_t zeta_cache_accept(const zeta_problem_t *p, const zeta_cache_t *cc,
+                                         const float *k, const void *v, const int32_t *start,
+                                         const int32_t *count, const int32_t *parent,
+                                         const int32_t *leaf, const int32_t *page_table,
+                                         float *k_pages, void *v_pages, int32_t *accepted,
+                                         int32_t *path, int32_t *dev_status,
+                                         cudaStream_t stream) {
+    zeta::CallRange range_("zeta_cache_accept");
+    return accept(p, cc, k, v, start, count, parent, leaf, nullptr, false, page_table, k_pages,
+                  v_pages, accepted, path, dev_status, stream);
+}
+
+ZETA_API zeta_status_t zeta_cache_accept_granted(
+    const zeta_problem_t *p, const zeta_cache_t *cc, const float *k, const void *v,
+    const int32_t *start, const int32_t *count, const int32_t *parent, const int32_t *leaf,
+    const int32_t *granted, const int32_t *page_table, float *k_pages, void *v_pages,
+    int32_t *accepted, int32_t *path, int32_t *dev_status, cudaStream_t stream) {
+    zeta::CallRange range_("zeta_cache_accept_granted");
+    return accept(p, cc, k, v, start, count, parent, leaf, granted, true, page_table, k_pages,
+                  v_pages, accepted, path, dev_status, stream);
 }
 
 ZETA_API zeta_status_t zeta_check_bounded_wait(uint32_t iterations, int32_t arrive,

@@ -1,7 +1,7 @@
 // cache_accept.cu -- the accepted branch of a draft into the pages.
 //
-// The line of nodes that ends in leaf[b], up to the end of the chunk that start lies in,
-// becomes the sequence's next tokens: a copy of rows, as cache_append.cu, through the
+// The line of nodes that ends in leaf[b], up to the end of the chunk that start lies in and to
+// granted[b] tokens where that is given, becomes the sequence's next tokens: a copy of rows, as cache_append.cu, through the
 // line.  A block per sequence and head finds the line in the parents in shared memory as
 // bits (one thread climbs, a run of nodes below one another in one step) and puts it in
 // order by counting bits, then copies its rows, a thread per 16-byte piece of a value row (a
@@ -23,7 +23,8 @@ __global__ void __launch_bounds__(kThreads)
 cache_accept_kernel(const float *__restrict__ k, const Piece *__restrict__ v,
                     float *__restrict__ k_pages, Piece *__restrict__ v_pages, Cache c,
                     const int32_t *__restrict__ parents, const int32_t *__restrict__ leaves,
-                    int32_t *__restrict__ accepted, int32_t *__restrict__ path, int32_t *status,
+                    const int32_t *__restrict__ granted, int32_t *__restrict__ accepted,
+                    int32_t *__restrict__ path, int32_t *status,
                     int N, int H, int C, int dK, int ppr) {
     __shared__ int parent[kMaxDraft], line[kMaxDraft];
     __shared__ uint32_t run[kMaxDraft / 32], bits[kMaxDraft / 32];
@@ -31,6 +32,7 @@ cache_accept_kernel(const float *__restrict__ k, const Piece *__restrict__ v,
     const int tid = threadIdx.x, warp = tid >> 5, h = blockIdx.x, b = blockIdx.y;
     const int early = tid < c.n ? __ldg(parents + (int64_t)b * c.n + tid) : -1;
     int leaf = __ldg(leaves + b);
+    const int most = granted ? max(__ldg(granted + b), 0) : INT32_MAX;
     const Seq seq = drafts_of(c, b, N, status);
     if (leaf < -1 || leaf >= seq.count) {
         if (tid == 0 && seq.count > 0) set_status(status, ZETA_ERR_BOUNDS);
@@ -51,7 +53,7 @@ cache_accept_kernel(const float *__restrict__ k, const Piece *__restrict__ v,
         len_sh = depth + 1;
     }
     __syncthreads();
-    const int len = min(len_sh, C - seq.start % C);  // no line: 0
+    const int len = min(min(len_sh, C - seq.start % C), most);       // no line: 0
     if (len > 0) {                                   // the line's nodes in order
         for (int u = tid; u <= leaf; u += kThreads) {
             const uint32_t own = bits[u >> 5];
@@ -104,15 +106,15 @@ cache_accept_kernel(const float *__restrict__ k, const Piece *__restrict__ v,
 }  // namespace
 
 cudaError_t launch_cache_accept(const Prob &p, const Cache &c, const int32_t *parent,
-                                const int32_t *leaf, const float *k, const void *v, float *k_pages,
-                                void *v_pages, int32_t *accepted, int32_t *path, int32_t *status,
-                                cudaStream_t st) {
+                                const int32_t *leaf, const int32_t *granted, const float *k,
+                                const void *v, float *k_pages, void *v_pages, int32_t *accepted,
+                                int32_t *path, int32_t *status, cudaStream_t st) {
     const int esz = p.vdt == ZETA_BF16 ? 2 : 4;
     const int bytes = p.dV * esz;
 #define ZETA_ACCEPT(Piece)                                                                     \
     cache_accept_kernel<Piece><<<dim3((unsigned)p.H, (unsigned)p.B), kThreads, 0, st>>>(       \
         k, static_cast<const Piece *>(v), k_pages, static_cast<Piece *>(v_pages), c, parent,   \
-        leaf, accepted, path, status, p.N, p.H, p.C, p.dK, bytes / (int)sizeof(Piece))
+        leaf, granted, accepted, path, status, p.N, p.H, p.C, p.dK, bytes / (int)sizeof(Piece))
     if (bytes % 16 == 0) ZETA_ACCEPT(uint4);
     else if (esz == 4) ZETA_ACCEPT(uint32_t);
     else ZETA_ACCEPT(uint16_t);

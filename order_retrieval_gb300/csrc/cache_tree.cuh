@@ -77,9 +77,9 @@ __device__ __forceinline__ uint32_t run_bits(const int *parent, int w, int nodes
 
 cudaError_t launch_cache_attend_tree(const Prob &p, const TreeArgs &g, cudaStream_t st);
 cudaError_t launch_cache_accept(const Prob &p, const Cache &c, const int32_t *parent,
-                                const int32_t *leaf, const float *k, const void *v, float *k_pages,
-                                void *v_pages, int32_t *accepted, int32_t *path, int32_t *status,
-                                cudaStream_t st);
+                                const int32_t *leaf, const int32_t *granted, const float *k,
+                                const void *v, float *k_pages, void *v_pages, int32_t *accepted,
+                                int32_t *path, int32_t *status, cudaStream_t st);
 cudaError_t launch_cache_reserve(const Prob &p, const Cache &c, int32_t *table, int32_t *held,
                                  int32_t *free_list, int32_t *free_count, int32_t *granted,
                                  int32_t *slots, int32_t *status, cudaStream_t st);

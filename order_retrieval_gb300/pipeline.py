@@ -156,10 +156,15 @@ class ZetaCache:
     Drafted tokens, a tree of up to n nodes per sequence (parent int32 [B, n], -1 at the
     top), whose keys and values stay in k and v until a line of them is accepted::
 
+        longest = torch.minimum(longest, C - start % C)      # a line ends with its chunk
         cache.reserve(start, longest, table, held, free, free_count, granted)
         cache.attend_tree(q, k, v, gamma, start, count, parent, table, out, rowsum)
-        cache.accept(k, v, start, count, parent, leaf, table, accepted)
+        cache.accept(k, v, start, count, parent, leaf, table, accepted, granted=granted)
         cache.order(start, accepted, table, n=n)
+
+    longest (int32 [B], 0 where count is 0): tokens of the longest line that may be accepted.
+    Where the free list was too short for a sequence, granted is 0 and so is accepted: nothing
+    counts as a token that has no page.
 
     The prefixes of completed chunks are kept in the order pools through
     order_table (default: table; pass another one when sequences share K/V pages).
@@ -377,21 +382,25 @@ class ZetaCache:
                    st, dev_status, stream)
 
     def accept(self, k, v, start, count, parent, leaf, page_table, accepted, path=None,
-               dev_status=None, stream=None):
+               dev_status=None, stream=None, granted=None):
         """The line of nodes that ends in leaf int32 [B] (-1: none) becomes the sequence's next
-        tokens, up to the end of the chunk that start[b] lies in; accepted int32 [B] gets how many,
-        path int32 [B,n], where given, their nodes (-1 behind them)."""
+        tokens, up to the end of the chunk that start[b] lies in and, where granted int32 [B] (of
+        ``reserve``) is given, at most granted[b] of them; accepted int32 [B] gets how many, path
+        int32 [B,n], where given, their nodes (-1 behind them).  Without granted the line's tokens
+        must have their pages: one that has none is counted, but stored nowhere (``status``)."""
         tp, B, width = self._table(page_table)
         n = self._rows(k, "k")
         p, c, per_seq, _, k_shape, v_shape, _ = self._sizes(B, n, width)
         take = self._take
         kp, vp, _, _, st = self._memory()
-        self._call(self._lib.zeta_cache_accept,
-                   (p, c, take(k, "k", _F32, k_shape), take(v, "v", self._vt, v_shape),
-                    take(start, "start", _I32, per_seq), take(count, "count", _I32, per_seq),
-                    take(parent, "parent", _I32, (B, n)), take(leaf, "leaf", _I32, per_seq), tp,
-                    kp, vp, take(accepted, "accepted", _I32, per_seq),
-                    None if path is None else take(path, "path", _I32, (B, n))),
+        f, cap = self._lib.zeta_cache_accept, ()
+        if granted is not None:
+            f, cap = self._lib.zeta_cache_accept_granted, (take(granted, "granted", _I32, per_seq),)
+        self._call(f, (p, c, take(k, "k", _F32, k_shape), take(v, "v", self._vt, v_shape),
+                       take(start, "start", _I32, per_seq), take(count, "count", _I32, per_seq),
+                       take(parent, "parent", _I32, (B, n)), take(leaf, "leaf", _I32, per_seq),
+                       *cap, tp, kp, vp, take(accepted, "accepted", _I32, per_seq),
+                       None if path is None else take(path, "path", _I32, (B, n))),
                    st, dev_status, stream)
 
     def reserve(self, start, count, page_table, held, free, free_count, granted, slots=None,
@@ -401,7 +410,8 @@ class ZetaCache:
         [0, free_count) are the free pages) and free_count int32 [1] change in place.  granted
         int32 [B] gets count[b], or 0 where the list was too short; slots int32 [B,n], where
         given, the row number of every new token.  n: the step's rows (default: those of slots,
-        or C)."""
+        or C).  start[b] + count[b] <= N: of a draft, the tokens of its longest line up to the
+        chunk's end (``accept`` takes granted)."""
         tp, B, width = self._table(page_table)
         if n is None:
             n = self.C if slots is None else slots.shape[-1]

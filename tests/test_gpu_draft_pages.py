@@ -1,0 +1,135 @@
+"""GPU tests of drafting when pages run out and at the end of a text: the step as it is documented
+(reserve the longest line up to the chunk's end, attend the whole tree, accept what was granted)."""
+import numpy as np
+import pytest
+import torch
+
+from order_retrieval_gb300 import binding as zb
+from order_retrieval_gb300 import workloads as W
+
+from draft_util import Drafting, line, tree
+
+pytestmark = [
+    pytest.mark.gpu,
+    pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU"),
+]
+
+
+def _work(**kw):
+    base = dict(name="draft", B=5, H=2, N=128, d_K=3, d_V=64, k=12, C=32, bits=10, v_dtype="bf16",
+                gamma=(0.5, 1.0), dist="uniform", v_dist="normal", seed=31)
+    base.update(kw)
+    return W.Workload(**base)
+
+
+@pytest.mark.parametrize("v_dtype,page", [("bf16", 16), ("f32", 4), ("bf16", 64)])
+def test_steps_under_a_short_list(v_dtype, page):
+    """Texts are written up to their last place, N - 1 among the starts; the list is too short for
+    all.  Who is refused accepts nothing, no page is read that was never written, and nothing is
+    recorded.  Where nobody gets a page the longest text ends and its place begins again."""
+    w = _work(v_dtype=v_dtype)
+    n, B, N, C = 11, w.B, w.N, w.C
+    d = Drafting(w, page, [0] * B, [0] * B, n)
+    c, rng = d.cache, np.random.default_rng(page)
+    full = [torch.from_numpy(d.g[x]).cuda() for x in "qk"]
+    full.append(torch.from_numpy(np.stack(d.values).astype(np.float32)).cuda().to(d.vdt))
+    pages = 7 if page == 64 else 3 * N // page       # of 5 N / page
+    table, held = d.ints(np.full((B, N // page), -1)), d.ints([0] * B)
+    free = d.ints(np.concatenate([rng.permutation(d.pages)[:pages], np.full(d.pages - pages, -7)]))
+    fc = d.ints([pages])
+    ours = set(free[:pages].tolist())
+    at, ended, refused, last, checked = np.zeros(B, np.int64), 0, 0, 0, 0
+    for step in range(400):
+        if ended >= 5 and last and refused > 20:
+            break
+        ended += int((at == N).sum())
+        at[at == N] = 0                              # a text is whole: another one begins
+        count = rng.integers(0, n + 1, B)
+        par, true, longest = np.full((B, n), 99), [[] for _ in range(B)], np.zeros(B, np.int64)
+        for b in range(B):
+            p = tree(rng, count[b], "tree")
+            par[b, :count[b]] = p
+            if count[b]:
+                true[b] = line(p, int(rng.integers(0, count[b])))
+                longest[b] = max(len(line(p, t)) for t in range(count[b]))
+        q, k = (torch.rand(B, w.H, n, w.d_K, device="cuda") * 2 - 1 for _ in range(2))
+        v = torch.randn(B, w.H, n, w.d_V, device="cuda").to(d.vdt)
+        for b in range(B):
+            for j, t in enumerate(true[b][:N - at[b]]):
+                for x, y in zip((q, k, v), full):
+                    x[b, :, t] = y[b, :, at[b] + j]
+        start, cnt, parent = d.ints(at), d.ints(count), d.ints(par)
+        leaf = d.ints([x[-1] if x else -1 for x in true])
+        want = torch.minimum(d.ints(longest), C - start % C)
+        out, rs, idx = d.outputs()
+        acc, granted = d.ints([9] * B), d.ints([9] * B)
+        c.reserve(start, want, table, held, free, fc, granted, n=n)
+        c.attend_tree(q, k, v, d.gamma, start, cnt, parent, table, out, rs, idx=idx)
+        c.accept(k, v, start, cnt, parent, leaf, table, acc, granted=granted)
+        c.order(start, acc, table, n=n)
+        assert int(c.status.item()) == 0
+        got, g = acc.cpu().numpy(), granted.cpu().numpy()
+        for b in range(B):
+            line_of = min(len(true[b]), C - at[b] % C)
+            assert g[b] in (0, int(want[b])) and got[b] == (line_of if g[b] else 0)
+            assert held[b] * page >= at[b] + got[b]
+            refused += int(want[b]) > 0 and g[b] == 0
+            last += at[b] == N - 1 and got[b] == 1
+            for j in range(got[b])[:2]:
+                i, t, h = int(at[b]) + j, true[b][j], j % w.H
+                d.parents[b], d.starts[b] = [-1], i
+                d.qn[b, h, 0], d.kn[b, h, 0] = d.g["q"][b, h, i], d.g["k"][b, h, i]
+                d.vn[b, h, 0] = d.values[b][h][i]
+                win, o, s, bo, bs = d.plain(b, 0, h)
+                assert np.array_equal(idx[b, h, t].cpu().numpy(), win if len(win) else [-1] * w.k)
+                assert (np.abs(out[b, h, t].double().cpu().numpy() - o) <= bo).all()
+                assert abs(float(rs[b, h, t]) - s) <= bs
+                checked += 1
+            e = torch.arange(int(at[b] + got[b]), device="cuda")
+            ids = table[b].long()[e // page]
+            for x, y in zip((c.k_pages, c.v_pages), full[1:]):
+                assert torch.equal(x[ids, :, e % page], y[b, :, e].transpose(0, 1))
+        at += got
+        if (count > 0).any() and not got.any():      # nobody moves: the longest one leaves
+            at[at.argmax()] = 0
+        c.reserve(d.ints(at), d.ints([0] * B), table, held, free, fc, granted, n=n)
+        used = sum((table[b, :int(held[b])].tolist() for b in range(B)), [])
+        left = used + free[:int(fc)].tolist()
+        assert len(left) == pages and set(left) == ours
+    assert ended >= 5 and refused > 20 and last and checked > 300, (ended, refused, last)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(v_dtype="f32", d_V=33), dict(d_V=250)])
+def test_granted_ends_the_line(kw):
+    w = _work(B=6, **kw)
+    d = Drafting(w, 16, [40, 40, 40, 40, 60, 0], [20, 20, 20, 20, 20, 0], 20, kind="chain")
+    kp, vp = d.cache.k_pages.clone(), d.cache.v_pages.clone()
+    granted = [3, 0, -5, 2 ** 31 - 1, 2, 7]
+    m = [3, 0, 0, 20, 2, 0]
+    for b in range(6):
+        for j in range(m[b]):
+            i = d.starts[b] + j
+            kp[d.table_np[b][i // 16], :, i % 16] = d.k[b, :, j]
+            vp[d.table_np[b][i // 16], :, i % 16] = d.v[b, :, j]
+    table = d.table.clone()
+    table[1, 2:], table[0, 3:] = -1, -1              # pages that nothing was granted for
+    acc, path = d.ints([9] * 6), d.ints(np.full((6, 20), 9))
+    d.cache.accept(d.k, d.v, d.start, d.count, d.parent, d.ints([19] * 6), table, acc, path,
+                   granted=d.ints(granted))
+    assert int(d.cache.status.item()) == 0 and acc.tolist() == m
+    for b in range(6):
+        assert path[b].tolist() == list(range(m[b])) + [-1] * (20 - m[b])
+    assert torch.equal(kp, d.cache.k_pages) and torch.equal(vp, d.cache.v_pages)
+    # the binding's call, and what it refuses
+    p = zb.problem(w.B, w.H, w.N, w.d_K, w.d_V, w.k, w.C, w.bits, w.v_dtype)
+    cc = zb.zeta_cache_t(20, 16, d.cache.pages, d.cache.order_pages, table.shape[1])
+    acc2 = d.ints([9] * 6)
+    args = (p, cc, d.k, d.v, d.start, d.count, d.parent, d.ints([19] * 6))
+    pools = (table, d.cache.k_pages, d.cache.v_pages)
+    zb.zeta_cache_accept_granted(*args, d.ints(granted), *pools, acc2)
+    assert torch.equal(acc, acc2)
+    for bad in (d.ints(granted).long(), d.ints(granted[:5])):
+        with pytest.raises((TypeError, ValueError)):
+            d.cache.accept(*args[2:], table, acc, granted=bad)
+        with pytest.raises((TypeError, ValueError)):
+            zb.zeta_cache_accept_granted(*args, bad, *pools, acc2)
