@@ -572,7 +572,7 @@ zeta_status_t zeta_cache_accept_granted(const zeta_problem_t *p, const zeta_cach
  * their count, zeta_cache_append, _order and _attend take what has pages; of a draft, whose
  * count is one of nodes, zeta_cache_accept_granted does.
  *   p, cc     B, N, C as everywhere, n, page, pages, table_len of the cache (the heads and
- *             the order pools play no part); n bounds count
+ *             the order pools play no part); n bounds count: 0 where the call only gives back
  *   start, count  int32 [B], 0 <= count <= n, 0 <= start, start + count <= N (of a draft the
  *               tokens of its longest line up to the chunk's end: there is always room for them)
  *   page_table  in/out: int32 [B, table_len]

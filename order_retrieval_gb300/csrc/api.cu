@@ -353,7 +353,12 @@ ZETA_API zeta_status_t zeta_cache_reserve(const zeta_problem_t *p, const zeta_ca
     zeta::Cache c;
     zeta_status_t s = check_cache(p, cc, &pr, &c);
     if (s != ZETA_OK) return s;
-    if (empty(pr) || c.n == 0) return ZETA_OK;
+    // Without rows (or heads) there are pages to give back all the same; only a call without
+    // sequences, or one of that kind that names no arrays, has nothing to do.
+    if (pr.B == 0) return ZETA_OK;
+    const bool none = !start && !count && !page_table && !held && !free_list && !free_count &&
+                      !granted && !slots;
+    if (none && (empty(pr) || c.n == 0)) return ZETA_OK;
     if (c.pages < 1) return ZETA_ERR_INVALID_ARG;
     if (!start || !count || !page_table || !held || !free_list || !free_count || !granted)
         return ZETA_ERR_INVALID_ARG;

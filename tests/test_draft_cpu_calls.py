@@ -38,3 +38,14 @@ def test_accept_granted_checks_as_accept_does(L):
     for p, c in ((_prob(B=0), _cache()), (_prob(H=0), _cache()), (_prob(), _cache(n=0))):
         assert call(ctypes.byref(p), ctypes.byref(c), *[None] * (GRANTED + 2)) == 0
     zb.zeta_cache_accept_granted(_prob(B=0), _cache(), *[None] * 11, stream=0)
+
+
+def test_reserve_without_rows_wants_its_arrays(L):
+    """It has pages to give back; without any array it is the empty call."""
+    for p, c in ((_prob(), _cache(n=0)), (_prob(H=0), _cache())):
+        P, Q = ctypes.byref(p), ctypes.byref(c)
+        assert L.zeta_cache_reserve(P, Q, *[None] * 10) == 0
+        for pos in range(7):
+            a = [ctypes.c_void_p(0x10000 * (i + 1)) for i in range(7)] + [None] * 3
+            a[pos] = None
+            assert L.zeta_cache_reserve(P, Q, *a) == 1, pos

@@ -1,13 +1,15 @@
 """GPU tests of drafting when pages run out and at the end of a text: the step as it is documented
-(reserve the longest line up to the chunk's end, attend the whole tree, accept what was granted)."""
+(reserve the longest line up to the chunk's end, attend the whole tree, accept what was granted); calls
+that only give pages back."""
 import numpy as np
 import pytest
 import torch
 
+from order_retrieval_gb300 import ZetaCache
 from order_retrieval_gb300 import binding as zb
 from order_retrieval_gb300 import workloads as W
 
-from draft_util import Drafting, line, tree
+from draft_util import Drafting, line, reserve_plain, tree
 
 pytestmark = [
     pytest.mark.gpu,
@@ -133,3 +135,30 @@ def test_granted_ends_the_line(kw):
             d.cache.accept(*args[2:], table, acc, granted=bad)
         with pytest.raises((TypeError, ValueError)):
             zb.zeta_cache_accept_granted(*args, bad, *pools, acc2)
+
+
+@pytest.mark.parametrize("how", ["n", "slots", "heads", "binding"])
+def test_reserve_without_rows_gives_back(how):
+    """Requests that end or were cut short, and no row of a new token in the call."""
+    B, page, pages, N = 9, 8, 80, 128
+    up, rng = Drafting.ints, np.random.default_rng(3)
+    cache = ZetaCache.empty(pages, page, 1, 1, 8, N, 32, 1, 8, order_pages=1)
+    table, held = np.full((B, N // page), -1), np.zeros(B, np.int64)
+    free, F = rng.permutation(pages), pages
+    _, _, F = reserve_plain(table, held, free, F, 10 * np.arange(B), [10] * B, 10, page, pages, N)
+    start = np.array([0, 3, 30, 0, 41, 8, 70, 16, 0])
+    x = [up(table), up(held), up(free), up([F])]
+    want, _, F2 = reserve_plain(table, held, free, F, start, [0] * B, 0, page, pages, N)
+    assert F2 > F
+    got, none = up([9] * B), up([0] * B)
+    if how == "n":
+        cache.reserve(up(start), none, *x, got, n=0)
+    elif how == "slots":
+        cache.reserve(up(start), none, *x, got, up(np.zeros((B, 0))))
+    else:
+        p = zb.problem(B, 0 if how == "heads" else 1, N, 1, 8, 1, 32, 8, "bf16")
+        cc = zb.zeta_cache_t(4 if how == "heads" else 0, page, pages, 1, N // page)
+        zb.zeta_cache_reserve(p, cc, up(start), none, *x, got)
+    assert int(cache.status.item()) == 0 and got.tolist() == want.tolist()
+    for a, b in zip(x, (table, held, free, [F2])):
+        assert np.array_equal(a.cpu().numpy(), b)
