@@ -482,6 +482,8 @@ zeta_status_t zeta_cache_attend(const zeta_problem_t *p, const zeta_cache_t *cc,
  *   start, count  as for the cache calls, but 0 <= start <= N and, where count > 0,
  *            start < N: only the line's tokens need room.
  * Limit: n <= 1024.
+ * No output of these calls may share memory with an input or another output, the pools aside
+ * (ZETA_ERR_INVALID_ARG); zeta_cache_reserve's granted may be the array given as count.
  */
 
 /*
@@ -497,7 +499,7 @@ zeta_status_t zeta_cache_attend(const zeta_problem_t *p, const zeta_cache_t *cc,
  *   v         in : v_dtype [B, H, n, d_V]  (16-B aligned)
  *   gamma     in : float [H]
  *   k_pages, v_pages, order_codes, order_idx  in : the cache before this step
- *   out       out: v_dtype [B, H, n, d_V]  (16-B aligned; not the memory of v)
+ *   out       out: v_dtype [B, H, n, d_V]  (16-B aligned)
  *   rowsum    out: float [B, H, n]
  *   idx       out: int32 [B, H, n, k], the window's tokens (-1 in chunk 0), or null
  *   dev_status  optional int32 device word; an order entry outside [0, cC) or a page
@@ -524,9 +526,8 @@ zeta_status_t zeta_cache_attend_tree(const zeta_problem_t *p, const zeta_cache_t
  *   k, v      in : the tensors given to zeta_cache_attend_tree (v 16-B aligned)
  *   leaf      in : int32 [B], -1: nothing is accepted; not looked at where count is 0
  *   k_pages, v_pages  in/out (written at the accepted tokens' rows only)
- *   accepted  out: int32 [B], tokens accepted: the count for zeta_cache_order (not the
- *             memory of start, count or leaf, nor path that of parent).  Every token of the
- *             line counts, one without a page too: where pages may be missing call
+ *   accepted  out: int32 [B], tokens accepted: the count for zeta_cache_order.  Every token
+ *             of the line counts, one without a page too: where pages may be missing call
  *             zeta_cache_accept_granted
  *   path      out: int32 [B, n], node of the j-th accepted token, -1 from accepted[b] on;
  *             or null
@@ -589,8 +590,7 @@ zeta_status_t zeta_cache_accept_granted(const zeta_problem_t *p, const zeta_cach
  * The result depends on the order of the sequences alone, and a call that takes pages is
  * undone by one that gives them back.  Calls on one list follow one another on a stream.
  * A page is in one table or in the list: a table whose entries below held were filled in
- * otherwise (shared prompts) gives them back as if they were its own.  granted may be the
- * array given as count, but not start or held.
+ * otherwise (shared prompts) gives them back as if they were its own.
  * Errors: ZETA_ERR_INVALID_ARG, ZETA_ERR_UNSUPPORTED.
  */
 zeta_status_t zeta_cache_reserve(const zeta_problem_t *p, const zeta_cache_t *cc,

@@ -3,6 +3,7 @@
 // Every check runs on the host before any CUDA call, so an invalid request
 // returns a status without touching the device (and works without a GPU).
 #include <climits>
+#include <initializer_list>
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -74,6 +75,27 @@ bool empty(const Prob &p) { return p.S == 0 || p.N == 0; }
 zeta_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? ZETA_OK : ZETA_ERR_CUDA; }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// An array of a call; null: not given.
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+
+// No output lies in an input, which other blocks may still read, or in another output.
+bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    auto meet = [](const Span &a, const Span &b) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+        return a.p && b.p && x < y + (uint64_t)b.bytes && y < x + (uint64_t)a.bytes;
+    };
+    for (const Span *o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span &i : ins)
+            if (meet(*o, i)) return false;
+        for (const Span *other = outs.begin(); other != o; ++other)
+            if (meet(*o, *other)) return false;
+    }
+    return true;
+}
 
 }  // namespace
 
@@ -362,8 +384,11 @@ ZETA_API zeta_status_t zeta_cache_reserve(const zeta_problem_t *p, const zeta_ca
     if (c.pages < 1) return ZETA_ERR_INVALID_ARG;
     if (!start || !count || !page_table || !held || !free_list || !free_count || !granted)
         return ZETA_ERR_INVALID_ARG;
-    if (granted == start || granted == held || held == start || held == count)
-        return ZETA_ERR_INVALID_ARG;                 // written while other blocks read them
+    const int64_t per = 4 * (int64_t)pr.B;
+    if (!apart({{page_table, per * c.tlen}, {held, per}, {free_list, 4 * (int64_t)c.pages},
+                {free_count, 4}, {slots, per * c.n}, {granted, per}},
+               {{start, per}, {granted == count ? nullptr : count, per}}))
+        return ZETA_ERR_INVALID_ARG;
     c.start = start;
     c.count = count;
     return from_cuda(zeta::launch_cache_reserve(pr, c, page_table, held, free_list, free_count,
@@ -388,7 +413,13 @@ ZETA_API zeta_status_t zeta_cache_attend_tree(
         !v_pages || !order_table || !order_codes || !order_idx || !out || !rowsum)
         return ZETA_ERR_INVALID_ARG;
     if (!aligned16(v) || !aligned16(v_pages) || !aligned16(out)) return ZETA_ERR_INVALID_ARG;
-    if (out == v) return ZETA_ERR_INVALID_ARG;       // written while other nodes read it
+    const int64_t rows = pr.S * c.n, vrow = (int64_t)pr.dV * (pr.vdt == ZETA_BF16 ? 2 : 4);
+    const int64_t per = 4 * (int64_t)pr.B;
+    if (!apart({{out, rows * vrow}, {rowsum, 4 * rows}, {idx, 4 * rows * pr.k}},
+               {{q, 4 * rows * pr.dK}, {k, 4 * rows * pr.dK}, {v, rows * vrow},
+                {gamma, 4 * (int64_t)pr.H}, {start, per}, {count, per}, {parent, per * c.n},
+                {page_table, per * c.tlen}, {order_table, per * c.tlen}}))
+        return ZETA_ERR_INVALID_ARG;
     c.start = start;
     c.count = count;
     c.ptab = page_table;
@@ -416,9 +447,12 @@ zeta_status_t accept(const zeta_problem_t *p, const zeta_cache_t *cc, const floa
     if (!k || !v || !start || !count || !parent || !leaf || !page_table || !k_pages || !v_pages ||
         !accepted || (limited && !granted))
         return ZETA_ERR_INVALID_ARG;
-    if (accepted == start || accepted == count || accepted == leaf || path == parent ||
-        (granted && (accepted == granted || path == granted)))
-        return ZETA_ERR_INVALID_ARG;                 // written while other heads read them
+    const int64_t rows = pr.S * c.n, vrow = (int64_t)pr.dV * (pr.vdt == ZETA_BF16 ? 2 : 4);
+    const int64_t per = 4 * (int64_t)pr.B;
+    if (!apart({{accepted, per}, {path, per * c.n}},
+               {{k, 4 * rows * pr.dK}, {v, rows * vrow}, {start, per}, {count, per},
+                {parent, per * c.n}, {leaf, per}, {granted, per}, {page_table, per * c.tlen}}))
+        return ZETA_ERR_INVALID_ARG;
     if (!aligned16(v) || !aligned16(v_pages)) return ZETA_ERR_INVALID_ARG;
     c.start = start;
     c.count = count;

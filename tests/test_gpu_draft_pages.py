@@ -162,3 +162,44 @@ def test_reserve_without_rows_gives_back(how):
     assert int(cache.status.item()) == 0 and got.tolist() == want.tolist()
     for a, b in zip(x, (table, held, free, [F2])):
         assert np.array_equal(a.cpu().numpy(), b)
+
+
+@pytest.mark.parametrize("v_dtype", ["bf16", "f32"])
+def test_arrays_side_by_side(v_dtype):
+    """All arrays of one node a sequence, end to end in one buffer: none meets another."""
+    w = _work(B=6, H=1, k=1, d_K=1, d_V=8, v_dtype=v_dtype)
+    d = Drafting(w, 16, [40, 33, 0, 100, 127, 64], [1] * 6, 1)
+    want = [x.clone() for x in d.attend()]
+    buf = torch.zeros(4096, dtype=torch.int32, device="cuda")
+    at = 0
+
+    def put(x):
+        """The tensor's copy behind the last one (values on 16 bytes)."""
+        nonlocal at
+        words = x.numel() * x.element_size() // 4
+        at = -(-at // 4) * 4 if x.dim() == 4 and x.shape[-1] == 8 else at
+        y = buf[at:at + words].view(x.dtype).view(x.shape)
+        at += words
+        y.copy_(x)
+        return y
+
+    out, rs, idx = d.outputs()
+    v, out = put(d.v), put(out)
+    q, k, rs, idx = put(d.q), put(d.k), put(rs), put(idx)
+    start, count, parent, table, gamma = (put(x) for x in (d.start, d.count, d.parent, d.table,
+                                                           d.gamma))
+    d.cache.attend_tree(q, k, v, gamma, start, count, parent, table, out, rs, idx=idx)
+    for a, b in zip((out, rs, idx), want):
+        assert torch.equal(a, b)
+    leaf, acc, granted, path = (put(d.ints(x)) for x in ([0] * 6, [9] * 6, [1] * 6, [[9]] * 6))
+    d.cache.accept(k, v, start, count, parent, leaf, table, acc, path, granted=granted)
+    assert acc.tolist() == [1] * 6 and path.tolist() == [[0]] * 6
+    tab, held = put(d.ints(np.full((6, w.N // 16), -1))), put(d.ints([0] * 6))
+    free, fc = put(d.ints(np.arange(d.pages))), put(d.ints([d.pages]))
+    got, slots = put(d.ints([0] * 6)), put(d.ints([[0]] * 6))
+    d.cache.reserve(start, count, tab, held, free, fc, got, slots)
+    assert int(d.cache.status.item()) == 0 and got.tolist() == [1] * 6 and at < 4096
+    want = [-(-(s + 1) // 16) for s in d.starts]
+    assert held.tolist() == want and fc.tolist() == [d.pages - sum(want)]
+    for b, s in enumerate(d.starts):
+        assert slots[b, 0] == int(tab[b, s // 16]) * 16 + s % 16
