@@ -26,8 +26,8 @@ def _name(kw):
     return "-".join(f"{a}{b}" for a, b in kw.items()) or "base"
 
 
-# Slices: 2 (clusters of 8), 24 and 60 (clusters of 4 and 2), 160 and 400 (single blocks; one
-# group of nodes up to 8 of them, two above).
+# Slices: 2, 24, 60, 160 and 400; with chunks of 256 a tree has one block or two (wider clusters:
+# below and in test_gpu_draft_layouts.py).
 @pytest.mark.parametrize("weight", ["cauchy", "softmax", "inv_euclid"])
 @pytest.mark.parametrize("kw", [dict(), dict(v_dtype="f32"), dict(d_V=128), dict(d_V=72, k=70),
                                 dict(v_dtype="f32", d_V=100), dict(d_K=2, bits=21, d_V=40)],
