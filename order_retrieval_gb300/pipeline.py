@@ -413,8 +413,10 @@ class ZetaCache:
         or C).  start[b] + count[b] <= N: of a draft, the tokens of its longest line up to the
         chunk's end (``accept`` takes granted)."""
         tp, B, width = self._table(page_table)
+        if slots is not None and slots.dim() != 2:
+            raise ValueError(f"slots: {slots.dim()} dimensions, expected 2")
         if n is None:
-            n = self.C if slots is None else slots.shape[-1]
+            n = self.C if slots is None else slots.shape[1]
         p, c, per_seq, *_ = self._sizes(B, n, width)
         take = self._take
         st = self._memory()[4]

@@ -203,3 +203,14 @@ def test_arrays_side_by_side(v_dtype):
     assert held.tolist() == want and fc.tolist() == [d.pages - sum(want)]
     for b, s in enumerate(d.starts):
         assert slots[b, 0] == int(tab[b, s // 16]) * 16 + s % 16
+
+
+def test_row_numbers_of_other_dimensions():
+    """Refused as every other wrong shape is."""
+    up, cache = Drafting.ints, ZetaCache.empty(10, 8, 1, 1, 8, 64, 32, 1, 8, order_pages=1)
+    x = [up(np.full((1, 8), -1)), up([0]), up(np.arange(10)), up([10])]
+    for slots in (up(7), up([7]), up([[[7]]])):
+        for n in (None, 1):
+            with pytest.raises(ValueError):
+                cache.reserve(up([0]), up([1]), *x, up([0]), slots, n=n)
+    assert x[3].tolist() == [10]
