@@ -8,8 +8,8 @@
 // value where the row is no multiple of 16 bytes), four rows a thread under way; the row's
 // first threads also carry its coordinates.
 //
-// 64 sequences, lines of a few nodes, 8 heads: 3.2 us, a launch and four dependent loads.  48
-// lines of 64 to 128 nodes, 4 heads, rows of 132 bytes a value a thread: 6.8 us for 4 MB (one
+// 64 sequences, lines of a few nodes, 8 heads: 3.3 us, a launch and four dependent loads.  48
+// lines of 64 to 128 nodes, 4 heads, rows of 132 bytes a value a thread: 6.9 us for 4 MB (one
 // row a thread at a time, the line climbed node by node: 14.7).
 #include "cache_tree.cuh"
 

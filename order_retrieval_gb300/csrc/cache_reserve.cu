@@ -17,9 +17,9 @@
 //
 // 512 requests with a token each: 6 us, of which launch, three dependent loads and the two
 // barriers are most; 256 requests of which half end or begin, up to 31 K pages moved, 262 K row numbers:
-// 12.5 us for 0.8 MB (a page at a time a lane, and a 64-bit division a row number: 26).  Eight
-// SMs write what there is to write; more blocks would need a second launch or a workspace for
-// the sums.
+// 12 us for 0.8 MB (a page at a time a lane, and a 64-bit division a row number: 26).  Eight
+// SMs write what there is to write.  A cluster of 16 (which a kernel has to ask for) and row numbers
+// of sequences that move no pages, written before the barriers, were not tried.
 #include <cooperative_groups.h>
 
 #include "cache_tree.cuh"

@@ -29,11 +29,14 @@
 // 59 sequences with trees of 25 nodes on average, 8 heads, 10 K tokens before each and 508 of
 // them in its chunk of 1024, windows of 48, d_V 64: 55 us for 120 MB, 2.2 TB/s (32 % of the
 // measured HBM rate; DRAM reads 156 MB: every search reads the fences' and its block's sectors).
-// What bounds it is the warps' own way: 20.7 M instructions (half of them in windows: about 800
-// for a search, its lookups, weights and sums; 147 for 16 shared keys and 16 nodes) at 32 % of the
+// What bounds it is the warps' own way: 21.3 M instructions (half of them in windows: about 800
+// for a search, its lookups, weights and sums; about 160 for 16 shared keys and 16 nodes) at 31 % of the
 // issue slots, with 16 warps an SM that wait for DRAM in turn and for results of their own
-// instructions; a fifth of the time SMs run empty at the end.  (At 57 us for this, texts of
-// up to 2 K tokens, all in L2, took 43.)  Tried on the way: value rows by cp.async through rings in shared memory, half the
+// instructions; a fifth of the time SMs run empty at the end.  Other d_K than 3 and chunks that begin
+// off a multiple of 16 (C = 1000: every other one) have no whole steps: the same trees take 63 to
+// 66 us with d_K 1, 2 or 4, 58 with C 1000.  Softmax 64 us, d_V 128 81, float32 77.
+// Tried on the way, with weights in two parts (52 us at the end of it, 57 on texts of over 2 K tokens
+// where those that lie in L2 took 43): value rows by cp.async through rings in shared memory, half the
 // warps on windows and half on shared keys 86; operands put together by byte permutes, a load
 // touching 32 rows' lines instead of 8, 59; windows of two nodes at once 66; three blocks an SM with
 // 80 registers 64 to 72 (spills); 8 nodes and 4 warps a block 60; two steps of shared keys at
@@ -64,7 +67,7 @@ struct TreeSmem {
     static constexpr bool MMA = sizeof(V) == 2;
     // NG groups of 8 nodes a block; warps, blocks an SM (128 registers a thread), a window's steps
     // under way (64 sequences, 16 nodes a block: 2, 3, 4 of them 54, 52, 56 us; lines of 200, 128
-    // wide, 8 nodes: 2, 3 of them 48.6, 51.7).
+    // wide, 8 nodes: 2, 3 of them 48.6, 51.7; weights in two parts).
     static constexpr int ROWS = 8 * NG, NW = 4 * NG, PER_SM = 4 / NG, NB = NG + 1;
     static constexpr int KS = MMA ? 16 : 8, KL = KS / 4, KP = KL / 2;    // shared keys a step, a lane; pairs
     static constexpr int NV = DVP / 16;              // 16-byte pieces of them a lane holds (float32: of four keys)
