@@ -20,7 +20,8 @@
 //    a load touches 8 lines of L1; movmatrix turns the 8 x 8 blocks into A operands (values
 //    times keys).  B (keys times columns) has 8 nodes' weights, a window's in columns 0 to 2.
 //    A weight enters as three bf16 parts, each the nearest to what those before it leave: 3 x 8
-//    bits hold all 24 of it, so that sums are those of float32 weights.  (Two parts, within 2^-16,
+//    bits hold all 24 of it (below 2^-110, where the last ones are no longer bf16 numbers, all
+//    but 2^-133), so that sums are those of float32 weights.  (Two parts, within 2^-16,
 //    let one output in a thousand round to the other neighbour; the third costs 2.9 of the 55 us
 //    below.)
 //  * A weight of zero times a value that is not finite is NaN: a node whose result is not

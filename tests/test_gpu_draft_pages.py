@@ -214,3 +214,54 @@ def test_row_numbers_of_other_dimensions():
             with pytest.raises(ValueError):
                 cache.reserve(up([0]), up([1]), *x, up([0]), slots, n=n)
     assert x[3].tolist() == [10]
+
+
+def test_a_captured_step_under_a_short_list():
+    """reserve, attend_tree, accept and order captured once; replayed with lists of other lengths they
+    give what eager calls do."""
+    w = _work(B=6, H=2)
+    starts, n = [46, 33, 95, 110, 127, 64], 7        # pages for the first, fourth and last
+    d = Drafting(w, 16, starts, [n] * 6, n, kind="chain")
+    c, leaf = d.cache, d.ints([6, 3, 5, 6, 6, 2])
+    longest = torch.minimum(d.count, w.C - d.start % w.C)
+    spare = d.ints(np.arange(d.pages))
+    pools = (c.k_pages, c.v_pages, c.order_codes, c.order_idx)
+    kept = [x.clone() for x in pools]
+    state = [d.table.clone(), d.ints([-(-s // 16) for s in starts]), spare, d.ints([0])]
+    state[0][:, w.N // 16:] = -1
+    for b, s in enumerate(starts):                   # pages of the text alone; the others are free
+        state[0][b, -(-s // 16):] = -1
+    used = {int(x) for x in state[0].flatten() if x >= 0}
+    rest = [x for x in range(d.pages) if x not in used]
+    state[2][:len(rest)] = d.ints(rest)
+    outs = [*d.outputs(), d.ints([9] * 6), d.ints([9] * 6), d.ints(np.full((6, n), 9))]
+    work = [x.clone() for x in state + outs]
+
+    def reset(places):
+        for a, b in zip([*work, *pools], [*state, *outs, *kept]):
+            a.copy_(b)
+        work[3].fill_(places)
+
+    def step():
+        table, held, free, fc, out, rs, idx, acc, granted, path = work
+        c.reserve(d.start, longest, table, held, free, fc, granted, n=n)
+        c.attend_tree(d.q, d.k, d.v, d.gamma, d.start, d.count, d.parent, table, out, rs, idx=idx)
+        c.accept(d.k, d.v, d.start, d.count, d.parent, leaf, table, acc, path, granted=granted)
+        c.order(d.start, acc, table, n=n)
+
+    want = {}
+    for places in (0, 1, 2, len(rest)):
+        reset(places)
+        step()
+        want[places] = [x.clone() for x in [*work, *pools]]
+    assert len({tuple(x[7].tolist()) for x in want.values()}) == 4
+    reset(0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for places in (2, 0, len(rest), 1):
+        reset(places)
+        graph.replay()
+        for a, b in zip([*work, *pools], want[places]):
+            assert torch.equal(a, b), places
+    assert int(c.status.item()) == 0
